@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "kargs.h"
+#include "ops.h"
 #include "plan.h"
 #include "purlin_gb.h"
 
@@ -304,7 +305,7 @@ purlin_status get_plan(purlin_ctx* h, int coll, int world, int dtype, const uint
 // address the driver does not know -- even where the device could reach
 // pageable memory, an unknown address may not be a mapping at all, and the
 // kernel would fault on it.
-purlin_status locate(const purlin_ctx* h, const void* p, const void** dev_p, bool* host) {
+purlin_status locate(int device, const void* p, const void** dev_p, bool* host) {
   *dev_p = p;
   if (!p) return PL_OK;  // a zero-byte rank of a V collective
   cudaPointerAttributes at;
@@ -315,7 +316,7 @@ purlin_status locate(const purlin_ctx* h, const void* p, const void** dev_p, boo
   }
   switch (at.type) {
     case cudaMemoryTypeDevice:
-      return at.device == h->device ? PL_OK : PL_ERR_INVALID_ARG;
+      return at.device == device ? PL_OK : PL_ERR_INVALID_ARG;
     case cudaMemoryTypeManaged:
       return PL_OK;
     case cudaMemoryTypeHost:
@@ -340,10 +341,10 @@ purlin_status run(purlin_ctx* h, int coll, int world, int dtype, const uint64_t*
   bool host_mem = false;
   purlin_status st;
   for (int r = 0; r < nin; ++r)
-    if ((st = locate(h, in_arg[r], &in[r], &host_mem))) return st;
+    if ((st = locate(h->device, in_arg[r], &in[r], &host_mem))) return st;
   for (int r = 0; r < nout; ++r) {
     const void* q = nullptr;
-    if ((st = locate(h, out_arg[r], &q, &host_mem))) return st;
+    if ((st = locate(h->device, out_arg[r], &q, &host_mem))) return st;
     out[r] = const_cast<void*>(q);
   }
   uint8_t sres[pl::kMaxWorld] = {}, dres[pl::kMaxWorld] = {};
@@ -466,6 +467,26 @@ std::vector<Range> ranges(const void* const* p, int n, const std::vector<uint64_
 }
 
 }  // namespace
+
+namespace pl {
+
+purlin_status op_begin(purlin_handle h, OpHandle* out) {
+  if (purlin_status st = check_handle(h)) return st;
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return cuda_fail(cudaErrorInvalidDevice);
+  if (cur != h->device) return PL_ERR_INVALID_ARG;
+  out->device = h->device;
+  out->sm_count = h->sm_count;
+  out->status = h->ctl + kCtlStatus;
+  return PL_OK;
+}
+
+purlin_status op_locate(const OpHandle& h, const void* p, const void** dev_p) {
+  bool host = false;
+  return locate(h.device, p, dev_p, &host);
+}
+
+}  // namespace pl
 
 extern "C" {
 

@@ -45,6 +45,8 @@ PATH_REGISTER, PATH_BULK = 1, 2
 PL_SCHED_ITEM, PL_SCHED_STREAM, PL_SCHED_QUEUE, PL_SCHED_QUEUE_GUIDED = 1, 2, 3, 4
 
 MAX_WORLD = 16
+MAX_EXPERTS, MAX_TOP_K, MAX_GROUPS = 1024, 32, 32
+PL_SCORES_SOFTMAX, PL_SCORES_SIGMOID = 0, 1
 
 
 class PurlinError(RuntimeError):
@@ -64,6 +66,11 @@ class purlin_item(ctypes.Structure):
     _fields_ = [("src_off", ctypes.c_uint64), ("dst_off", ctypes.c_uint64), ("len", ctypes.c_uint64),
                 ("src_mask", ctypes.c_uint32), ("dst_mask", ctypes.c_uint32), ("wait", ctypes.c_uint32),
                 ("notify", ctypes.c_uint32), ("cta", ctypes.c_uint32), ("order", ctypes.c_uint32)]
+
+
+class purlin_routing(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("experts", "top_k", "scores", "groups", "kept_groups", "group_best",
+                                            "renormalise")] + [("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -105,6 +112,20 @@ _SIGNATURES = {
                                   ctypes.POINTER(ctypes.c_uint64), _i, ctypes.POINTER(purlin_tune),
                                   ctypes.POINTER(purlin_item), _sz, _SZP, ctypes.POINTER(_i),
                                   ctypes.POINTER(_i)]),
+    "purlin_route_experts": (_i, [_vp, _vp, _sz, _i, _vp, _sz, ctypes.POINTER(purlin_routing), _vp, _vp, _vp]),
+    "purlin_route_experts_grad": (_i, [_vp, _vp, _sz, _i, _sz, ctypes.POINTER(purlin_routing), _vp, _vp, _vp, _sz,
+                                       _vp]),
+    "purlin_expert_plan_bytes": (_sz, [_sz, _i, _i]),
+    "purlin_expert_plan": (_i, [_vp, _vp, _sz, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "purlin_dispatch_rows": (_i, [_vp, _vp, _sz, _vp, _sz, _i, _sz, _i, _vp, _sz, _vp]),
+    "purlin_combine_rows": (_i, [_vp, _vp, _sz, _vp, _vp, _sz, _i, _sz, _i, _vp, _sz, _vp]),
+    "purlin_combine_rows_grad": (_i, [_vp, _vp, _sz, _vp, _vp, _vp, _sz, _sz, _i, _sz, _i, _vp, _sz, _vp, _vp]),
+    "purlin_embed": (_i, [_vp, _vp, _sz, _sz, ctypes.c_int64, _vp, _i, _sz, _sz, ctypes.c_float, _i, _vp, _sz, _vp]),
+    "purlin_embed_grad_bytes": (_sz, [_sz, _sz, _sz]),
+    "purlin_embed_grad": (_i, [_vp, _vp, _sz, _i, _vp, _i, _sz, _sz, ctypes.c_float, _vp, _sz, _vp, _sz, _i, _sz,
+                               ctypes.c_int64, _vp, _sz, _vp]),
+    "purlin_clip_grad_norm_bytes": (_sz, []),
+    "purlin_clip_grad_norm": (_i, [_vp, _PP, _PP, _SZP, _sz, _i, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -259,6 +280,80 @@ def purlin_all_reduce_noalloc(world, src, dst, bytes_per_rank, dtype, device_sta
     """Allocation-free AllReduce (no handle); device_status: device int pointer or None."""
     return load().purlin_all_reduce_noalloc(world, _ptr_array(src), _ptr_array(dst), bytes_per_rank, dtype,
                                             _addr(device_status) or None, _stream(stream))
+
+
+def make_routing(experts, top_k, scores=PL_SCORES_SOFTMAX, groups=1, kept_groups=1, group_best=1, renormalise=True,
+                 scale=1.0) -> purlin_routing:
+    return purlin_routing(experts, top_k, int(scores), groups, kept_groups, group_best, int(renormalise), scale)
+
+
+def purlin_route_experts(h, logits, stride, dtype, bias, tokens, routing, ids, weights, stream=None) -> int:
+    return load().purlin_route_experts(h, _addr(logits), stride, dtype, _addr(bias), tokens, ctypes.byref(routing),
+                                       _addr(ids), _addr(weights), _stream(stream))
+
+
+def purlin_route_experts_grad(h, logits, stride, dtype, tokens, routing, ids, grad_weights, grad_logits, grad_stride,
+                              stream=None) -> int:
+    return load().purlin_route_experts_grad(h, _addr(logits), stride, dtype, tokens, ctypes.byref(routing), _addr(ids),
+                                            _addr(grad_weights), _addr(grad_logits), grad_stride, _stream(stream))
+
+
+def purlin_expert_plan_bytes(tokens, top_k, experts) -> int:
+    return load().purlin_expert_plan_bytes(tokens, top_k, experts)
+
+
+def purlin_expert_plan(h, ids, tokens, top_k, experts, offsets, places, workspace=None, workspace_bytes=0,
+                       stream=None) -> int:
+    return load().purlin_expert_plan(h, _addr(ids), tokens, top_k, experts, _addr(offsets), _addr(places),
+                                     _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def purlin_dispatch_rows(h, x, x_stride, places, tokens, top_k, width, dtype, rows, rows_stride, stream=None) -> int:
+    return load().purlin_dispatch_rows(h, _addr(x), x_stride, _addr(places), tokens, top_k, width, dtype, _addr(rows),
+                                       rows_stride, _stream(stream))
+
+
+def purlin_combine_rows(h, rows, rows_stride, places, weights, tokens, top_k, width, dtype, y, y_stride,
+                        stream=None) -> int:
+    return load().purlin_combine_rows(h, _addr(rows), rows_stride, _addr(places), _addr(weights), tokens, top_k, width,
+                                      dtype, _addr(y), y_stride, _stream(stream))
+
+
+def purlin_combine_rows_grad(h, rows, rows_stride, places, weights, grad_y, grad_y_stride, tokens, top_k, width, dtype,
+                             grad_rows, grad_rows_stride, grad_weights, stream=None) -> int:
+    return load().purlin_combine_rows_grad(h, _addr(rows), rows_stride, _addr(places), _addr(weights), _addr(grad_y),
+                                           grad_y_stride, tokens, top_k, width, dtype, _addr(grad_rows),
+                                           grad_rows_stride, _addr(grad_weights), _stream(stream))
+
+
+def purlin_embed(h, table, table_stride, rows, first, tokens, token_bytes, n, width, scale, dtype, out, out_stride,
+                 stream=None) -> int:
+    return load().purlin_embed(h, _addr(table), table_stride, rows, first, _addr(tokens), token_bytes, n, width, scale,
+                               dtype, _addr(out), out_stride, _stream(stream))
+
+
+def purlin_embed_grad_bytes(tokens, rows, width) -> int:
+    return load().purlin_embed_grad_bytes(tokens, rows, width)
+
+
+def purlin_embed_grad(h, grad_out, grad_out_stride, grad_out_dtype, tokens, token_bytes, n, width, scale, base,
+                      base_stride, grad_table, grad_table_stride, grad_table_dtype, rows, first, workspace,
+                      workspace_bytes, stream=None) -> int:
+    return load().purlin_embed_grad(h, _addr(grad_out), grad_out_stride, grad_out_dtype, _addr(tokens), token_bytes, n,
+                                    width, scale, _addr(base), base_stride, _addr(grad_table), grad_table_stride,
+                                    grad_table_dtype, rows, first, _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def purlin_clip_grad_norm_bytes() -> int:
+    return load().purlin_clip_grad_norm_bytes()
+
+
+def purlin_clip_grad_norm(h, grads, outs, counts, dtype, scale, max_norm, norm, workspace, workspace_bytes,
+                          stream=None) -> int:
+    """outs: one buffer per gradient, or None for the norm alone."""
+    return load().purlin_clip_grad_norm(h, _ptr_array(grads), None if outs is None else _ptr_array(outs),
+                                        _size_array(counts), len(grads), dtype, scale, max_norm, _addr(norm),
+                                        _addr(workspace), workspace_bytes, _stream(stream))
 
 
 def purlin_status_get(h, stream=None):

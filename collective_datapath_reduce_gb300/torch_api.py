@@ -22,6 +22,11 @@ class ReductionMode(enum.IntEnum):
     DETERMINISTIC = P.PL_DETERMINISTIC
 
 
+class Scores(enum.IntEnum):
+    SOFTMAX = P.PL_SCORES_SOFTMAX
+    SIGMOID = P.PL_SCORES_SIGMOID
+
+
 _DTYPES = {torch.float32: P.PL_F32, torch.bfloat16: P.PL_BF16}
 
 
@@ -186,3 +191,242 @@ def reduce_scatter_v(xs, outs, counts, handle: Handle, stream=None, reduction_mo
     with _on(handle):
         _check(P.purlin_reduce_scatter_v(handle.raw, xs, outs, [int(c) * es for c in counts], dt, int(reduction_mode),
                                          _stream(stream, handle.device)), "reduce_scatter_v")
+
+
+# --------------------------------------- operators around the collectives
+#
+# Outputs are the caller's, as for the collectives.  Matrices are 2-D tensors
+# whose rows are packed (the last stride is 1) and any stride apart; vectors,
+# picks and places are contiguous.  Workspaces come from torch's allocator, on
+# the stream that the call runs on.
+
+def _values(t, what):
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{what}: float32 or bfloat16 tensors")
+    return dt
+
+
+def _matrix(t, rows, width, dtype, what, name):
+    """Checks a rows x width matrix and returns its row stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{what}: {name} must be {rows} x {width}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: {name} must have dtype {dtype}")
+    stride = t.stride(0) if rows > 1 else width
+    if (width > 1 and t.stride(1) != 1) or stride < width:
+        raise ValueError(f"{what}: {name} must have packed rows")
+    if not (t.is_cuda or t.is_pinned()):
+        raise ValueError(f"{what}: tensors must be CUDA tensors or pinned host tensors")
+    return stride
+
+
+def _packed(t, shape, dtype, what, name):
+    if t.shape != shape:
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: {name} must have dtype {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous")
+    if not (t.is_cuda or t.is_pinned()):
+        raise ValueError(f"{what}: tensors must be CUDA tensors or pinned host tensors")
+
+
+def _two(t, what, name):
+    if t.dim() != 2:
+        raise ValueError(f"{what}: {name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _workspace(nbytes, stream, device):
+    """nbytes of device memory that later work on the call's stream may reuse
+    (torch's allocator hands a block on only in the order of its own stream)."""
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def route_experts(logits, ids, weights, handle: Handle, bias=None, scores=Scores.SOFTMAX, groups=1, kept_groups=1,
+                  group_best=1, renormalise=True, scale=1.0, stream=None):
+    """ids[t, j], weights[t, j] = token t's j-th best expert and its weight.
+
+    logits: tokens x experts (float32 or bfloat16); ids int32 and weights
+    float32, tokens x top_k.  bias (float32, one per expert) orders the experts
+    but is not part of the weights.  With groups > 1 only the kept_groups best
+    runs of experts take part, each counted by its group_best (1 or 2) best
+    experts.  Experts with logit -inf are never picked: missing picks have id
+    -1 and weight 0."""
+    what = "route_experts"
+    T, E = _two(logits, what, "logits")
+    k = _two(ids, what, "ids")[1]
+    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    dt = _values(logits, what)
+    _packed(ids, (T, k), torch.int32, what, "ids")
+    _packed(weights, (T, k), torch.float32, what, "weights")
+    if bias is not None:
+        _packed(bias, (E,), torch.float32, what, "bias")
+    with _on(handle):
+        _check(P.purlin_route_experts(handle.raw, logits, ld, dt, bias, T,
+                                      P.make_routing(E, k, scores, groups, kept_groups, group_best, renormalise, scale),
+                                      ids, weights, _stream(stream, handle.device)), what)
+
+
+def route_experts_grad(logits, ids, grad_weights, grad_logits, handle: Handle, scores=Scores.SOFTMAX, renormalise=True,
+                       scale=1.0, stream=None):
+    """grad_logits (like logits) = the gradient that grad_weights (like the
+    weights) gives, the picks held fixed.  Groups and bias only choose the
+    picks, so the gradient does not ask for them."""
+    what = "route_experts_grad"
+    T, E = _two(logits, what, "logits")
+    k = _two(ids, what, "ids")[1]
+    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    dt = _values(logits, what)
+    _packed(ids, (T, k), torch.int32, what, "ids")
+    _packed(grad_weights, (T, k), torch.float32, what, "grad_weights")
+    ldg = _matrix(grad_logits, T, E, logits.dtype, what, "grad_logits")
+    with _on(handle):
+        _check(P.purlin_route_experts_grad(handle.raw, logits, ld, dt, T,
+                                           P.make_routing(E, k, scores, renormalise=renormalise, scale=scale), ids,
+                                           grad_weights, grad_logits, ldg, _stream(stream, handle.device)), what)
+
+
+def expert_plan(ids, offsets, places, handle: Handle, stream=None):
+    """places[t, j] = the row of pick ids[t, j] among all picks sorted by
+    expert (equal ones by token and j); offsets[e] .. offsets[e + 1] are expert
+    e's rows.  ids and places int32, tokens x top_k; offsets int32, experts + 1
+    values.  A pick outside [0, experts) is dropped: its place is ~p, p a row
+    past offsets[experts]."""
+    what = "expert_plan"
+    T, k = _two(ids, what, "ids")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"{what}: offsets must hold experts + 1 values, got {tuple(offsets.shape)}")
+    E = offsets.shape[0] - 1
+    _packed(ids, (T, k), torch.int32, what, "ids")
+    _packed(places, (T, k), torch.int32, what, "places")
+    _packed(offsets, (E + 1,), torch.int32, what, "offsets")
+    with _on(handle):
+        nbytes = P.purlin_expert_plan_bytes(T, k, E)
+        ws = _workspace(nbytes, stream, handle.device)
+        _check(P.purlin_expert_plan(handle.raw, ids, T, k, E, offsets, places, ws, nbytes,
+                                    _stream(stream, handle.device)), what)
+
+
+def dispatch_rows(x, places, rows, handle: Handle, stream=None):
+    """rows[places[t, j]] = x[t]; rows of dropped picks are 0.  x: tokens x
+    width; rows: (tokens x top_k) x width, of one dtype."""
+    what = "dispatch_rows"
+    T, D = _two(x, what, "x")
+    k = _two(places, what, "places")[1]
+    ldx = _matrix(x, T, D, x.dtype, what, "x")
+    dt = _values(x, what)
+    _packed(places, (T, k), torch.int32, what, "places")
+    ldr = _matrix(rows, T * k, D, x.dtype, what, "rows")
+    with _on(handle):
+        _check(P.purlin_dispatch_rows(handle.raw, x, ldx, places, T, k, D, dt, rows, ldr,
+                                      _stream(stream, handle.device)), what)
+
+
+def combine_rows(rows, places, weights, y, handle: Handle, stream=None):
+    """y[t] = the sum over j of weights[t, j] x rows[places[t, j]].  weights:
+    float32, or None for all 1 (the gradient of dispatch_rows)."""
+    what = "combine_rows"
+    T, k = _two(places, what, "places")
+    D = _two(y, what, "y")[1]
+    ldr = _matrix(rows, T * k, D, y.dtype, what, "rows")
+    dt = _values(y, what)
+    _packed(places, (T, k), torch.int32, what, "places")
+    if weights is not None:
+        _packed(weights, (T, k), torch.float32, what, "weights")
+    ldy = _matrix(y, T, D, y.dtype, what, "y")
+    with _on(handle):
+        _check(P.purlin_combine_rows(handle.raw, rows, ldr, places, weights, T, k, D, dt, y, ldy,
+                                     _stream(stream, handle.device)), what)
+
+
+def combine_rows_grad(rows, places, weights, grad_y, grad_rows, grad_weights, handle: Handle, stream=None):
+    """grad_rows[places[t, j]] = weights[t, j] x grad_y[t], and grad_weights[t,
+    j] = the product of rows[places[t, j]] and grad_y[t]."""
+    what = "combine_rows_grad"
+    T, k = _two(places, what, "places")
+    D = _two(grad_y, what, "grad_y")[1]
+    dt = _values(grad_y, what)
+    ldr = _matrix(rows, T * k, D, grad_y.dtype, what, "rows")
+    _packed(places, (T, k), torch.int32, what, "places")
+    _packed(weights, (T, k), torch.float32, what, "weights")
+    ldy = _matrix(grad_y, T, D, grad_y.dtype, what, "grad_y")
+    ldg = _matrix(grad_rows, T * k, D, grad_y.dtype, what, "grad_rows")
+    _packed(grad_weights, (T, k), torch.float32, what, "grad_weights")
+    with _on(handle):
+        _check(P.purlin_combine_rows_grad(handle.raw, rows, ldr, places, weights, grad_y, ldy, T, k, D, dt, grad_rows,
+                                          ldg, grad_weights, _stream(stream, handle.device)), what)
+
+
+def _tokens(tokens, what):
+    if tokens.dim() != 1 or tokens.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{what}: tokens must be a vector of int32 or int64")
+    _packed(tokens, tokens.shape, tokens.dtype, what, "tokens")
+    return tokens.shape[0], tokens.element_size()
+
+
+def embed(table, tokens, out, handle: Handle, first=0, scale=1.0, stream=None):
+    """out[i] = scale x table[tokens[i] - first], 0 for a token outside the
+    table's range of the vocabulary."""
+    what = "embed"
+    R, D = _two(table, what, "table")
+    n, size = _tokens(tokens, what)
+    ldt = _matrix(table, R, D, table.dtype, what, "table")
+    dt = _values(table, what)
+    ldo = _matrix(out, n, D, table.dtype, what, "out")
+    with _on(handle):
+        _check(P.purlin_embed(handle.raw, table, ldt, R, int(first), tokens, size, n, D, scale, dt, out, ldo,
+                              _stream(stream, handle.device)), what)
+
+
+def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0, base=None, stream=None):
+    """grad_table[r] = base[r] + scale x the sum of grad_out[i] over the tokens
+    with tokens[i] - first == r.  base: like grad_table, or None for 0; base is
+    grad_table adds in place and touches only the rows that tokens name.
+    grad_out and grad_table may have different dtypes."""
+    what = "embed_grad"
+    R, D = _two(grad_table, what, "grad_table")
+    n, size = _tokens(tokens, what)
+    dx, dt = _values(grad_out, what), _values(grad_table, what)
+    ldx = _matrix(grad_out, n, D, grad_out.dtype, what, "grad_out")
+    ldt = _matrix(grad_table, R, D, grad_table.dtype, what, "grad_table")
+    ldb = _matrix(base, R, D, grad_table.dtype, what, "base") if base is not None else 0
+    with _on(handle):
+        nbytes = P.purlin_embed_grad_bytes(n, R, D)
+        ws = _workspace(nbytes, stream, handle.device)
+        _check(P.purlin_embed_grad(handle.raw, grad_out, ldx, dx, tokens, size, n, D, scale, base, ldb, grad_table, ldt,
+                                   dt, R, int(first), ws, nbytes, _stream(stream, handle.device)), what)
+
+
+def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, stream=None):
+    """norm[0] = |scale| x the 2-norm of all grads together; outs[i] = grads[i] x
+    scale x min(1, max_norm / (norm + 1e-6)).  grads: contiguous tensors of any
+    shapes and one dtype; outs: as many of the same sizes, or the grads
+    themselves (in place), or None for the norm alone; norm: one float32."""
+    what = "clip_grad_norm"
+    _packed(norm, (1,), torch.float32, what, "norm")
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError(f"{what}: expected {len(grads)} outputs, got {len(outs)}")
+    dt = P.PL_F32
+    counts = [t.numel() for t in grads]
+    if len(grads):
+        dtype = grads[0].dtype
+        dt = _values(grads[0], what)
+        for side in (grads,) if outs is None or outs is grads else (grads, outs):
+            for t, n in zip(side, counts):
+                if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
+                    raise ValueError(f"{what}: gradients and outputs must be contiguous CUDA (or pinned host) tensors of "
+                                     f"one dtype, each output of its gradient's size")
+    with _on(handle):
+        nbytes = P.purlin_clip_grad_norm_bytes()
+        ws = _workspace(nbytes, stream, handle.device)
+        _check(P.purlin_clip_grad_norm(handle.raw, grads, outs, counts, dt, scale, max_norm, norm, ws, nbytes,
+                                       _stream(stream, handle.device)), what)

@@ -79,7 +79,8 @@ typedef enum {
   PL_ERR_LAUNCH = 6,       /* the kernel could not be launched */
   PL_ERR_TIMEOUT = 7,      /* device: a SNAC consume wait gave up */
   PL_ERR_FINALIZED = 8,    /* the handle was finalized */
-  PL_ERR_BOUNDS = 9        /* device, checking build only: a work item reached outside a rank buffer */
+  PL_ERR_BOUNDS = 9        /* device: a place outside an operator's rows; in the checking build also
+                              a work item that reached outside a rank buffer */
 } purlin_status;
 
 typedef enum { PL_U8 = 0, PL_F32 = 1, PL_BF16 = 2 } purlin_dtype;
@@ -295,11 +296,147 @@ purlin_status purlin_atom_reduce(purlin_handle h, const void* const* src, int ns
                                  void* const* dst, int ndst, size_t bytes, purlin_dtype dtype,
                                  purlin_stream_t stream);
 
+/* -------------------------------------------- operators around the collectives */
+
+/* What stands directly before and after the collectives in a training or
+ * serving step: the copies and sums whose rows are named by indices, and the
+ * norm over many buffers.  Routing decides what an AllToAllV carries; plan,
+ * dispatch and combine pack token rows by expert, as purlin_all_to_all_v wants
+ * them, and sum them back; the embedding looks tokens up in one rank's range of
+ * the vocabulary (an AllReduce sums the ranges' parts); the clip takes the
+ * global norm of what a ReduceScatter or AllReduce left.
+ *
+ * The conventions at the top hold (pointers, streams, refusals before any
+ * launch), with these additions:
+ *   - Values are PL_F32 or PL_BF16.  Sums are binary32 in one fixed order,
+ *     rounded once: the same from call to call.
+ *   - Strides count elements from one row's start to the next's, and are at
+ *     least the row's width.  Rows may have any width and any alignment to
+ *     their element; 16-byte aligned rows are the fast path.
+ *   - Written buffers must not overlap any other, except where said.
+ *   - Workspaces are the caller's: at least as many bytes as the _bytes
+ *     function of the same name gives, used until the call's work on the
+ *     stream is done; too few return PL_ERR_WORKSPACE.  Nothing is kept in
+ *     them between calls, and the handle's own workspace is not used, so
+ *     these calls need no order among each other.
+ *   - Indices are read on the device and checked there: each operator says
+ *     what one outside its range does.  None is followed out of a buffer. */
+#define PURLIN_MAX_EXPERTS 1024
+#define PURLIN_MAX_TOP_K 32
+#define PURLIN_MAX_GROUPS 32
+
+typedef enum { PL_SCORES_SOFTMAX = 0, PL_SCORES_SIGMOID = 1 } purlin_scores;
+
+/* How tokens are routed.  Every token's expert scores s are the softmax of its
+ * logits, or their sigmoids 1 / (1 + exp(-x)).  Experts are ordered by s +
+ * bias, where a bias is given (it balances the experts' load and only orders),
+ * else by their logits, which are in the scores' order; equal ones by number.
+ * With groups > 1 the experts stand in that many equal runs; a group counts as
+ * its best expert (group_best 1) or as the sum of its two best (2; of s +
+ * bias, or of s), and only the kept_groups best groups take part.  The top_k
+ * best experts are picked.  A pick's weight is scale x s, with renormalise
+ * scale x s / (the sum of the picks' s + 1e-20). */
+typedef struct {
+  int experts;     /* 1 .. PURLIN_MAX_EXPERTS */
+  int top_k;       /* 1 .. PURLIN_MAX_TOP_K, at most the experts of the kept groups */
+  int scores;      /* purlin_scores */
+  int groups;      /* 1 .. PURLIN_MAX_GROUPS, divides experts */
+  int kept_groups; /* 1 .. groups */
+  int group_best;  /* 1 or 2 */
+  int renormalise; /* 0 or 1 */
+  float scale;
+} purlin_routing;
+
+/* ids[t][j], weights[t][j] (tokens x top_k, packed): token t's j-th best
+ * expert and its weight.  logits: tokens x experts; bias: experts, or NULL.
+ * An expert whose logit (or s + bias) is -inf or NaN is never picked; where
+ * fewer than top_k remain, the other picks have id -1 and weight 0.  A NaN
+ * logit makes the softmax weights of its token NaN. */
+purlin_status purlin_route_experts(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype,
+                                   const float* bias, size_t tokens, const purlin_routing* routing, int32_t* ids,
+                                   float* weights, purlin_stream_t stream);
+
+/* grad_logits = the gradient of the weights, given theirs, with the picks
+ * (ids) held fixed.  The bias has none.  An id outside [0, experts) is no
+ * pick; a token without picks has gradient 0. */
+purlin_status purlin_route_experts_grad(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype,
+                                        size_t tokens, const purlin_routing* routing, const int32_t* ids,
+                                        const float* grad_weights, void* grad_logits, size_t grad_stride,
+                                        purlin_stream_t stream);
+
+/* Places of picks in expert order.  ids (tokens x top_k, packed) are numbered
+ * t x top_k + j; places gives each pick's row among all picks sorted by
+ * expert, equal ones by number.  offsets[e] .. offsets[e + 1] (experts + 1
+ * values) are expert e's rows, so the rows of experts on one rank are one
+ * range, the block that purlin_all_to_all_v sends there.  An id outside [0,
+ * experts) drops the pick: it takes a row p past offsets[experts], and its
+ * place reads ~p, below 0.  tokens x top_k must be below 2^31. */
+size_t purlin_expert_plan_bytes(size_t tokens, int top_k, int experts);
+purlin_status purlin_expert_plan(purlin_handle h, const int32_t* ids, size_t tokens, int top_k, int experts,
+                                 int32_t* offsets, int32_t* places, void* workspace, size_t workspace_bytes,
+                                 purlin_stream_t stream);
+
+/* rows[places[t][j]] = x[t] (tokens rows of x; tokens x top_k rows of rows);
+ * the row of a dropped pick is set to 0.  Every row is written once if the
+ * places are those of a plan.  A place outside the rows is skipped and
+ * recorded as PL_ERR_BOUNDS in the handle's device status. */
+purlin_status purlin_dispatch_rows(purlin_handle h, const void* x, size_t x_stride, const int32_t* places,
+                                   size_t tokens, int top_k, size_t width, purlin_dtype dtype, void* rows,
+                                   size_t rows_stride, purlin_stream_t stream);
+
+/* y[t] = the sum over j, ascending, of weights[t][j] x rows[places[t][j]];
+ * dropped picks add nothing.  weights NULL: all 1, which is the gradient of
+ * purlin_dispatch_rows.  Places as there. */
+purlin_status purlin_combine_rows(purlin_handle h, const void* rows, size_t rows_stride, const int32_t* places,
+                                  const float* weights, size_t tokens, int top_k, size_t width, purlin_dtype dtype,
+                                  void* y, size_t y_stride, purlin_stream_t stream);
+
+/* The gradient of purlin_combine_rows: grad_rows[places[t][j]] = weights[t][j]
+ * x grad_y[t] and grad_weights[t][j] = the product of rows[places[t][j]] and
+ * grad_y[t]; 0 for dropped picks, in both.  Places as there. */
+purlin_status purlin_combine_rows_grad(purlin_handle h, const void* rows, size_t rows_stride, const int32_t* places,
+                                       const float* weights, const void* grad_y, size_t grad_y_stride, size_t tokens,
+                                       int top_k, size_t width, purlin_dtype dtype, void* grad_rows,
+                                       size_t grad_rows_stride, float* grad_weights, purlin_stream_t stream);
+
+/* out[i] = scale x table[tokens[i] - first], or 0 for a token outside [first,
+ * first + rows) (another rank's, or padding).  tokens: n values of token_bytes
+ * 4 or 8, signed. */
+purlin_status purlin_embed(purlin_handle h, const void* table, size_t table_stride, size_t rows, int64_t first,
+                           const void* tokens, int token_bytes, size_t n, size_t width, float scale, purlin_dtype dtype,
+                           void* out, size_t out_stride, purlin_stream_t stream);
+
+/* grad_table[r] = base[r] + scale x the sum of grad_out[i] over the tokens
+ * with tokens[i] - first == r.  base NULL: 0.  base may be grad_table itself
+ * (same stride), which adds to it and touches only the rows that tokens name.
+ * The sum and base are added in binary32 and rounded once to
+ * grad_table_dtype, which base shares.  n, rows and width below 2^31; the
+ * workspace 16-byte aligned. */
+size_t purlin_embed_grad_bytes(size_t tokens, size_t rows, size_t width);
+purlin_status purlin_embed_grad(purlin_handle h, const void* grad_out, size_t grad_out_stride,
+                                purlin_dtype grad_out_dtype, const void* tokens, int token_bytes, size_t n, size_t width,
+                                float scale, const void* base, size_t base_stride, void* grad_table,
+                                size_t grad_table_stride, purlin_dtype grad_table_dtype, size_t rows, int64_t first,
+                                void* workspace, size_t workspace_bytes, purlin_stream_t stream);
+
+/* *norm (device) = |scale| x the 2-norm of all n gradients together, of
+ * counts[i] elements each; outs[i] = grads[i] x scale x min(1, max_norm / (norm
+ * + 1e-6)).  outs NULL: the norm alone.  outs[i] may be grads[i].  max_norm +inf
+ * never clips.  A norm that is not finite follows the formula: infinite, the
+ * factor is 0; NaN, every output is NaN.  Squares are added in binary32 within
+ * a thread's share of 16384 elements and in binary64 from there.  grads, outs
+ * and counts are host arrays, read during the call.  The workspace is 8-byte
+ * aligned. */
+size_t purlin_clip_grad_norm_bytes(void);
+purlin_status purlin_clip_grad_norm(purlin_handle h, const void* const* grads, void* const* outs, const size_t* counts,
+                                    size_t n, purlin_dtype dtype, float scale, float max_norm, float* norm,
+                                    void* workspace, size_t workspace_bytes, purlin_stream_t stream);
+
 /* ------------------------------------------------------ status and tuning */
 
 /* Wait for `stream`'s queued work, then report (and clear) the first error
- * recorded on the device since the last call: *device_status = PL_OK or
- * PL_ERR_TIMEOUT.  Returns PL_OK when the query itself worked. */
+ * recorded on the device since the last call: *device_status = PL_OK,
+ * PL_ERR_TIMEOUT or PL_ERR_BOUNDS.  Returns PL_OK when the query itself worked. */
 purlin_status purlin_status_get(purlin_handle h, purlin_stream_t stream, int* device_status);
 
 const char* purlin_status_string(purlin_status s);
