@@ -195,7 +195,7 @@ def _addr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 def _stream(s):

@@ -207,29 +207,36 @@ def _values(t, what):
     return dt
 
 
-def _matrix(t, rows, width, dtype, what, name):
-    """Checks a rows x width matrix and returns its row stride."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
-        raise ValueError(f"{what}: {name} must be {rows} x {width}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: {name} must have dtype {dtype}")
-    stride = t.stride(0) if rows > 1 else width
-    if (width > 1 and t.stride(1) != 1) or stride < width:
-        raise ValueError(f"{what}: {name} must have packed rows")
+def _resident_one(t, what):
     if not (t.is_cuda or t.is_pinned()):
         raise ValueError(f"{what}: tensors must be CUDA tensors or pinned host tensors")
+
+
+def _matrix(t, rows, width, dtype, what, name):
+    """Checks a rows x width matrix and returns its row stride."""
+    if t.shape != (rows, width):
+        raise ValueError(f"{what}: {name} must be {rows} x {width}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {name} must have dtype {dtype}")
+    stride, one = t.stride()
+    if rows <= 1:
+        stride = width
+    if (one != 1 and width > 1) or stride < width:
+        raise ValueError(f"{what}: {name} must have packed rows")
+    if not t.is_cuda:
+        _resident_one(t, what)
     return stride
 
 
 def _packed(t, shape, dtype, what, name):
     if t.shape != shape:
         raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: {name} must have dtype {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be contiguous")
-    if not (t.is_cuda or t.is_pinned()):
-        raise ValueError(f"{what}: tensors must be CUDA tensors or pinned host tensors")
+    if not t.is_cuda:
+        _resident_one(t, what)
 
 
 def _two(t, what, name):
@@ -251,6 +258,19 @@ def _workspace(nbytes, stream, device):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _call(fn, what, handle, stream, *args):
+    """fn(handle, *args, stream) with the handle's device current.  The guard
+    of the device and the stream's object cost more than a small operator does,
+    so both are skipped where the device is current already."""
+    index = handle.device.index
+    if index is None or torch.cuda.current_device() != index:
+        with _on(handle):
+            _check(fn(handle.raw, *args, _stream(stream, handle.device)), what)
+        return
+    stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, handle.device)
+    _check(fn(handle.raw, *args, stream), what)
+
+
 def route_experts(logits, ids, weights, handle: Handle, bias=None, scores=Scores.SOFTMAX, groups=1, kept_groups=1,
                   group_best=1, renormalise=True, scale=1.0, stream=None):
     """ids[t, j], weights[t, j] = token t's j-th best expert and its weight.
@@ -270,10 +290,8 @@ def route_experts(logits, ids, weights, handle: Handle, bias=None, scores=Scores
     _packed(weights, (T, k), torch.float32, what, "weights")
     if bias is not None:
         _packed(bias, (E,), torch.float32, what, "bias")
-    with _on(handle):
-        _check(P.purlin_route_experts(handle.raw, logits, ld, dt, bias, T,
-                                      P.make_routing(E, k, scores, groups, kept_groups, group_best, renormalise, scale),
-                                      ids, weights, _stream(stream, handle.device)), what)
+    routing = P.make_routing(E, k, scores, groups, kept_groups, group_best, renormalise, scale)
+    _call(P.purlin_route_experts, what, handle, stream, logits, ld, dt, bias, T, routing, ids, weights)
 
 
 def route_experts_grad(logits, ids, grad_weights, grad_logits, handle: Handle, scores=Scores.SOFTMAX, renormalise=True,
@@ -289,10 +307,9 @@ def route_experts_grad(logits, ids, grad_weights, grad_logits, handle: Handle, s
     _packed(ids, (T, k), torch.int32, what, "ids")
     _packed(grad_weights, (T, k), torch.float32, what, "grad_weights")
     ldg = _matrix(grad_logits, T, E, logits.dtype, what, "grad_logits")
-    with _on(handle):
-        _check(P.purlin_route_experts_grad(handle.raw, logits, ld, dt, T,
-                                           P.make_routing(E, k, scores, renormalise=renormalise, scale=scale), ids,
-                                           grad_weights, grad_logits, ldg, _stream(stream, handle.device)), what)
+    routing = P.make_routing(E, k, scores, renormalise=renormalise, scale=scale)
+    _call(P.purlin_route_experts_grad, what, handle, stream, logits, ld, dt, T, routing, ids, grad_weights, grad_logits,
+          ldg)
 
 
 def expert_plan(ids, offsets, places, handle: Handle, stream=None):
@@ -309,11 +326,9 @@ def expert_plan(ids, offsets, places, handle: Handle, stream=None):
     _packed(ids, (T, k), torch.int32, what, "ids")
     _packed(places, (T, k), torch.int32, what, "places")
     _packed(offsets, (E + 1,), torch.int32, what, "offsets")
-    with _on(handle):
-        nbytes = P.purlin_expert_plan_bytes(T, k, E)
-        ws = _workspace(nbytes, stream, handle.device)
-        _check(P.purlin_expert_plan(handle.raw, ids, T, k, E, offsets, places, ws, nbytes,
-                                    _stream(stream, handle.device)), what)
+    nbytes = P.purlin_expert_plan_bytes(T, k, E)
+    ws = _workspace(nbytes, stream, handle.device)
+    _call(P.purlin_expert_plan, what, handle, stream, ids, T, k, E, offsets, places, ws, nbytes)
 
 
 def dispatch_rows(x, places, rows, handle: Handle, stream=None):
@@ -326,9 +341,7 @@ def dispatch_rows(x, places, rows, handle: Handle, stream=None):
     dt = _values(x, what)
     _packed(places, (T, k), torch.int32, what, "places")
     ldr = _matrix(rows, T * k, D, x.dtype, what, "rows")
-    with _on(handle):
-        _check(P.purlin_dispatch_rows(handle.raw, x, ldx, places, T, k, D, dt, rows, ldr,
-                                      _stream(stream, handle.device)), what)
+    _call(P.purlin_dispatch_rows, what, handle, stream, x, ldx, places, T, k, D, dt, rows, ldr)
 
 
 def combine_rows(rows, places, weights, y, handle: Handle, stream=None):
@@ -343,9 +356,7 @@ def combine_rows(rows, places, weights, y, handle: Handle, stream=None):
     if weights is not None:
         _packed(weights, (T, k), torch.float32, what, "weights")
     ldy = _matrix(y, T, D, y.dtype, what, "y")
-    with _on(handle):
-        _check(P.purlin_combine_rows(handle.raw, rows, ldr, places, weights, T, k, D, dt, y, ldy,
-                                     _stream(stream, handle.device)), what)
+    _call(P.purlin_combine_rows, what, handle, stream, rows, ldr, places, weights, T, k, D, dt, y, ldy)
 
 
 def combine_rows_grad(rows, places, weights, grad_y, grad_rows, grad_weights, handle: Handle, stream=None):
@@ -361,16 +372,15 @@ def combine_rows_grad(rows, places, weights, grad_y, grad_rows, grad_weights, ha
     ldy = _matrix(grad_y, T, D, grad_y.dtype, what, "grad_y")
     ldg = _matrix(grad_rows, T * k, D, grad_y.dtype, what, "grad_rows")
     _packed(grad_weights, (T, k), torch.float32, what, "grad_weights")
-    with _on(handle):
-        _check(P.purlin_combine_rows_grad(handle.raw, rows, ldr, places, weights, grad_y, ldy, T, k, D, dt, grad_rows,
-                                          ldg, grad_weights, _stream(stream, handle.device)), what)
+    _call(P.purlin_combine_rows_grad, what, handle, stream, rows, ldr, places, weights, grad_y, ldy, T, k, D, dt,
+          grad_rows, ldg, grad_weights)
 
 
 def _tokens(tokens, what):
     if tokens.dim() != 1 or tokens.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"{what}: tokens must be a vector of int32 or int64")
     _packed(tokens, tokens.shape, tokens.dtype, what, "tokens")
-    return tokens.shape[0], tokens.element_size()
+    return tokens.shape[0], 8 if tokens.dtype is torch.int64 else 4
 
 
 def embed(table, tokens, out, handle: Handle, first=0, scale=1.0, stream=None):
@@ -382,9 +392,7 @@ def embed(table, tokens, out, handle: Handle, first=0, scale=1.0, stream=None):
     ldt = _matrix(table, R, D, table.dtype, what, "table")
     dt = _values(table, what)
     ldo = _matrix(out, n, D, table.dtype, what, "out")
-    with _on(handle):
-        _check(P.purlin_embed(handle.raw, table, ldt, R, int(first), tokens, size, n, D, scale, dt, out, ldo,
-                              _stream(stream, handle.device)), what)
+    _call(P.purlin_embed, what, handle, stream, table, ldt, R, int(first), tokens, size, n, D, scale, dt, out, ldo)
 
 
 def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0, base=None, stream=None):
@@ -399,11 +407,10 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
     ldx = _matrix(grad_out, n, D, grad_out.dtype, what, "grad_out")
     ldt = _matrix(grad_table, R, D, grad_table.dtype, what, "grad_table")
     ldb = _matrix(base, R, D, grad_table.dtype, what, "base") if base is not None else 0
-    with _on(handle):
-        nbytes = P.purlin_embed_grad_bytes(n, R, D)
-        ws = _workspace(nbytes, stream, handle.device)
-        _check(P.purlin_embed_grad(handle.raw, grad_out, ldx, dx, tokens, size, n, D, scale, base, ldb, grad_table, ldt,
-                                   dt, R, int(first), ws, nbytes, _stream(stream, handle.device)), what)
+    nbytes = P.purlin_embed_grad_bytes(n, R, D)
+    ws = _workspace(nbytes, stream, handle.device)
+    _call(P.purlin_embed_grad, what, handle, stream, grad_out, ldx, dx, tokens, size, n, D, scale, base, ldb, grad_table,
+          ldt, dt, R, int(first), ws, nbytes)
 
 
 def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, stream=None):
@@ -415,18 +422,16 @@ def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, strea
     _packed(norm, (1,), torch.float32, what, "norm")
     if outs is not None and len(outs) != len(grads):
         raise ValueError(f"{what}: expected {len(grads)} outputs, got {len(outs)}")
-    dt = P.PL_F32
-    counts = [t.numel() for t in grads]
-    if len(grads):
-        dtype = grads[0].dtype
+    dt, counts = P.PL_F32, [t.numel() for t in grads]
+    if counts:
         dt = _values(grads[0], what)
-        for side in (grads,) if outs is None or outs is grads else (grads, outs):
-            for t, n in zip(side, counts):
-                if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
-                    raise ValueError(f"{what}: gradients and outputs must be contiguous CUDA (or pinned host) tensors of "
-                                     f"one dtype, each output of its gradient's size")
-    with _on(handle):
-        nbytes = P.purlin_clip_grad_norm_bytes()
-        ws = _workspace(nbytes, stream, handle.device)
-        _check(P.purlin_clip_grad_norm(handle.raw, grads, outs, counts, dt, scale, max_norm, norm, ws, nbytes,
-                                       _stream(stream, handle.device)), what)
+        kinds = {(t.dtype, t.is_cuda or t.is_pinned(), t.is_contiguous()) for t in grads}
+        if outs is not None and outs is not grads:
+            kinds |= {(t.dtype, t.is_cuda or t.is_pinned(), t.is_contiguous()) for t in outs}
+            if [t.numel() for t in outs] != counts:
+                raise ValueError(f"{what}: each output must have its gradient's size")
+        if kinds != {(grads[0].dtype, True, True)}:
+            raise ValueError(f"{what}: gradients and outputs must be contiguous CUDA (or pinned host) tensors of one dtype")
+    nbytes = P.purlin_clip_grad_norm_bytes()
+    ws = _workspace(nbytes, stream, handle.device)
+    _call(P.purlin_clip_grad_norm, what, handle, stream, grads, outs, counts, dt, scale, max_norm, norm, ws, nbytes)

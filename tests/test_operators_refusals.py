@@ -73,7 +73,7 @@ def test_clip(h):
     _bad("norm must have shape", purlin.clip_grad_norm, [z(4)], None, 1.0, z(2), h)
     _bad("expected 1 outputs", purlin.clip_grad_norm, [z(4)], [], 1.0, z(1), h)
     _bad("one dtype", purlin.clip_grad_norm, [z(4), z(4, dtype=torch.bfloat16)], None, 1.0, z(1), h)
-    _bad("its gradient's size", purlin.clip_grad_norm, [z(4)], [z(5)], 1.0, z(1), h)
+    _bad("gradient's size", purlin.clip_grad_norm, [z(4)], [z(5)], 1.0, z(1), h)
     _bad("contiguous", purlin.clip_grad_norm, [z(4, 4).t()], None, 1.0, z(1), h)
 
 
