@@ -32,6 +32,7 @@ struct RouteArgs {
   int experts, top_k;
   int sigmoid;
   int groups, kept, best;
+  int group_size, group_shift;  // set by launch_route
   int renormalise;
   float scale;
   int32_t* ids;

@@ -25,24 +25,43 @@ __device__ __forceinline__ uint64_t row_of(const EmbedArgs& a, uint64_t i) {
   return r < a.rows ? r : a.rows;
 }
 
-constexpr int kRowThreads = 256;
-
-template <typename T, int N>
+// A group of tpt threads takes U tokens and keeps one vector of each in flight.
+template <typename T, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreads) embed_kernel(const __grid_constant__ EmbedArgs a, int tpt) {
   op_wait();
-  const uint64_t t = (uint64_t)blockIdx.x * (kRowThreads / tpt) + threadIdx.x / tpt;
-  if (t >= a.n) return;
-  const uint64_t row = row_of(a, t), nv = a.width / N;
-  const T* x = (const T*)a.x + row * a.ldx;
-  T* y = (T*)a.y + t * a.ldy;
-  for (uint64_t v = threadIdx.x % tpt; v < nv; v += tpt) {
-    Pack<T, N> r = zero_pack<T, N>();
-    if (row < a.rows) {
-      r = ld_pack<T, N>(x + v * N);
+  constexpr int V = V16<T>;
+  static_assert(!SHIFT || U == 1, "tokens of one thread cut their rows alike");
+  const int per = blockDim.x / tpt, lane = threadIdx.x % tpt;
+  const uint64_t t0 = (uint64_t)blockIdx.x * per * U + threadIdx.x / tpt;
+  const T* x[U];
+  bool in[U];
 #pragma unroll
-      for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(to_f32(r.v[i]) * a.scale);
+  for (int u = 0; u < U; ++u) {
+    const uint64_t t = t0 + u * per, row = t < a.n ? row_of(a, t) : a.rows;
+    in[u] = row < a.rows;
+    x[u] = (const T*)a.x + row * a.ldx;
+  }
+  const Cut c = cut_of<T, SHIFT>((T*)a.y + t0 * a.ldy, a.width);
+  for (uint64_t v = lane; v < c.nv + c.beside; v += tpt) {
+    if (SHIFT && v >= c.nv) {
+      const uint64_t e = c.at<V>((uint32_t)(v - c.nv));
+      if (t0 < a.n) ((T*)a.y)[t0 * a.ldy + e] = from_f32<T>(ld1_if(x[0] + e, in[0]) * (in[0] ? a.scale : 0.f));
+      continue;
     }
-    st_pack<T, N>(y + v * N, r);
+    Pack<T, V> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = ld_row_if<T, SHIFT>(x[u] + c.head + v * V, in[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) pin(r[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint64_t t = t0 + u * per;
+      if (t >= a.n) continue;
+      // a token outside the range is 0, whatever the scale
+#pragma unroll
+      for (int i = 0; i < V; ++i) r[u].v[i] = from_f32<T>(to_f32(r[u].v[i]) * (in[u] ? a.scale : 0.f));
+      st_pack_once<T, V>((T*)a.y + t * a.ldy + c.head + v * V, r[u]);
+    }
   }
 }
 
@@ -64,6 +83,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint64_t i) {
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortArgs a, uint32_t chunk) {
   op_wait();
+  op_next();
   __shared__ uint32_t hist[kSortBins];
   const int bins = 1 << a.bits;
   for (int b = threadIdx.x; b < bins; b += blockDim.x) hist[b] = 0;
@@ -77,7 +97,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_constant__ SortArgs a, uint32_t chunk,
                                                                   int ipt) {
-  op_wait();
   extern __shared__ uint16_t cnt[];
   __shared__ uint32_t base[kSortBins], before[kSortBins], tmp[33];
   const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -91,11 +110,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
       key[q] = i < a.e.n ? sort_key(a, i) : 0;
       digit[q] = i < a.e.n ? (int)(key[q] >> a.shift & (bins - 1)) : -1;
     }
-  sum_chunks(a.counts, gridDim.x, blockIdx.x, bins, base, before);
   rank_chunk(digit, local, ipt, bins, cnt, [](int, uint32_t) {});
-  uint32_t total;
-  const uint32_t at = block_exclusive(threadIdx.x < bins ? base[threadIdx.x] : 0, tmp, &total);
-  if (threadIdx.x < bins) base[threadIdx.x] = at + before[threadIdx.x];
+  op_wait();
+  sum_chunks(a.counts, gridDim.x, blockIdx.x, bins, base, before);
+  uint32_t carry = 0;
+  for (int b0 = 0; b0 < bins; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    uint32_t total;
+    const uint32_t at = carry + block_exclusive(b < bins ? base[b] : 0, tmp, &total);
+    if (b < bins) base[b] = at + before[b];
+    carry += total;
+  }
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kSortIpt; ++q)
@@ -107,69 +132,143 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     }
 }
 
-// All digits by one CTA, between two arrays in shared memory.
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const __grid_constant__ SortArgs a, int ipt) {
-  op_wait();
-  extern __shared__ uint32_t pair[];  // keys, indexes, then the warps' counters
-  __shared__ uint32_t base[kSortBins], tmp[33];
+// All digits by one cluster.  Its CTAs hold the items in place order, per =
+// 1024 x ipt each; a digit reads them into registers, and writes them to their
+// new places in all CTAs' shared memory, the last digit to the workspace.
+__device__ __forceinline__ void cluster_sort(const SortArgs& a, int ipt, char* shared) {
+  const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  __shared__ uint32_t hist[kSortBins], base[kSortBins], tmp[33];
   const int bins = 1 << a.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t n = (uint32_t)a.e.n;
-  uint32_t *keys = pair, *idx = pair + n;
-  uint16_t* cnt = (uint16_t*)(pair + 2 * n);
-  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-    keys[i] = (uint32_t)row_of(a.e, i);
-    idx[i] = i;
-  }
-  __syncthreads();
+  const uint32_t n = (uint32_t)a.e.n, per = kClusterThreads * ipt, i0 = cluster.block_rank() * per;
+  const int log_per = 31 - __clz(per);
+  uint32_t *keys = (uint32_t*)shared, *idx = keys + per;
+  uint16_t* cnt = (uint16_t*)(idx + per);
   for (int p = 0; p < a.passes; ++p) {
     int digit[kSortIpt];
     uint32_t local[kSortIpt], key[kSortIpt], id[kSortIpt];
 #pragma unroll
     for (int q = 0; q < kSortIpt; ++q)
       if (q < ipt) {
-        const uint32_t i = (uint32_t)(warp * ipt + q) * 32 + lane;
-        key[q] = i < n ? keys[i] : 0;
-        id[q] = i < n ? idx[i] : 0;
-        digit[q] = i < n ? (int)(key[q] >> (p * a.bits) & (bins - 1)) : -1;
+        const uint32_t at = (uint32_t)(warp * ipt + q) * 32 + lane, i = i0 + at;
+        digit[q] = -1;
+        if (i < n) {
+          key[q] = p ? keys[at] : (uint32_t)row_of(a.e, i);
+          id[q] = p ? idx[at] : i;
+          digit[q] = (int)(key[q] >> (p * a.bits) & (bins - 1));
+        }
       }
-    rank_chunk(digit, local, ipt, bins, cnt, [&](int b, uint32_t c) { base[b] = c; });
-    uint32_t carry = 0;
-    for (int b0 = 0; b0 < bins; b0 += blockDim.x) {
-      const int b = b0 + threadIdx.x;
-      uint32_t total;
-      const uint32_t at = carry + block_exclusive(b < bins ? base[b] : 0, tmp, &total);
-      if (b < bins) base[b] = at;
-      carry += total;
-    }
-    __syncthreads();
+    rank_chunk(digit, local, ipt, bins, cnt, [&](int b, uint32_t c) { hist[b] = c; });
+    cluster_bases(hist, bins, base, tmp);
 #pragma unroll
     for (int q = 0; q < kSortIpt; ++q)
       if (q < ipt && digit[q] >= 0) {
         const uint32_t to = base[digit[q]] + cnt[warp * bins + digit[q]] + local[q];
-        keys[to] = key[q];
-        idx[to] = id[q];
+        if (p + 1 < a.passes) {
+          cluster.map_shared_rank(keys, to >> log_per)[to & (per - 1)] = key[q];
+          cluster.map_shared_rank(idx, to >> log_per)[to & (per - 1)] = id[q];
+        } else {
+          a.out_key[to] = key[q];
+          a.out_idx[to] = id[q];
+        }
       }
+    cluster.sync();
+  }
+}
+
+// Row r of the table's gradient where no token names it: zero, or the base's,
+// by `lanes` threads in vectors of B bytes.
+template <int B>
+__device__ __forceinline__ void fill_row(const EmbedArgs& a, int elem, uint64_t r, int lane, int lanes) {
+  using W = uint16_t;
+  char* y = (char*)a.y + r * a.ldy * elem;
+  const char* b = (const char*)a.base + r * a.ldb * elem;
+  const uint64_t nv = a.width * elem / B;
+  if (!a.base) {
+    for (uint64_t v = lane; v < nv; v += lanes) st_pack_once<W, B / 2>((W*)(y + v * B), Pack<W, B / 2>{});
+  } else {
+#pragma unroll 4
+    for (uint64_t v = lane; v < nv; v += lanes)
+      st_pack_once<W, B / 2>((W*)(y + v * B), ld_pack<W, B / 2>((const W*)(b + v * B)));
+  }
+}
+
+// Fills what no token names of rows r0 .. r1.  The rows that tokens name are
+// marked in a bitmap first, by a look at all tokens.
+constexpr uint64_t kBitmapRows = 1 << 18;
+template <int B>
+__device__ __forceinline__ void fill_rows(const EmbedArgs& a, int elem, uint64_t r0, uint64_t r1, uint32_t* bits) {
+  int lanes = 32;  // per row
+  while (lanes > 1 && (uint64_t)lanes / 2 >= a.width * elem / B) lanes /= 2;
+  for (uint64_t s0 = r0; s0 < r1; s0 += kBitmapRows) {
+    const uint32_t rows = (uint32_t)min(kBitmapRows, r1 - s0);
     __syncthreads();
+    for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) bits[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (uint64_t i = threadIdx.x; i < a.n; i += blockDim.x) {
+      const uint64_t r = row_of(a, i) - s0;
+      if (r < rows) atomicOr(bits + r / 32, 1u << (r % 32));
+    }
+    __syncthreads();
+    for (uint32_t k = threadIdx.x / lanes; k < rows; k += blockDim.x / lanes)
+      if (!(bits[k / 32] >> (k % 32) & 1u)) fill_row<B>(a, elem, s0 + k, threadIdx.x % lanes, lanes);
   }
-  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-    a.out_key[i] = keys[i];
-    a.out_idx[i] = idx[i];
+}
+
+// The first cluster sorts, the others fill: that needs no sorted tokens and
+// mostly takes longer than the sort.
+template <int B>
+__global__ void __launch_bounds__(kClusterThreads) sort_fill_kernel(const __grid_constant__ SortArgs a, int ipt, int elem) {
+  op_wait();
+  op_next();
+  extern __shared__ char dyn[];
+  const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const uint32_t skip = a.e.n ? cluster.num_blocks() : 0;
+  if (blockIdx.x < skip) {
+    cluster_sort(a, ipt, dyn);
+    return;
   }
+  const uint64_t part = blockIdx.x - skip, parts = gridDim.x - skip;
+  fill_rows<B>(a.e, elem, a.e.rows * part / parts, a.e.rows * (part + 1) / parts, (uint32_t*)dyn);
 }
 
 // ------------------------------------------------------- sums of sorted rows
 
-constexpr int kRun = 32;          // sorted places of one run
-constexpr int kSumThreads = 128;  // one vector of the row each
-constexpr int kFill = 32;         // table rows of one CTA that fills untouched rows
+constexpr int kRun = 32;          // sorted places of one run, at most
+constexpr int kSumThreads = 256;  // one vector of the row each, at most
 
 struct SumArgs {
   EmbedArgs e;
   const uint32_t *key, *idx;
   float* part;      // [run][head, tail][width]
   uint64_t runs;
+  uint32_t run;     // places of a run
   uint32_t tiles;   // column tiles of a row
+  uint64_t fills;   // CTAs that fill kFill rows each, before those that sum
 };
+
+// The same as fill_rows where the tokens are sorted already and too many to
+// look at: each row is searched among them.
+constexpr int kFill = 32;
+template <typename TY, int N>
+__device__ __forceinline__ void fill_searched(const SumArgs& a, uint64_t r0) {
+  __shared__ uint32_t touched;
+  if (threadIdx.x < 32) {
+    const uint64_t r = r0 + threadIdx.x;
+    uint64_t lo = 0, hi = a.e.n;
+    while (lo < hi) {
+      const uint64_t mid = (lo + hi) / 2;
+      if (a.key[mid] < r) lo = mid + 1;
+      else hi = mid;
+    }
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, r >= a.e.rows || (lo < a.e.n && a.key[lo] == r));
+    if (threadIdx.x == 0) touched = m;
+  }
+  __syncthreads();
+  const int warps = blockDim.x / 32;
+  for (int k = threadIdx.x / 32; k < kFill; k += warps)
+    if (!(touched >> k & 1u)) fill_row<N * sizeof(TY)>(a.e, sizeof(TY), r0 + k, threadIdx.x % 32, 32);
+}
 
 template <typename TY, int N>
 __device__ __forceinline__ void finish(const SumArgs& a, uint64_t row, uint64_t c, const float (&acc)[N]) {
@@ -183,55 +282,29 @@ __device__ __forceinline__ void finish(const SumArgs& a, uint64_t row, uint64_t 
 #pragma unroll
     for (int i = 0; i < N; ++i) o.v[i] = from_f32<TY>(acc[i] * a.e.scale);
   }
-  st_pack<TY, N>((TY*)a.e.y + row * a.e.ldy + c, o);
-}
-
-// Rows that no token names: zero, or the base's.
-template <typename TY, int N>
-__device__ void fill_rows(const SumArgs& a, uint64_t block) {
-  __shared__ uint32_t touched;
-  const uint64_t r0 = block * kFill;
-  if (threadIdx.x < 32) {
-    const uint64_t r = r0 + threadIdx.x;
-    uint64_t lo = 0, hi = a.e.n;
-    while (lo < hi) {
-      const uint64_t mid = (lo + hi) / 2;
-      if (a.key[mid] < r) lo = mid + 1;
-      else hi = mid;
-    }
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, r >= a.e.rows || (lo < a.e.n && a.key[lo] == r));
-    if (threadIdx.x == 0) touched = m;
-  }
-  __syncthreads();
-  const uint64_t nv = a.e.width / N;
-  for (int k = 0; k < kFill; ++k) {
-    if (touched >> k & 1u) continue;
-    for (uint64_t v = threadIdx.x; v < nv; v += kSumThreads) {
-      Pack<TY, N> o = zero_pack<TY, N>();
-      if (a.e.base) o = ld_pack<TY, N>((const TY*)a.e.base + (r0 + k) * a.e.ldb + v * N);
-      st_pack<TY, N>((TY*)a.e.y + (r0 + k) * a.e.ldy + v * N, o);
-    }
-  }
+  st_pack_once<TY, N>((TY*)a.e.y + row * a.e.ldy + c, o);
 }
 
 template <typename TX, typename TY, int N>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant__ SumArgs a) {
   op_wait();
-  if (blockIdx.x >= a.runs * a.tiles) {
-    fill_rows<TY, N>(a, blockIdx.x - a.runs * a.tiles);
+  op_next();
+  if (blockIdx.x < a.fills) {
+    fill_searched<TY, N>(a, (uint64_t)blockIdx.x * kFill);
     return;
   }
+  const uint64_t block = blockIdx.x - a.fills;
   __shared__ uint32_t key[kRun + 2], idx[kRun];  // key[1 + i]: place i of the run; its neighbours at the ends
-  const uint64_t run = blockIdx.x / a.tiles, p0 = run * kRun;
-  const int n = (int)(a.e.n - p0 < kRun ? a.e.n - p0 : kRun);
+  const uint64_t run = block / a.tiles, p0 = run * a.run;
+  const int n = (int)(a.e.n - p0 < a.run ? a.e.n - p0 : a.run);
   const uint32_t none = 0xFFFFFFFFu;
-  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+  for (int i = threadIdx.x; i < n + 2; i += blockDim.x) {
     const uint64_t p = p0 + i;  // place p - 1
     key[i] = p >= 1 && p <= a.e.n ? a.key[p - 1] : none;
     if (i >= 1 && i <= n) idx[i - 1] = a.idx[p - 1];
   }
   __syncthreads();
-  const uint64_t c = ((uint64_t)(blockIdx.x % a.tiles) * kSumThreads + threadIdx.x) * N;
+  const uint64_t c = ((block % a.tiles) * blockDim.x + threadIdx.x) * N;
   if (c >= a.e.width) return;
   const uint32_t rows = (uint32_t)a.e.rows;
   float acc[N];
@@ -243,7 +316,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
     Pack<TX, N> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (q + u < n && key[q + u + 1] < rows) x[u] = ld_pack<TX, N>((const TX*)a.e.x + (uint64_t)idx[q + u] * a.e.ldx + c);
+      x[u] = ld_pack_if<TX, N>((const TX*)a.e.x + (uint64_t)idx[min(q + u, n - 1)] * a.e.ldx + c, q + u < n && key[q + u + 1] < rows);
+#pragma unroll
+    for (int u = 0; u < U; ++u) pin(x[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (q + u >= n) break;
@@ -274,21 +349,32 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
 template <typename TX, typename TY, int N>
 __global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant__ SumArgs a) {
   op_wait();
-  const uint64_t run = blockIdx.x / a.tiles, p0 = run * kRun, p1 = p0 + kRun;
+  const uint64_t run = blockIdx.x / a.tiles, p0 = run * a.run, p1 = p0 + a.run;
   if (p1 >= a.e.n) return;
-  const uint32_t k = a.key[p1 - 1];
-  if (k >= (uint32_t)a.e.rows || a.key[p1] != k) return;
-  if (p0 > 0 && a.key[p0 - 1] == k) return;  // begun earlier
-  const uint64_t c = ((uint64_t)(blockIdx.x % a.tiles) * kSumThreads + threadIdx.x) * N;
+  // loaded together: one after another they would take three round trips
+  const uint32_t k = a.key[p1 - 1], next = a.key[p1], earlier = p0 > 0 ? a.key[p0 - 1] : 0xFFFFFFFFu;
+  if (k >= (uint32_t)a.e.rows || next != k || earlier == k) return;
+  // how many runs it reaches, so that the loads below need not wait for keys
+  __shared__ uint32_t reach;
+  if (threadIdx.x == 0) reach = 0;
+  __syncthreads();
+  for (uint64_t r = run + 1 + threadIdx.x; r < a.runs && a.key[r * a.run] == k; r += blockDim.x)
+    atomicMax(&reach, (uint32_t)(r - run));
+  __syncthreads();
+  const uint64_t c = ((uint64_t)(blockIdx.x % a.tiles) * blockDim.x + threadIdx.x) * N;
   if (c >= a.e.width) return;
   float acc[N];
+  const float* part = a.part + (run * 2 + 1) * a.e.width + c;
   {
-    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(a.part + (run * 2 + 1) * a.e.width + c);
+    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(part);
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = x.v[i];
   }
-  for (uint64_t r = run + 1; r < a.runs && a.key[r * kRun] == k; ++r) {
-    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(a.part + r * 2 * a.e.width + c);
+  part += a.e.width;
+  const uint32_t heads = reach;
+#pragma unroll 16
+  for (uint32_t r = 0; r < heads; ++r) {
+    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(part + (uint64_t)r * 2 * a.e.width);
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] += x.v[i];
   }
@@ -303,29 +389,35 @@ void digits_of(uint64_t rows, int* passes, int* bits) {
   *bits = (b + *passes - 1) / *passes;
 }
 
+// Places of a run: 32, or fewer (8 at least) until the runs of 256-thread
+// tiles fill the SMs twice.
+uint32_t run_of(uint64_t n, uint64_t width) {
+  uint32_t run = kRun;
+  while (run > 8 && (n + run - 1) / run * ((width + 2047) / 2048) < 2 * 152) run /= 2;
+  return run;
+}
+
 struct Space {
   uint64_t key[2], idx[2], counts, part, end;
 };
 
-uint64_t up(uint64_t x) { return (x + 255) & ~(uint64_t)255; }
-
 Space space_of(uint64_t n, uint64_t rows, uint64_t width) {
   int passes, bits;
   digits_of(rows, &passes, &bits);
-  const bool small = n <= kSortSmall;
-  const uint64_t runs = (n + kRun - 1) / kRun;
+  const bool one = n <= kClusterSort;
+  const uint64_t run = run_of(n, width), runs = (n + run - 1) / run;
   Space s;
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
     const uint64_t p = at;
-    at += up(bytes);
+    at += (bytes + 255) & ~(uint64_t)255;
     return p;
   };
   s.key[0] = take(n * 4);
   s.idx[0] = take(n * 4);
-  s.key[1] = take(small ? 0 : n * 4);
-  s.idx[1] = take(small ? 0 : n * 4);
-  s.counts = take(small ? 0 : sort_chunks(n) * ((uint64_t)4 << bits));
+  s.key[1] = take(one ? 0 : n * 4);
+  s.idx[1] = take(one ? 0 : n * 4);
+  s.counts = take(one ? 0 : sort_chunks(n) * ((uint64_t)4 << bits));
   s.part = take(runs > 1 ? runs * 2 * width * 4 : 0);
   s.end = at;
   return s;
@@ -343,13 +435,12 @@ purlin_status sums(const SumArgs& in, cudaStream_t s) {
   auto go = [&](auto n) -> purlin_status {
     constexpr int N = decltype(n)::value;
     SumArgs a = in;
-    a.tiles = (uint32_t)((a.e.width / N + kSumThreads - 1) / kSumThreads);
-    // rows that no token names are left alone when they already hold the base
-    const bool fill = a.e.base != a.e.y || a.e.ldb != a.e.ldy;
-    const uint64_t fills = fill ? (a.e.rows + kFill - 1) / kFill : 0;
-    if (purlin_status st = op_launch(sum_kernel<TX, TY, N>, a.runs * a.tiles + fills, kSumThreads, 0, s, a)) return st;
+    const uint64_t nv = a.e.width / N;
+    a.tiles = (uint32_t)((nv + kSumThreads - 1) / kSumThreads);
+    const int threads = (int)((nv + a.tiles * 32 - 1) / (a.tiles * 32)) * 32;
+    if (purlin_status st = op_launch(sum_kernel<TX, TY, N>, a.fills + a.runs * a.tiles, threads, 0, s, a)) return st;
     if (a.runs < 2) return PL_OK;
-    return op_launch(join_kernel<TX, TY, N>, a.runs * a.tiles, kSumThreads, 0, s, a);
+    return op_launch(join_kernel<TX, TY, N>, a.runs * a.tiles, threads, 0, s, a);
   };
   if constexpr (kMost >= 8)
     if (fits(8)) return go(std::integral_constant<int, 8>());
@@ -358,26 +449,46 @@ purlin_status sums(const SumArgs& in, cudaStream_t s) {
   return go(std::integral_constant<int, 1>());
 }
 
-int threads_per_token(uint64_t nv) {
-  int t = 32;
-  while (t < kRowThreads && (uint64_t)t < nv) t *= 2;
-  return t;
-}
-
 template <typename T>
 purlin_status embed_t(const EmbedArgs& a, cudaStream_t s) {
   const uint64_t bits = (uint64_t)(uintptr_t)a.x | (uint64_t)(uintptr_t)a.y | (a.ldx | a.ldy | a.width) * sizeof(T);
-  return with_vec<T>(vec_bytes(bits), [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    const int tpt = threads_per_token(a.width / N), per = kRowThreads / tpt;
-    return op_launch(embed_kernel<T, N>, (a.n + per - 1) / per, kRowThreads, 0, s, a, tpt);
-  });
+  const RowShape c = RowShape::of<T>(a.width, bits % 16 != 0);
+  auto go = [&](auto shift, auto u) {
+    constexpr int U = decltype(u)::value;
+    return op_launch(embed_kernel<T, decltype(shift)::value, U>, c.ctas(a.n, U), c.tpt * c.per, 0, s, a, c.tpt);
+  };
+  if (bits % 16) return go(std::true_type(), std::integral_constant<int, 1>());
+  if (c.ctas(a.n, 4) < kManyCtas) return go(std::false_type(), std::integral_constant<int, 1>());
+  return go(std::false_type(), std::integral_constant<int, 4>());
 }
 
-purlin_status raise_smem(const void* fn, int bytes) {
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return PL_OK;
-  (void)cudaGetLastError();
-  return PL_ERR_CUDA;
+// Up to kClusterSort tokens: one launch sorts them and fills the rows that
+// none of them names.
+purlin_status launch_sort_fill(const SortArgs& a, bool fill, int elem, cudaStream_t s) {
+  const EmbedArgs& e = a.e;
+  // A fill of 64 MiB or more hides the sort: then few CTAs take many tokens
+  // each, because clusters of 2 find places among the others' that clusters of
+  // 8 do not (16384 tokens, 512 MiB: 122 against 135 us in all).  Else the sort
+  // is what takes the time.
+  const uint64_t bytes = fill ? e.rows * e.width * elem : 0;
+  const ClusterShape c(e.n, bytes >= (uint64_t)64 << 20 ? kSortIpt : 2);
+  // about two rounds of CTAs fill, each at least 16 KiB
+  const uint64_t fills = (std::min<uint64_t>(2 * 152, bytes / 16384) + c.ctas - (fill ? 1 : 0)) / c.ctas * c.ctas;
+  const uint64_t grid = (e.n ? c.ctas : 0) + (fill ? std::max<uint64_t>(fills, c.ctas) : 0);
+  if (grid == 0) return PL_OK;
+  const size_t sorted = e.n ? (size_t)8 * kClusterThreads * c.ipt + ((size_t)kClusterThreads / 32 * 2 << a.bits) : 0;
+  const size_t smem = std::max<size_t>(sorted, fill ? kBitmapRows / 8 : 0);
+  constexpr int kMost = 8 * kClusterThreads * kSortIpt + kClusterThreads / 32 * 2 * kSortBins;
+  const uint64_t rows = (uint64_t)(uintptr_t)e.y | (uint64_t)(uintptr_t)e.base | (e.ldy | e.ldb | e.width) * elem;
+  auto go = [&](auto b) {
+    constexpr int B = decltype(b)::value;
+    if (purlin_status st = op_smem((const void*)sort_fill_kernel<B>, smem, kMost)) return st;
+    return op_launch_cluster(c.ctas, sort_fill_kernel<B>, grid, kClusterThreads, smem, s, a, c.ipt, elem);
+  };
+  const int b = vec_bytes(rows);
+  if (b == 16) return go(std::integral_constant<int, 16>());
+  if (b == 8) return go(std::integral_constant<int, 8>());
+  return b == 4 ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 2>());
 }
 
 }  // namespace
@@ -394,22 +505,17 @@ purlin_status launch_embed_grad(const EmbedArgs& e, int x_dtype, int y_dtype, cu
   SortArgs a = {};
   a.e = e;
   digits_of(e.rows, &a.passes, &a.bits);
-  int out = 0;
+  a.out_key = (uint32_t*)(ws + sp.key[0]);
+  a.out_idx = (uint32_t*)(ws + sp.idx[0]);
+  // rows that no token names are left alone where they hold the base already
+  const bool fill = e.base != e.y || e.ldb != e.ldy;
   purlin_status st;
-  if (e.n == 0) {
-    out = 0;
-  } else if (e.n <= kSortSmall) {
-    a.out_key = (uint32_t*)(ws + sp.key[0]);
-    a.out_idx = (uint32_t*)(ws + sp.idx[0]);
-    const int ipt = (int)((e.n + kSortThreads - 1) / kSortThreads);
-    const uint64_t wide = std::max<uint64_t>(e.n, (uint64_t)1 << a.bits);
-    const int threads = (int)std::min<uint64_t>(kSortThreads, (wide + 31) / 32 * 32);
-    const size_t smem = 8 * e.n + (size_t)(threads / 32 << a.bits) * sizeof(uint16_t);
-    constexpr int kMost = 8 * kSortSmall + kSortWarps * kSortBins * 2;
-    if ((st = raise_smem((const void*)sort_small_kernel, kMost))) return st;
-    if ((st = op_launch(sort_small_kernel, 1, threads, smem, s, a, ipt))) return st;
+  int out = 0;
+  uint64_t fills = 0;
+  if (e.n <= kClusterSort) {
+    if ((st = launch_sort_fill(a, fill, y_dtype == PL_F32 ? 4 : 2, s))) return st;
   } else {
-    if ((st = raise_smem((const void*)sort_place_kernel, kSortWarps * kSortBins * 2))) return st;
+    fills = fill ? (e.rows + kFill - 1) / kFill : 0;
     const uint64_t chunk = sort_chunk(e.n), chunks = sort_chunks(e.n);
     a.counts = (uint32_t*)(ws + sp.counts);
     for (int p = 0; p < a.passes; ++p) {
@@ -417,8 +523,8 @@ purlin_status launch_embed_grad(const EmbedArgs& e, int x_dtype, int y_dtype, cu
       out = p & 1;
       a.out_key = (uint32_t*)(ws + sp.key[out]);
       a.out_idx = (uint32_t*)(ws + sp.idx[out]);
+      const size_t smem = (size_t)(kSortThreads / 32 << a.bits) * sizeof(uint16_t);
       if ((st = op_launch(sort_count_kernel, chunks, kSortThreads, 0, s, a, (uint32_t)chunk))) return st;
-      const size_t smem = (size_t)(kSortWarps << a.bits) * sizeof(uint16_t);
       if ((st = op_launch(sort_place_kernel, chunks, kSortThreads, smem, s, a, (uint32_t)chunk, (int)(chunk / kSortThreads)))) return st;
       a.in_key = a.out_key;
       a.in_idx = a.out_idx;
@@ -429,7 +535,9 @@ purlin_status launch_embed_grad(const EmbedArgs& e, int x_dtype, int y_dtype, cu
   m.key = (const uint32_t*)(ws + sp.key[out]);
   m.idx = (const uint32_t*)(ws + sp.idx[out]);
   m.part = (float*)(ws + sp.part);
-  m.runs = (e.n + kRun - 1) / kRun;
+  m.fills = fills;
+  m.run = run_of(e.n, e.width);
+  m.runs = (e.n + m.run - 1) / m.run;
   if (x_dtype == PL_F32) return y_dtype == PL_F32 ? sums<float, float>(m, s) : sums<float, bf16>(m, s);
   return y_dtype == PL_F32 ? sums<bf16, float>(m, s) : sums<bf16, bf16>(m, s);
 }

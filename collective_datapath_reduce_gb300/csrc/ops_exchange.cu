@@ -18,11 +18,12 @@ __device__ __forceinline__ int expert_of(const int32_t* ids, uint64_t i, uint64_
   return e >= 0 && e < experts ? e : experts;  // bin `experts`: dropped
 }
 
+// Counts of a chunk's picks by expert; dropped ones are not counted.
 __global__ void __launch_bounds__(kSortThreads) plan_count_kernel(const __grid_constant__ PlanArgs a, uint32_t chunk) {
   op_wait();
+  op_next();
   __shared__ uint32_t hist[kSortBins + 1];
-  const int bins = a.experts + 1;
-  for (int b = threadIdx.x; b < bins; b += blockDim.x) hist[b] = 0;
+  for (int b = threadIdx.x; b <= a.experts; b += blockDim.x) hist[b] = 0;
   __syncthreads();
   const uint64_t i0 = (uint64_t)blockIdx.x * chunk;
   for (uint32_t i = threadIdx.x; i < chunk; i += blockDim.x) {
@@ -30,234 +31,462 @@ __global__ void __launch_bounds__(kSortThreads) plan_count_kernel(const __grid_c
     if (e >= 0) atomicAdd(hist + e, 1u);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += blockDim.x) a.counts[(uint64_t)blockIdx.x * bins + b] = hist[b];
+  for (int b = threadIdx.x; b < a.experts; b += blockDim.x) a.counts[(uint64_t)blockIdx.x * a.experts + b] = hist[b];
 }
 
-// One chunk's places.  counts == nullptr: the chunk is everything.
-__global__ void __launch_bounds__(kSortThreads) plan_place_kernel(const __grid_constant__ PlanArgs a, uint32_t chunk,
-                                                                  int ipt) {
-  op_wait();
+__device__ __forceinline__ void store_places(const PlanArgs& a, uint64_t i0, int ipt, const int (&digit)[kSortIpt],
+                                             const uint32_t (&local)[kSortIpt], const uint32_t* base, const uint16_t* cnt) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int q = 0; q < kSortIpt; ++q) {
+    if (q < ipt && digit[q] >= 0) {
+      const uint64_t i = i0 + (uint64_t)(warp * ipt + q) * 32 + lane;
+      const int32_t p = (int32_t)(base[digit[q]] + cnt[warp * (a.experts + 1) + digit[q]] + local[q]);
+      a.places[i] = digit[q] == a.experts ? ~p : p;
+    }
+  }
+}
+
+// One chunk's places, of many.
+__global__ void __launch_bounds__(kSortThreads) plan_place_kernel(const __grid_constant__ PlanArgs a, uint32_t chunk, int ipt) {
   extern __shared__ uint16_t cnt[];
-  __shared__ uint32_t base[kSortBins + 1], before[kSortBins + 1], tmp[33];
-  const int bins = a.experts + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ uint32_t base[kSortBins + 1], before[kSortBins], tmp[33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t i0 = (uint64_t)blockIdx.x * chunk;
   int digit[kSortIpt];
   uint32_t local[kSortIpt];
 #pragma unroll
   for (int q = 0; q < kSortIpt; ++q)
     if (q < ipt) digit[q] = expert_of(a.ids, i0 + (uint64_t)(warp * ipt + q) * 32 + lane, a.slots, a.experts);
-  if (a.counts) {
-    sum_chunks(a.counts, gridDim.x, blockIdx.x, bins, base, before);
-    rank_chunk(digit, local, ipt, bins, cnt, [](int, uint32_t) {});
-  } else {
-    rank_chunk(digit, local, ipt, bins, cnt, [&](int b, uint32_t n) {
-      base[b] = n;
-      before[b] = 0;
-    });
-  }
-  uint32_t carry = 0;
+  rank_chunk(digit, local, ipt, a.experts + 1, cnt, [](int, uint32_t) {});
+  op_wait();
+  sum_chunks(a.counts, gridDim.x, blockIdx.x, a.experts, base, before);
+  uint32_t carry = 0, earlier = 0;  // picks with an expert: all, and those of earlier chunks
   for (int b0 = 0; b0 < a.experts; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    const uint32_t n = b < a.experts ? base[b] : 0;
-    uint32_t total;
+    const uint32_t n = b < a.experts ? base[b] : 0, m = b < a.experts ? before[b] : 0;
+    uint32_t total, more;
     const uint32_t at = carry + block_exclusive(n, tmp, &total);
+    block_exclusive(m, tmp, &more);
     if (b < a.experts) {
-      base[b] = at + before[b];
+      base[b] = at + m;
       if (blockIdx.x == 0) a.offsets[b] = (int32_t)at;
     }
     carry += total;
+    earlier += more;
   }
   if (threadIdx.x == 0) {
-    base[a.experts] = carry + before[a.experts];
+    base[a.experts] = carry + (uint32_t)(i0 - earlier);  // dropped picks follow all others
     if (blockIdx.x == 0) a.offsets[a.experts] = (int32_t)carry;
   }
   __syncthreads();
+  store_places(a, i0, ipt, digit, local, base, cnt);
+}
+
+// All places, by one cluster.
+__global__ void __launch_bounds__(kClusterThreads) plan_cluster_kernel(const __grid_constant__ PlanArgs a, int ipt) {
+  op_wait();
+  extern __shared__ uint16_t cnt[];
+  __shared__ uint32_t hist[kSortBins + 1], base[kSortBins + 1], tmp[33];
+  const int bins = a.experts + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t i0 = (uint64_t)blockIdx.x * blockDim.x * ipt;
+  int digit[kSortIpt];
+  uint32_t local[kSortIpt];
 #pragma unroll
-  for (int q = 0; q < kSortIpt; ++q) {
-    if (q < ipt && digit[q] >= 0) {
-      const uint64_t i = i0 + (uint64_t)(warp * ipt + q) * 32 + lane;
-      const int32_t p = (int32_t)(base[digit[q]] + cnt[warp * bins + digit[q]] + local[q]);
-      a.places[i] = digit[q] == a.experts ? ~p : p;
-    }
-  }
+  for (int q = 0; q < kSortIpt; ++q)
+    if (q < ipt) digit[q] = expert_of(a.ids, i0 + (uint64_t)(warp * ipt + q) * 32 + lane, a.slots, a.experts);
+  rank_chunk(digit, local, ipt, bins, cnt, [&](int b, uint32_t n) { hist[b] = n; });
+  cluster_bases(hist, bins, base, tmp);
+  if (blockIdx.x == 0)  // the first CTA has no items before it: its bases are the experts'
+    for (int b = threadIdx.x; b < bins; b += blockDim.x) a.offsets[b] = (int32_t)base[b];
+  store_places(a, i0, ipt, digit, local, base, cnt);
+  cooperative_groups::this_cluster().sync();  // the counts stay until all have read them
 }
 
 // ------------------------------------------------------------ rows by index
 
-constexpr int kRowThreads = 256;
 
-// A token's row by `tpt` neighbouring threads, 256 / tpt tokens in a CTA.
-struct Lane {
-  uint64_t token;
-  uint32_t first, step;
+// A CTA holds `per` groups of tpt threads (a multiple of 32); each group takes
+// U tokens and keeps one vector of each in flight.  The picks of the CTA's
+// tokens are read once, into shared memory.
+constexpr int kMostTokens = 8 * 4;
+struct Picks {
+  int64_t row[kMostTokens * PURLIN_MAX_TOP_K];  // the row, ~row of a dropped pick, kNoRow outside
+  float w[kMostTokens * PURLIN_MAX_TOP_K];
 };
+constexpr int64_t kNoRow = INT64_MIN;
 
-__device__ __forceinline__ Lane lane_of(int tpt) {
-  return {(uint64_t)blockIdx.x * (kRowThreads / tpt) + threadIdx.x / tpt, threadIdx.x % tpt, (uint32_t)tpt};
+// A place outside the rows is recorded in the handle's status and moves nothing.
+__device__ __forceinline__ void load_picks(const RowsArgs& a, uint64_t t0, int tokens, Picks& s) {
+  const uint64_t left = a.tokens - t0;
+  const int n = (int)(left < tokens ? left : tokens) * a.top_k;
+  for (int i = threadIdx.x; i < tokens * a.top_k; i += blockDim.x) {
+    int64_t row = kNoRow;  // tokens past the end have none
+    float w = 0.f;
+    if (i < n) {
+      const uint64_t slot = t0 * a.top_k + i;
+      const int64_t p = a.places[slot];
+      if ((uint64_t)(p >= 0 ? p : ~p) < a.tokens * (uint64_t)a.top_k) {
+        row = p;
+        if (p >= 0) w = a.weights ? a.weights[slot] : 1.f;
+      } else {
+        op_status(a.status, PL_ERR_BOUNDS);
+      }
+    }
+    s.row[i] = row;
+    s.w[i] = w;
+  }
+  __syncthreads();
 }
 
-// Row of a pick in [0, rows), and whether the pick is live (~row: dropped).  A
-// place outside is recorded in the handle's status and moves nothing.
-__device__ __forceinline__ bool row_of(const RowsArgs& a, uint64_t slot, uint64_t* row, bool* live) {
-  const int32_t p = a.places[slot];
-  *live = p >= 0;
-  *row = (uint64_t)(p >= 0 ? p : ~p);
-  if (*row < a.tokens * (uint64_t)a.top_k) return true;
-  op_status(a.status, PL_ERR_BOUNDS);
-  *live = false;
-  return false;
-}
-
-template <typename T, int N>
+template <typename T, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
-  const Lane l = lane_of(tpt);
-  if (l.token >= a.tokens) return;
-  const T* x = (const T*)a.x + l.token * a.ldx;
-  const uint64_t nv = a.width / N;
-  for (uint64_t v = l.first; v < nv; v += l.step) {
-    const Pack<T, N> r = ld_pack<T, N>(x + v * N);
-    for (int j = 0; j < a.top_k; ++j) {
-      uint64_t row;
-      bool live;
-      if (!row_of(a, l.token * a.top_k + j, &row, &live)) continue;
-      st_pack<T, N>((T*)a.y + row * a.ldy + v * N, live ? r : zero_pack<T, N>());
+  __shared__ Picks picks;
+  const int per = blockDim.x / tpt, group = threadIdx.x / tpt, lane = threadIdx.x % tpt, k = a.top_k;
+  const uint64_t t0 = (uint64_t)blockIdx.x * per * U;
+  load_picks(a, t0, per * U, picks);
+  constexpr int V = V16<T>;
+  const T* x[U];
+  bool on[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint64_t t = t0 + u * per + group;
+    on[u] = t < a.tokens;
+    x[u] = (const T*)a.x + t * a.ldx;
+  }
+  if (!SHIFT) {
+    // every token's vector is read once and stored to all its rows
+    for (uint64_t v = lane; v < a.width / V; v += tpt) {
+      Pack<T, V> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = ld_row_if<T, false>(x[u] + v * V, on[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) pin(r[u]);
+      for (int j = 0; j < k; ++j) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t p = picks.row[(u * per + group) * k + j];
+          if (p == kNoRow) continue;
+          st_pack_once<T, V>((T*)a.y + (uint64_t)(p >= 0 ? p : ~p) * a.ldy + v * V, p >= 0 ? r[u] : zero_pack<T, V>());
+        }
+      }
+    }
+  } else {
+    // each row cuts the token its own way; after the first, it is in the L1
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      for (int j = 0; j < k; ++j) {
+        const int64_t p = picks.row[(u * per + group) * k + j];
+        if (p == kNoRow) continue;
+        T* y = (T*)a.y + (uint64_t)(p >= 0 ? p : ~p) * a.ldy;
+        const Cut c = cut_of<T, true>(y, a.width);
+        for (uint64_t v = lane; v < c.nv + c.beside; v += tpt) {
+          if (v < c.nv) {
+            st_pack_once<T, V>(y + c.head + v * V, ld_row_if<T, true>(x[u] + c.head + v * V, p >= 0));
+          } else {
+            const uint64_t e = c.at<V>((uint32_t)(v - c.nv));
+            y[e] = from_f32<T>(ld1_if(x[u] + e, p >= 0));
+          }
+        }
+      }
     }
   }
 }
 
-// y = sum over j of w_j rows[place_j], in binary32, ascending j.
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const __grid_constant__ RowsArgs a, int tpt) {
+// y = sum over j of w_j rows[place_j], in binary32, ascending j: J rows of U
+// tokens are in flight in each thread.  Four CTAs per SM: with the registers
+// that the compiler takes by itself (32), it spreads the loads out again.
+template <typename T, int U, int J>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
-  const Lane l = lane_of(tpt);
-  if (l.token >= a.tokens) return;
-  T* y = (T*)a.y + l.token * a.ldy;
-  const uint64_t nv = a.width / N;
-  for (uint64_t v = l.first; v < nv; v += l.step) {
-    float acc[N];
+  __shared__ Picks picks;
+  const int per = blockDim.x / tpt, group = threadIdx.x / tpt, lane = threadIdx.x % tpt, k = a.top_k;
+  const uint64_t t0 = (uint64_t)blockIdx.x * per * U;
+  load_picks(a, t0, per * U, picks);
+  constexpr int V = V16<T>;
+  for (uint64_t v = lane; v < a.width / V; v += tpt) {
+    float acc[U][V];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < a.top_k; ++j) {
-      uint64_t row;
-      bool live;
-      if (!row_of(a, l.token * a.top_k + j, &row, &live) || !live) continue;
-      const float w = a.weights ? a.weights[l.token * a.top_k + j] : 1.f;
-      const Pack<T, N> r = ld_pack<T, N>((const T*)a.x + row * a.ldx + v * N);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(w, to_f32(r.v[i]), acc[i]);
+      for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += J) {
+      Pack<T, V> r[U][J];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int64_t p = j0 + j < k ? picks.row[(u * per + group) * k + j0 + j] : kNoRow;
+          r[u][j] = ld_row_if<T, false>((const T*)a.x + (uint64_t)p * a.ldx + v * V, p >= 0);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) pin(r[u][j]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float w = j0 + j < k ? picks.w[(u * per + group) * k + j0 + j] : 0.f;  // 0 where nothing was loaded
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[u][i] = __fmaf_rn(w, to_f32(r[u][j].v[i]), acc[u][i]);
+        }
     }
-    Pack<T, N> o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-    st_pack<T, N>(y + v * N, o);
+    for (int u = 0; u < U; ++u) {
+      const uint64_t t = t0 + u * per + group;
+      if (t >= a.tokens) continue;
+      Pack<T, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o.v[i] = from_f32<T>(acc[u][i]);
+      st_pack_once<T, V>((T*)a.y + t * a.ldy + v * V, o);
+    }
   }
 }
 
-// grad_rows[place_j] = w_j dy, grad_w_j = <rows[place_j], dy>: one warp per
-// token and pick holds the product's partial sums.
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(const __grid_constant__ RowsArgs a) {
+// The same for rows that are not 16-byte aligned: S elements of a thread, tpt
+// apart, of J rows each in flight.  Cutting aligned vectors out of the rows'
+// granules moves fewer requests but waits longer for each (41 against 25
+// us for 3001 tokens, 6 rows of 1537 binary32 values).
+template <typename T, int S, int J>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_narrow_kernel(const __grid_constant__ RowsArgs a, int tpt) {
+  op_wait();
+  __shared__ Picks picks;
+  const int per = blockDim.x / tpt, group = threadIdx.x / tpt, lane = threadIdx.x % tpt, k = a.top_k;
+  const uint64_t t0 = (uint64_t)blockIdx.x * per;
+  load_picks(a, t0, per, picks);
+  for (uint64_t e = lane; e < a.width; e += (uint64_t)S * tpt) {
+    float acc[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += J) {
+      float x[J][S];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t p = j0 + j < k ? picks.row[group * k + j0 + j] : kNoRow;
+        const T* row = (const T*)a.x + (uint64_t)p * a.ldx + e;
+#pragma unroll
+        for (int i = 0; i < S; ++i) x[j][i] = ld1_if(row + i * tpt, p >= 0 && e + i * tpt < a.width);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < S; ++i) asm volatile("" : "+f"(x[j][i]));
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float w = j0 + j < k ? picks.w[group * k + j0 + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < S; ++i) acc[i] = __fmaf_rn(w, x[j][i], acc[i]);
+      }
+    }
+    if (t0 + group >= a.tokens) continue;
+    T* y = (T*)a.y + (t0 + group) * a.ldy + e;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+      if (e + i * tpt < a.width) y[i * tpt] = from_f32<T>(acc[i]);
+  }
+}
+
+// grad_rows[place_j] = w_j dy, grad_w_j = <rows[place_j], dy>: dy is read once
+// for J picks, and J rows are in flight in each thread.  The products' parts
+// are joined in a fixed order, by lanes and then by warps.  Rows are stored
+// evict-first: as ordinary stores they cost a third more.
+template <typename T, int J>
+__global__ void __launch_bounds__(kRowThreads, 4) combine_grad_kernel(const __grid_constant__ RowsArgs a, int tpt) {
+  op_wait();
+  __shared__ Picks picks;
+  __shared__ float part[kRowThreads / 32][J];
+  const int per = blockDim.x / tpt, group = threadIdx.x / tpt, first = threadIdx.x % tpt, k = a.top_k;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t t = (uint64_t)blockIdx.x * per + group;
+  load_picks(a, (uint64_t)blockIdx.x * per, per, picks);
+  constexpr int V = V16<T>;
+  const bool on = t < a.tokens;
+  const T* dy = (const T*)a.grad_y + t * a.ldg;
+  for (int j0 = 0; j0 < k; j0 += J) {
+    float dot[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) dot[j] = 0.f;
+    for (uint64_t v = first; v < a.width / V; v += tpt) {
+      Pack<T, V> g = ld_row_if<T, false>(dy + v * V, on), r[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t p = j0 + j < k ? picks.row[group * k + j0 + j] : kNoRow;
+        r[j] = ld_row_if<T, false>((const T*)a.x + (uint64_t)p * a.ldx + v * V, p >= 0);
+      }
+      pin(g);
+#pragma unroll
+      for (int j = 0; j < J; ++j) pin(r[j]);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t p = j0 + j < k ? picks.row[group * k + j0 + j] : kNoRow;
+        if (p == kNoRow) continue;
+        const float w = picks.w[group * k + j0 + j];
+        Pack<T, V> o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          dot[j] = __fmaf_rn(to_f32(r[j].v[i]), to_f32(g.v[i]), dot[j]);
+          o.v[i] = from_f32<T>(w * to_f32(g.v[i]));
+        }
+        st_pack_once<T, V>((T*)a.y + (uint64_t)(p >= 0 ? p : ~p) * a.ldy + v * V, p >= 0 ? o : zero_pack<T, V>());
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+      if (lane == 0) part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (on && first < J && j0 + first < k) {
+      float s = 0.f;
+      for (int q = 0; q < tpt / 32; ++q) s += part[group * (tpt / 32) + q][first];
+      a.grad_weights[t * k + j0 + first] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// The same for rows that are not 16-byte aligned: one warp for each pick.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const __grid_constant__ RowsArgs a) {
   op_wait();
   const uint64_t slot = (uint64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
   if (slot >= a.tokens * a.top_k) return;
+  constexpr int V = V16<T>;
   const int lane = threadIdx.x & 31;
-  uint64_t row;
-  bool live;
-  const bool in = row_of(a, slot, &row, &live);
-  const float w = a.weights && live ? a.weights[slot] : live ? 1.f : 0.f;
+  const int32_t p = a.places[slot];
+  const bool live = p >= 0;
+  const uint64_t row = (uint64_t)(live ? p : ~p);
+  if (row >= a.tokens * (uint64_t)a.top_k) {
+    if (lane == 0) {
+      op_status(a.status, PL_ERR_BOUNDS);
+      a.grad_weights[slot] = 0.f;
+    }
+    return;
+  }
   const T* dy = (const T*)a.grad_y + slot / a.top_k * a.ldg;
   const T* x = (const T*)a.x + row * a.ldx;
   T* dx = (T*)a.y + row * a.ldy;
+  const float w = live ? a.weights[slot] : 0.f;
+  const Cut c = cut_of<T, true>(dx, a.width);
   float dot = 0.f;
-  if (in) {
-    const uint64_t nv = a.width / N;
-#pragma unroll 2
-    for (uint64_t v = lane; v < nv; v += 32) {
-      const Pack<T, N> g = ld_pack<T, N>(dy + v * N);
-      Pack<T, N> o = zero_pack<T, N>();
-      if (live) {
-        const Pack<T, N> r = ld_pack<T, N>(x + v * N);
+  for (uint64_t v = lane; v < c.nv; v += 32) {
+    Pack<T, V> g = ld_row_if<T, true>(dy + c.head + v * V, live);
+    const Pack<T, V> r = ld_row_if<T, true>(x + c.head + v * V, live);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dot = __fmaf_rn(to_f32(r.v[i]), to_f32(g.v[i]), dot);
-          o.v[i] = from_f32<T>(w * to_f32(g.v[i]));
-        }
-      }
-      st_pack<T, N>(dx + v * N, o);
+    for (int i = 0; i < V; ++i) {
+      dot = __fmaf_rn(to_f32(r.v[i]), to_f32(g.v[i]), dot);
+      g.v[i] = from_f32<T>(w * to_f32(g.v[i]));
     }
+    st_pack_once<T, V>(dx + c.head + v * V, live ? g : zero_pack<T, V>());
+  }
+  for (uint32_t i = lane; i < c.beside; i += 32) {
+    const uint64_t e = c.at<V>(i);
+    const float r = ld1_if(x + e, live), g = ld1_if(dy + e, live);
+    dot = __fmaf_rn(r, g, dot);
+    dx[e] = from_f32<T>(live ? w * g : 0.f);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
   if (lane == 0) a.grad_weights[slot] = dot;
 }
 
+// Whether every row is 16-byte aligned and a whole number of vectors.
 template <typename T>
-uint64_t row_bits(const RowsArgs& a) {
-  return (uint64_t)(uintptr_t)a.x | (uint64_t)(uintptr_t)a.y | (uint64_t)(uintptr_t)a.grad_y |
-         (a.ldx | a.ldy | a.ldg | a.width) * sizeof(T);
-}
-
-// Threads per token: a power of two that covers the row, 32 to 256.
-int threads_per_token(uint64_t nv) {
-  int t = 32;
-  while (t < kRowThreads && (uint64_t)t < nv) t *= 2;
-  return t;
+bool aligned(const RowsArgs& a) {
+  const uint64_t bits = (uint64_t)(uintptr_t)a.x | (uint64_t)(uintptr_t)a.y | (uint64_t)(uintptr_t)a.grad_y |
+                        (a.ldx | a.ldy | a.ldg | a.width) * sizeof(T);
+  return bits % 16 == 0;
 }
 
 }  // namespace
 
 size_t expert_plan_bytes(uint64_t slots, int experts) {
-  if (slots <= kSortSmall) return 0;
-  return (size_t)(sort_chunks(slots) * (uint64_t)(experts + 1) * sizeof(uint32_t));
+  if (slots <= kClusterSort) return 0;
+  return (size_t)(sort_chunks(slots) * (uint64_t)experts * sizeof(uint32_t));
 }
 
-purlin_status launch_expert_plan(const PlanArgs& in, cudaStream_t s) {
-  PlanArgs a = in;
+purlin_status launch_expert_plan(const PlanArgs& a, cudaStream_t s) {
   const int bins = a.experts + 1;
-  static_assert(kSortWarps * (kSortBins + 1) * sizeof(uint16_t) <= 96 * 1024, "counters fit shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return PL_ERR_CUDA;
+  purlin_status st;
+  if (a.slots <= kClusterSort) {
+    const ClusterShape c(a.slots);
+    int threads = kClusterThreads;
+    if (c.ctas == 1 && c.ipt == 1) {  // few picks: as many warps as they or the bins need
+      const uint64_t wide = std::max<uint64_t>(a.slots, bins);
+      threads = (int)std::min<uint64_t>(kClusterThreads, (wide + 31) / 32 * 32);
+    }
+    const size_t smem = (size_t)(threads / 32) * bins * sizeof(uint16_t);
+    constexpr int kMost = kClusterThreads / 32 * (kSortBins + 1) * sizeof(uint16_t);
+    if ((st = op_smem((const void*)plan_cluster_kernel, smem, kMost))) return st;
+    return op_launch_cluster(c.ctas, plan_cluster_kernel, c.ctas, threads, smem, s, a, c.ipt);
   }
-  if (a.slots <= kSortSmall) {
-    a.counts = nullptr;
-    const int ipt = (int)std::max<uint64_t>(1, (a.slots + kSortThreads - 1) / kSortThreads);
-    const int threads = (int)std::min<uint64_t>(kSortThreads, std::max<uint64_t>(32, (std::max<uint64_t>(a.slots, bins) + 31) / 32 * 32));
-    return op_launch(plan_place_kernel, 1, threads, (size_t)(threads / 32) * bins * sizeof(uint16_t), s, a, (uint32_t)0, ipt);
-  }
-  const uint64_t chunk = sort_chunk(a.slots);
-  if (purlin_status st = op_launch(plan_count_kernel, sort_chunks(a.slots), kSortThreads, 0, s, a, (uint32_t)chunk)) return st;
-  return op_launch(plan_place_kernel, sort_chunks(a.slots), kSortThreads, (size_t)kSortWarps * bins * sizeof(uint16_t), s, a,
-                   (uint32_t)chunk, (int)(chunk / kSortThreads));
+  const uint32_t chunk = (uint32_t)sort_chunk(a.slots);
+  const uint64_t chunks = sort_chunks(a.slots);
+  const size_t smem = (size_t)(kSortThreads / 32) * bins * sizeof(uint16_t);
+  if ((st = op_launch(plan_count_kernel, chunks, kSortThreads, 0, s, a, chunk))) return st;
+  return op_launch(plan_place_kernel, chunks, kSortThreads, smem, s, a, chunk, (int)(chunk / kSortThreads));
 }
 
 template <typename T>
 purlin_status dispatch_t(const RowsArgs& a, cudaStream_t s) {
-  return with_vec<T>(vec_bytes(row_bits<T>(a)), [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    const int tpt = threads_per_token(a.width / N);
-    return op_launch(dispatch_kernel<T, N>, (a.tokens + kRowThreads / tpt - 1) / (kRowThreads / tpt), kRowThreads, 0, s, a, tpt);
-  });
+  const bool shift = !aligned<T>(a);
+  const RowShape c = RowShape::of<T>(a.width, shift);
+  auto go = [&](auto sh, auto u) {
+    constexpr int U = decltype(u)::value;
+    return op_launch(dispatch_kernel<T, decltype(sh)::value, U>, c.ctas(a.tokens, U), c.tpt * c.per, 0, s, a, c.tpt);
+  };
+  const std::integral_constant<int, 1> one;
+  if (shift) return go(std::true_type(), one);
+  // with few copies of each token, two tokens (1 pick: 22 against 24 us at 8192 x 4096; 8 picks: 94 against 92)
+  if (a.top_k > 4 || c.ctas(a.tokens, 2) < kManyCtas) return go(std::false_type(), one);
+  return go(std::false_type(), std::integral_constant<int, 2>());
+}
+
+// f(integral_constant i) for i in 1 .. N
+template <int N, typename F>
+purlin_status with_int(int i, F f) {
+  if constexpr (N > 1)
+    if (i < N) return with_int<N - 1>(i, f);
+  return f(std::integral_constant<int, N>());
+}
+
+// Rows in flight: the picks in as few equal passes of at most 8 as hold them.
+int rows_in_flight(int k) {
+  const int passes = (k + 7) / 8;
+  return (k + passes - 1) / passes;
 }
 
 template <typename T>
 purlin_status combine_t(const RowsArgs& a, cudaStream_t s) {
-  return with_vec<T>(vec_bytes(row_bits<T>(a)), [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    const int tpt = threads_per_token(a.width / N);
-    return op_launch(combine_kernel<T, N>, (a.tokens + kRowThreads / tpt - 1) / (kRowThreads / tpt), kRowThreads, 0, s, a, tpt);
+  const bool narrow = !aligned<T>(a);
+  return with_int<8>(rows_in_flight(a.top_k), [&](auto each) {
+    constexpr int J = decltype(each)::value;
+    if (narrow) {
+      constexpr int S = sizeof(T) == 4 ? 2 : 4;
+      const RowShape c((a.width + S - 1) / S);
+      return op_launch(combine_narrow_kernel<T, S, J>, c.ctas(a.tokens, 1), c.tpt * c.per, 0, s, a, c.tpt);
+    }
+    // with few picks, more tokens
+    constexpr int U = J == 1 ? 4 : J == 2 ? 2 : 1;
+    const RowShape c(a.width / V16<T>);
+    if (U > 1 && c.ctas(a.tokens, U) >= kManyCtas)
+      return op_launch(combine_kernel<T, U, J>, c.ctas(a.tokens, U), c.tpt * c.per, 0, s, a, c.tpt);
+    return op_launch(combine_kernel<T, 1, J>, c.ctas(a.tokens, 1), c.tpt * c.per, 0, s, a, c.tpt);
   });
 }
 
 template <typename T>
 purlin_status combine_grad_t(const RowsArgs& a, cudaStream_t s) {
-  return with_vec<T>(vec_bytes(row_bits<T>(a)), [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    return op_launch(combine_grad_kernel<T, N>, (a.tokens * a.top_k + kRowThreads / 32 - 1) / (kRowThreads / 32), kRowThreads, 0,
-                     s, a);
+  if (!aligned<T>(a)) {
+    const uint64_t grid = (a.tokens * a.top_k + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    return op_launch(combine_grad_shift_kernel<T>, grid, kRowThreads, 0, s, a);
+  }
+  return with_int<8>(rows_in_flight(a.top_k), [&](auto each) {
+    const RowShape c(a.width / V16<T>);
+    return op_launch(combine_grad_kernel<T, decltype(each)::value>, c.ctas(a.tokens, 1), c.tpt * c.per, 0, s, a, c.tpt);
   });
 }
 

@@ -2,9 +2,8 @@
 //
 // One warp holds one token's logits, VPT neighbouring experts in each lane's
 // registers, as keys: a binary32 value mapped to an unsigned integer of the
-// same order (0 = the expert may not be picked), so that the best of the row
-// is one integer max across the warp and ties fall to the lowest lane, which
-// holds the lowest expert.
+// same order, so that the best of the row is one integer max across the warp
+// and ties fall to the lowest lane, which holds the lowest expert.
 #include <float.h>
 #include <math.h>
 
@@ -18,16 +17,19 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;  // tokens per CTA
 
-// Order-preserving map to unsigned; -inf and NaN map to 0, below everything.
-// Adding +0 first makes -0 and +0 one key.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  if (!(x > -INFINITY)) return 0;
-  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.f));
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+constexpr uint32_t kOff = 0x007FFFFFu;   // the key of -inf: may not be picked
+constexpr uint32_t kLook = 0xFFFFFFFFu;  // above every key: the lane has to look for its best again
+
+// Order-preserving map to unsigned.  NaN, the lesser of every maximum, becomes
+// -inf; adding +0 makes -0 and +0 one key.
+__device__ __forceinline__ uint32_t key_of_sum(float x) {
+  const int b = __float_as_int(fmaxf(x, -INFINITY));
+  return (uint32_t)(b ^ (b >> 31 | (int)0x80000000));
 }
+__device__ __forceinline__ uint32_t key_of(float x) { return key_of_sum(__fadd_rn(x, 0.f)); }
 
 __device__ __forceinline__ float of_key(uint32_t k) {
-  return k == 0 ? -INFINITY : __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -38,7 +40,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // Binary32 operations in the order of the formula, each rounded: the scores
 // that decide between experts are the same as any other IEEE evaluation of it.
-__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x))); }
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(__fadd_rn(1.f, expf(-x))); }
 
 template <typename T, int VPT>
 __device__ __forceinline__ void load_logits(const T* row, int lane, int experts, bool vec, float (&x)[VPT]) {
@@ -65,11 +67,11 @@ __device__ __forceinline__ void load_logits(const T* row, int lane, int experts,
 // Largest logit of the row, 0 where there is none; the sum of exp(x - best).
 template <int VPT>
 __device__ __forceinline__ void softmax_of(const float (&x)[VPT], int lane, int experts, float* best, float* sum) {
-  uint32_t m = 0;
+  uint32_t m = kOff;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) m = max(m, key_of(x[i]));
   m = __reduce_max_sync(kAll, m);
-  *best = m ? of_key(m) : 0.f;
+  *best = m > kOff ? of_key(m) : 0.f;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
@@ -77,49 +79,70 @@ __device__ __forceinline__ void softmax_of(const float (&x)[VPT], int lane, int 
   *sum = warp_sum(s);
 }
 
-// Keeps the keys of the `kept` best groups.  `val` (shared, one warp's own):
-// every expert's value of the group score; P lanes scan one group's.
-template <int VPT>
-__device__ __forceinline__ void keep_groups(uint32_t (&key)[VPT], const float* val, int lane, const RouteArgs& a) {
-  const int n = a.experts / a.groups;
-  int P = 32;
-  while (P * a.groups > 32) P >>= 1;
-  const int g = lane / P, q = lane % P;
-  float one = -INFINITY, two = -INFINITY;
-  if (g < a.groups) {
-    for (int i = q; i < n; i += P) {
-      const float v = val[g * n + i];
-      two = fmaxf(two, fminf(one, v));
-      one = fmaxf(one, v);
-    }
-  }
-  for (int d = 1; d < P; d <<= 1) {
-    const float o1 = __shfl_xor_sync(kAll, one, d), o2 = __shfl_xor_sync(kAll, two, d);
-    two = fmaxf(fmaxf(two, o2), fminf(one, o1));
-    one = fmaxf(one, o1);
-  }
-  const float of_group = a.best == 2 && two > -INFINITY ? __fadd_rn(one, two) : one;
-  uint32_t gk = g < a.groups && q == 0 ? key_of(of_group) : 0;
-  uint32_t keep = 0;  // bit g: group g
-  for (int r = 0; r < a.kept; ++r) {
-    const uint32_t top = __reduce_max_sync(kAll, gk);
-    if (top == 0) break;
-    const int who = __ffs(__ballot_sync(kAll, gk == top)) - 1;
-    if (lane == who) gk = 0;
-    keep |= 1u << (who / P);
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int e = lane * VPT + i;
-    if (e < a.experts && !(keep >> (e / n) & 1u)) key[i] = 0;
-  }
+// The better two of two pairs.
+__device__ __forceinline__ void merge_two(float& one, float& two, float o1, float o2) {
+  two = fmaxf(fmaxf(two, o2), fminf(one, o1));
+  one = fmaxf(one, o1);
 }
 
+__device__ __forceinline__ uint32_t lowest(uint32_t bits) { return bits & (0u - bits); }
+
+// Bits of the first lanes of the `kept` best groups.  2^shift neighbouring
+// lanes hold a group's best two values (first group in lane 0).
+__device__ __forceinline__ uint32_t kept_groups(float one, float two, int shift, int lane, const RouteArgs& a) {
+  for (int d = 1; d < 1 << shift; d <<= 1) {
+    const float o1 = __shfl_xor_sync(kAll, one, d), o2 = __shfl_xor_sync(kAll, two, d);
+    merge_two(one, two, o1, o2);
+  }
+  const float value = a.best == 2 && two > -INFINITY ? __fadd_rn(one, two) : one;
+  const bool first = (lane & ((1 << shift) - 1)) == 0 && lane >> shift < a.groups;
+  uint32_t key = first ? key_of(value) : kOff;
+  uint32_t keep = 0;
+  for (int r = 0; r < a.kept; ++r) {
+    const uint32_t top = __reduce_max_sync(kAll, key);
+    if (top <= kOff) break;
+    const uint32_t best = lowest(__ballot_sync(kAll, key == top));
+    if (best == 1u << lane) key = kOff;
+    keep |= best;
+  }
+  return keep;
+}
+
+// A lane's best two keys and their experts, equal ones in order.
+struct Two {
+  uint32_t k1, k2;
+  int e1, e2;
+};
+template <int VPT>
+__device__ __forceinline__ Two best_two(const uint32_t (&key)[VPT], int e0) {
+  Two t = {kOff, kOff, 0, 0};
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const bool first = key[i] > t.k1, second = key[i] > t.k2;
+    t.k2 = first ? t.k1 : max(t.k2, key[i]);
+    t.e2 = first ? t.e1 : second ? e0 + i : t.e2;
+    t.k1 = max(t.k1, key[i]);
+    t.e1 = first ? e0 + i : t.e1;
+  }
+  return t;
+}
+
+// The picks are taken one by one: each lane offers its best key left, one
+// integer max across the warp finds the best of the row.  A lane keeps its best
+// two keys ready and searches its registers again only after its second pick.
+//
+// Bound by the instructions of a row, not by its bytes.  16384 tokens, 256
+// experts, 8 picks, sigmoid, bias, 4 of 8 groups by their best two: 35 us with a
+// search at every pick, 22 us with two keys ready, 19 us with shifts for the
+// divisions by the group's lanes, and the pick found by its lane's bit and
+// passed through shared memory (bit scans and reductions run at half a warp
+// per cycle and SM).
 template <typename T, int VPT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a, int vec) {
   op_wait();
   extern __shared__ float shared[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int picks[kWarps][PURLIN_MAX_TOP_K];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * VPT;
   const uint64_t t = (uint64_t)blockIdx.x * kWarps + warp;
   if (t >= a.tokens) return;
   const T* row = (const T*)a.logits + t * a.ld;
@@ -129,51 +152,87 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   if (!a.sigmoid) softmax_of<VPT>(x, lane, a.experts, &best, &sum);
 
   uint32_t key[VPT];
-  float* val = shared + warp * a.experts;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int e = lane * VPT + i;
-    key[i] = key_of(x[i]);
-    if (a.bias && key[i]) {
+  for (int i = 0; i < VPT; ++i) key[i] = key_of(x[i]);
+  if (a.bias && e0 < a.experts) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const float b = e0 + i < a.experts ? __ldg(a.bias + e0 + i) : 0.f;
       const float s = a.sigmoid ? sigmoid(x[i]) : __fdiv_rn(expf(__fsub_rn(x[i], best)), sum);
-      key[i] = key_of(__fadd_rn(s, a.bias[e]));
-    }
-    if (a.groups > 1 && e < a.experts) {
-      float v = of_key(key[i]);
-      if (a.best == 2 && !a.bias && key[i]) v = a.sigmoid ? sigmoid(x[i]) : expf(__fsub_rn(x[i], best));
-      val[e] = v;
+      key[i] = key[i] > kOff ? key_of_sum(__fadd_rn(s, b)) : kOff;  // scores are +0 at least: the sum is never -0
     }
   }
-  if (a.groups > 1) {
-    __syncwarp();
-    keep_groups<VPT>(key, val, lane, a);
-  }
+  // what counts for a group of the expert with this key: s + bias or the
+  // logit, or, of a sum of two without a bias, s (softmax: times the sum)
+  const bool by_score = a.best == 2 && !a.bias;
+  auto value = [&](uint32_t k) {
+    const float v = of_key(k);
+    if (!by_score || k <= kOff) return v;
+    return a.sigmoid ? sigmoid(v) : expf(__fsub_rn(v, best));
+  };
 
-  uint32_t mine = 0;
+  if (a.groups > 1 && a.group_shift < 0) {
+    // groups that cut through lanes: through shared memory, 2^shift lanes scan a group
+    float* val = shared + warp * a.experts;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) mine = max(mine, key[i]);
-  int id = -1;  // lane j: pick j
-  for (int j = 0; j < a.top_k; ++j) {
-    const uint32_t top = __reduce_max_sync(kAll, mine);
-    if (top == 0) break;
-    const int who = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-    int e = 0;
-    if (lane == who) {
-      bool found = false;
-      mine = 0;
+    for (int i = 0; i < VPT; ++i)
+      if (e0 + i < a.experts) val[e0 + i] = value(key[i]);
+    __syncwarp();
+    const int n = a.group_size;
+    int shift = 5;
+    while (a.groups << shift > 32) --shift;
+    float one = -INFINITY, two = -INFINITY;
+    if (lane >> shift < a.groups)
+      for (int i = lane & ((1 << shift) - 1); i < n; i += 1 << shift) merge_two(one, two, val[(lane >> shift) * n + i], -INFINITY);
+    const uint32_t keep = kept_groups(one, two, shift, lane, a);
+    int g = e0 / n, left = n - e0 % n;  // the group of expert e0 + i, and its experts from there on
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (!found && key[i] == top) {
-          found = true;
-          e = lane * VPT + i;
-          key[i] = 0;
-        }
-        mine = max(mine, key[i]);
+    for (int i = 0; i < VPT; ++i) {
+      if (!(keep >> (g << shift & 31) & 1u)) key[i] = kOff;
+      if (--left == 0) {
+        ++g;
+        left = n;
       }
     }
-    e = __shfl_sync(kAll, e, who);
-    if (lane == j) id = e;
   }
+  Two b = best_two<VPT>(key, e0);
+  if (a.groups > 1 && a.group_shift >= 0) {
+    const uint32_t keep = kept_groups(value(b.k1), value(b.k2), a.group_shift, lane, a);
+    if (!(keep >> (lane & -1 << a.group_shift) & 1u)) b.k1 = kOff;
+  }
+
+  int* pick = picks[warp];
+  int j = 0;
+  uint32_t last = 0;  // this lane's last pick
+  int last_e = 0;
+  while (j < a.top_k) {
+    const uint32_t top = __reduce_max_sync(kAll, b.k1);
+    if (top - kOff - 1 >= kLook - kOff - 1) {
+      if (top <= kOff) break;
+      if (b.k1 == kLook) {  // the best key behind the lane's last pick
+        b.k1 = kOff;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const bool behind = key[i] < last || (key[i] == last && e0 + i > last_e);
+          if (behind && key[i] > b.k1) {
+            b.k1 = key[i];
+            b.e1 = e0 + i;
+          }
+        }
+      }
+      continue;
+    }
+    if (lowest(__ballot_sync(kAll, b.k1 == top)) == 1u << lane) {
+      pick[j] = last_e = b.e1;
+      last = b.k1;
+      b.k1 = b.k2;
+      b.e1 = b.e2;
+      b.k2 = kLook;
+    }
+    ++j;
+  }
+  __syncwarp();
+  const int id = lane < j ? pick[lane] : -1;
   float w = 0.f;
   if (id >= 0) {
     const float v = to_f32(row[id]);
@@ -255,6 +314,14 @@ purlin_status with_vpt(int experts, F f) {
   return f(std::integral_constant<int, 32>());
 }
 
+// 2^shift lanes hold a group of n experts, or -1 where a group's end cuts a lane.
+int shift_of(int n, int vpt) {
+  if (n % vpt) return -1;
+  for (int s = 0; s <= 5; ++s)
+    if (n / vpt == 1 << s) return s;
+  return -1;
+}
+
 template <typename T, int VPT>
 int vec_ok(const RouteArgs& a) {
   const int need = std::min<int>(16, VPT * (int)sizeof(T));
@@ -263,11 +330,15 @@ int vec_ok(const RouteArgs& a) {
 
 }  // namespace
 
-purlin_status launch_route(const RouteArgs& a, int dtype, cudaStream_t s) {
-  const uint64_t grid = (a.tokens + kWarps - 1) / kWarps;
-  const size_t smem = a.groups > 1 ? (size_t)kWarps * a.experts * sizeof(float) : 0;  // at most 32 KiB
-  return with_vpt(a.experts, [&](auto v) {
+purlin_status launch_route(const RouteArgs& in, int dtype, cudaStream_t s) {
+  const uint64_t grid = (in.tokens + kWarps - 1) / kWarps;
+  return with_vpt(in.experts, [&](auto v) {
     constexpr int V = decltype(v)::value;
+    RouteArgs a = in;
+    a.group_size = a.experts / a.groups;
+    a.group_shift = shift_of(a.group_size, V);
+    // the groups' values, at most 32 KiB
+    const size_t smem = a.groups > 1 && a.group_shift < 0 ? (size_t)kWarps * a.experts * sizeof(float) : 0;
     if (dtype == PL_F32) return op_launch(route_kernel<float, V>, grid, kWarps * 32, smem, s, a, vec_ok<float, V>(a));
     return op_launch(route_kernel<bf16, V>, grid, kWarps * 32, smem, s, a, vec_ok<bf16, V>(a));
   });

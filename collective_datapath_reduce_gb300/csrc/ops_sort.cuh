@@ -2,28 +2,49 @@
 // of an expert exchange (one digit: the expert) and the embedding's gradient
 // (two or three digits of the token) share.
 //
-// A CTA of 32 warps takes a chunk of items; a warp takes a run of the chunk's
-// items in order, 32 at a time, so an item's place among its equals is: equals
-// in earlier chunks + in earlier warps + in earlier steps of its warp + in
-// lower lanes.  Lanes with equal digits find each other with one match; only
+// A CTA takes a chunk of items; a warp takes a run of the chunk's items in
+// order, 32 at a time, so an item's place among its equals is: equals in earlier
+// chunks + in earlier warps + in earlier steps of its warp + in lower lanes.
+// (The kernel that counts lets the one that places start at once; that one does
+// what needs no counts and then waits for them.  What it reads before is older
+// than the counting kernel, which lets it start only after its own op_wait.)  Lanes with equal digits find each other with one match; only
 // the lowest of them touches the warp's counter, so no atomics order anything.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "ops_common.cuh"
 
 namespace pl {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 512;    // of a chunk's CTA
 constexpr int kSortIpt = 8;          // items per thread, at most
 constexpr int kSortBins = 1024;      // bins of one digit, at most; one more for dropped items
-constexpr uint64_t kSortSmall = 8192;  // items that one CTA sorts by itself
 
-// Items of one CTA's chunk: 1024 for every started 152 x 1024, so that the
-// chunks fill the SMs once, up to 8192; more items take more chunks.
+// Up to kClusterSort items are sorted by one cluster in one launch: its CTAs
+// keep the items in shared memory and read each other's counts there.  More go
+// through two launches a digit, one that counts and one that places.  (One
+// digit of 65536 items with 257 bins takes 18 us by one cluster, 11 us in two
+// launches; 8192 items 5 us and 8 us.)
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterMost = 8;
+constexpr uint64_t kClusterSort = (uint64_t)kClusterThreads * kClusterMost * 2;
+
+// CTAs of the cluster and items per thread (powers of two) for n items: a CTA
+// for every started 1024 x each, then more items per thread.
+struct ClusterShape {
+  int ctas = 1, ipt = 1;
+  explicit ClusterShape(uint64_t n, int each = 2) {
+    while (ctas < kClusterMost && n > (uint64_t)ctas * each * kClusterThreads) ctas *= 2;
+    while (n > (uint64_t)ctas * ipt * kClusterThreads) ipt *= 2;
+  }
+};
+
+// Items of one CTA's chunk: 1024, or more where 152 x 1024 do not hold them,
+// so that the chunks fill the SMs once, up to 4096; then there are more chunks.
 inline uint64_t sort_chunk(uint64_t n) {
   const uint64_t per = (n + 152 * kSortThreads - 1) / (152 * kSortThreads);
-  return (uint64_t)kSortThreads * std::max<uint64_t>(1, std::min<uint64_t>(per, kSortIpt));
+  return (uint64_t)kSortThreads * std::max<uint64_t>(2, std::min<uint64_t>(per, kSortIpt));
 }
 inline uint64_t sort_chunks(uint64_t n) { return (n + sort_chunk(n) - 1) / sort_chunk(n); }
 
@@ -81,12 +102,19 @@ __device__ __forceinline__ void rank_chunk(const int (&digit)[kSortIpt], uint32_
     }
   }
   __syncthreads();
+  // eight counts of a bin are loaded before their sums are stored: one by one,
+  // each load would wait for the sum before it
   for (int b = threadIdx.x; b < bins; b += blockDim.x) {
     uint32_t sum = 0;
-    for (int w = 0; w < warps; ++w) {
-      const uint32_t c = cnt[w * bins + b];
-      cnt[w * bins + b] = (uint16_t)sum;
-      sum += c;
+    for (int w0 = 0; w0 < warps; w0 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = w0 + i < warps ? cnt[(w0 + i) * bins + b] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (w0 + i < warps) cnt[(w0 + i) * bins + b] = (uint16_t)sum;
+        sum += c[i];
+      }
     }
     each(b, sum);
   }
@@ -95,15 +123,15 @@ __device__ __forceinline__ void rank_chunk(const int (&digit)[kSortIpt], uint32_
 
 // Sums of the chunks' counts (rows of `bins` words, one per chunk): all[b] over
 // every chunk, before[b] over the chunks before this one.
-__device__ __forceinline__ void sum_chunks(const uint32_t* counts, uint32_t chunks, uint32_t chunk, int bins, uint32_t* all,
-                                           uint32_t* before) {
+__device__ __forceinline__ void sum_chunks(const uint32_t* counts, uint32_t chunks, uint32_t chunk, int bins,
+                                           uint32_t* all, uint32_t* before) {
   for (int b = threadIdx.x; b < bins; b += blockDim.x) all[b] = before[b] = 0;
   __syncthreads();
   const int parts = max(1, (int)blockDim.x / bins);
   const int part = threadIdx.x / bins;
   for (int b = threadIdx.x - part * bins; part < parts && b < bins; b += blockDim.x) {
     uint32_t s = 0, sb = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t c = part; c < chunks; c += parts) {
       const uint32_t v = __ldcg(counts + (uint64_t)c * bins + b);
       s += v;
@@ -113,6 +141,36 @@ __device__ __forceinline__ void sum_chunks(const uint32_t* counts, uint32_t chun
     atomicAdd(before + b, sb);
   }
   __syncthreads();
+}
+
+// base[b] = the first place of this CTA's items of bin b: items of lower bins in
+// the whole cluster, and those of bin b in the CTAs before.  `hist`: this CTA's
+// counts, at the same place in every CTA of the cluster.  total: all items.
+__device__ __forceinline__ uint32_t cluster_bases(uint32_t* hist, int bins, uint32_t* base, uint32_t* tmp) {
+  const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+  cluster.sync();
+  uint32_t carry = 0;
+  for (int b0 = 0; b0 < bins; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    uint32_t all = 0, before = 0;
+    if (b < bins) {
+      uint32_t v[kClusterMost];
+#pragma unroll
+      for (int r = 0; r < kClusterMost; ++r) v[r] = r < ctas ? cluster.map_shared_rank(hist, r)[b] : 0;
+#pragma unroll
+      for (int r = 0; r < kClusterMost; ++r) {
+        all += v[r];
+        before += r < me ? v[r] : 0;
+      }
+    }
+    uint32_t total;
+    const uint32_t at = carry + block_exclusive(all, tmp, &total);
+    if (b < bins) base[b] = at + before;
+    carry += total;
+  }
+  __syncthreads();
+  return carry;
 }
 
 }  // namespace pl

@@ -222,7 +222,8 @@ def test_route_gradient(h, T, E, k, pad, kind, renormalise, dtype):
 # ------------------------------------------------------------------ exchange
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 32, 1024), (5, 3, 2), (17, 8, 128), (1000, 8, 7),
-                                   (1024, 8, 256), (8193, 1, 64), (1025, 8, 1024), (20000, 8, 256), (200003, 6, 33)])
+                                   (1024, 8, 256), (8193, 1, 64), (1025, 8, 1024), (20000, 8, 256), (200003, 6, 33),
+                                   (2048, 1, 16), (2049, 1, 16), (4097, 1, 1024), (32768, 2, 100), (65537, 1, 100)])
 def test_plan(h, T, k, E):
     rng = np.random.default_rng(T + k)
     ids = rng.integers(-1, E + 2, (T, k)) if E > 1 else rng.integers(0, 2, (T, k))
@@ -372,6 +373,8 @@ GRADS = [
     (4097, 3000, 16, 0, 0, -7, "hot"), (8192, 100, 8, 0, 0, 0, "any"), (8193, 100, 8, 0, 0, 0, "any"),
     (9000, 2, 24, 0, 0, 0, "one"), (20000, 70000, 8, 0, 0, 0, "hot"), (8200, 1300000, 2, 0, 0, 0, "any"),
     (300, 1100000, 4, 0, 0, 0, "any"), (200, 64, 1100, 0, 0, 0, "outside"), (170000, 900, 4, 0, 0, 0, "hot"),
+    (2048, 3000, 4, 0, 0, 0, "any"), (2049, 3000, 4, 0, 0, 0, "hot"), (65536, 700, 4, 0, 0, 0, "hot"),
+    (65537, 70000, 4, 0, 0, 0, "hot"), (40, 600000, 3, 1, 0, 0, "any"), (0, 100, 48, 0, 0, 0, "any"),
 ]
 
 
@@ -589,7 +592,8 @@ def test_refusals_on_the_gpu(h):
     purlin.clip_grad_norm([flat[:50], flat[:50]], [f(50), f(50)], 1.0, f(1), h)            # reads may share
     s = torch.cuda.current_stream().cuda_stream
     # workspaces too small, misaligned pointers, unknown handle
-    assert P.purlin_expert_plan(h.raw, i(9000, 1), 9000, 1, 8, i(9), i(9000, 1), None, 0, s) == P.PL_ERR_WORKSPACE
+    assert P.purlin_expert_plan_bytes(90000, 1, 8) > 0
+    assert P.purlin_expert_plan(h.raw, i(90000, 1), 90000, 1, 8, i(9), i(90000, 1), None, 0, s) == P.PL_ERR_WORKSPACE
     assert P.purlin_embed_grad(h.raw, x, 16, P.PL_F32, i(8), 4, 8, 16, 1.0, None, 0, f(8, 16), 16, P.PL_F32, 8, 0, None, 0,
                                s) == P.PL_ERR_WORKSPACE
     assert P.purlin_clip_grad_norm(h.raw, [x], None, [8], P.PL_F32, 1.0, 1.0, f(1), None, 0, s) == P.PL_ERR_WORKSPACE
