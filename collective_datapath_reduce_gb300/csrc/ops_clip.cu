@@ -2,8 +2,15 @@
 //
 // The first kernel leaves each CTA's sum of squares; the second adds them in a
 // fixed order in every CTA (so all agree, and from call to call), derives the
-// factor and writes.  Squares are added in binary32 over a few vectors of one
-// thread and from there on in binary64.
+// factor and writes.  Few elements go through one CTA of one kernel.  Squares
+// are added in binary32 over a few vectors of one thread and from there on in
+// binary64.
+//
+// Past the L2 the values have to be read twice and written once: 238 M binary32
+// values in 180 tensors take 147 + 287 us, 6.5 and 6.6 TB/s.  Shares in one
+// piece for each CTA (300 us), evict-first stores (295 us) and the opposite
+// order (291 us) were no faster in the second kernel; in the first one, shares in
+// one piece beat strided ones (163 us) because a share looks its tensor up once.
 #include <math.h>
 
 #include <type_traits>
@@ -41,92 +48,130 @@ __device__ __forceinline__ int tensor_of(const Table<M>& a, uint32_t chunk) {
   return lo;
 }
 
-// Calls vec(first element) for the 16-byte vectors and one(element) for the
-// others of elements [e0, e1) at p; `q` shares p's alignment or vec is not used.
-template <typename T, typename V, typename O>
+// CTA b's pieces are share(b) .. share(b + 1): neighbours, so that the tensor
+// is looked up once and then followed.
+__device__ __forceinline__ uint32_t share(uint32_t chunks, uint32_t b) {
+  return (uint32_t)((uint64_t)chunks * b / gridDim.x);
+}
+
+// Runs vec(vector, first element, whether there is one) for the 16-byte vectors
+// of elements [e0, e1) at p, F of a thread in flight at a time, and one(element)
+// for the elements beside them.
+template <int THREADS, int F, typename T, typename V, typename O>
 __device__ __forceinline__ void walk(const T* p, bool aligned, uint64_t e0, uint64_t e1, V vec, O one) {
   constexpr int N = 16 / sizeof(T);
+  const uint32_t tid = threadIdx.x % THREADS;
   if (!aligned) {
-    for (uint64_t i = e0 + threadIdx.x; i < e1; i += kThreads) one(i);
+    for (uint64_t i = e0 + tid; i < e1; i += THREADS) one(i);
     return;
   }
   const uint64_t off = ((uintptr_t)(p + e0) & 15) / sizeof(T);
   const uint64_t v0 = min(e1, off ? e0 + N - off : e0);
-  const uint64_t v1 = v0 + (e1 - v0) / N * N;
-  for (uint64_t i = v0 + (uint64_t)threadIdx.x * N; i < v1; i += (uint64_t)kThreads * N) vec(i);
-  if (threadIdx.x < N && e0 + threadIdx.x < v0) one(e0 + threadIdx.x);
-  if (threadIdx.x < N && v1 + threadIdx.x < e1) one(v1 + threadIdx.x);
+  const uint32_t nv = (uint32_t)((e1 - v0) / N);
+  for (uint32_t v = tid; v < nv; v += THREADS * F) {
+    Pack<T, N> x[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u) x[u] = ld_pack_if<T, N>(p + v0 + (uint64_t)(v + u * THREADS) * N, v + u * THREADS < nv);
+#pragma unroll
+    for (int u = 0; u < F; ++u) pin(x[u]);
+#pragma unroll
+    for (int u = 0; u < F; ++u) vec(x[u], v0 + (uint64_t)(v + u * THREADS) * N, v + u * THREADS < nv);
+  }
+  const uint64_t v1 = v0 + (uint64_t)nv * N;
+  if (tid < N && e0 + tid < v0) one(e0 + tid);
+  if (tid < N && v1 + tid < e1) one(v1 + tid);
 }
 
+// Squares of elements [e0, e1) at p, this thread's part.
+template <int THREADS, int F, typename T>
+__device__ __forceinline__ float squares(const T* p, uint64_t e0, uint64_t e1) {
+  float s = 0.f;
+  walk<THREADS, F, T>(
+      p, true, e0, e1,
+      [&](const auto& x, uint64_t, bool) {  // zeros where there is none
+#pragma unroll
+        for (int k = 0; k < 16 / (int)sizeof(T); ++k) s = __fmaf_rn(to_f32(x.v[k]), to_f32(x.v[k]), s);
+      },
+      [&](uint64_t i) { s = __fmaf_rn(to_f32(p[i]), to_f32(p[i]), s); });
+  return s;
+}
+
+// In place, an element is loaded and stored by the same thread, and by no other.
+template <int THREADS, int F, typename T>
+__device__ __forceinline__ void scale(const T* p, T* o, uint64_t e0, uint64_t e1, float f) {
+  walk<THREADS, F, T>(
+      p, (((uintptr_t)p ^ (uintptr_t)o) & 15) == 0, e0, e1,
+      [&](auto& x, uint64_t i, bool on) {
+#pragma unroll
+        for (int k = 0; k < 16 / (int)sizeof(T); ++k) x.v[k] = from_f32<T>(to_f32(x.v[k]) * f);
+        if (on) st_pack_once(o + i, x);
+      },
+      [&](uint64_t i) { o[i] = from_f32<T>(to_f32(p[i]) * f); });
+}
+
+// Sum over the CTA, the same in every thread.  Binary64 additions are slow
+// here, so they are few in a row: by lanes, then by warps.
+template <int THREADS>
 __device__ __forceinline__ double block_sum(double s, double* tmp) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) tmp[threadIdx.x / 32] = s;
   __syncthreads();
-  s = 0.0;
+  constexpr int W = THREADS / 32;
+  s = tmp[threadIdx.x % W];
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += tmp[w];
+  for (int d = W / 2; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   return s;
 }
 
-template <typename T, int M>
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<M> a) {
-  op_wait();
-  __shared__ double tmp[kThreads / 32];
-  constexpr int N = 16 / sizeof(T);
-  double sum = 0.0;
-  for (uint32_t c = blockIdx.x; c < a.first[a.n]; c += gridDim.x) {
-    const int t = tensor_of(a, c);
-    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk, e1 = min(a.t[t].n, e0 + kChunk);
-    const T* p = (const T*)a.t[t].in;
-    float s = 0.f;
-    walk<T>(
-        p, true, e0, e1,
-        [&](uint64_t i) {
-          const Pack<T, N> x = ld_pack<T, N>(p + i);
-#pragma unroll
-          for (int k = 0; k < N; ++k) s = __fmaf_rn(to_f32(x.v[k]), to_f32(x.v[k]), s);
-        },
-        [&](uint64_t i) { s = __fmaf_rn(to_f32(p[i]), to_f32(p[i]), s); });
-    sum += (double)s;
-  }
-  sum = block_sum(sum, tmp);
-  if (threadIdx.x == 0) a.parts[a.part0 + blockIdx.x] = sum;
-}
-
-// norm and factor, by every CTA alike
+// The factor, given the sum of squares; one thread writes the norm.
 template <int M>
-__device__ __forceinline__ float factor_of(const Table<M>& a, double* tmp, bool tell) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.nparts; i += kThreads) s += a.parts[i];
-  const float norm = (float)(sqrt(block_sum(s, tmp)) * fabs((double)a.scale));
-  if (tell && threadIdx.x == 0) *a.norm = norm;
+__device__ __forceinline__ float factor_of(const Table<M>& a, double sum, bool tell) {
+  // binary64 square roots take long: only where the sum is outside binary32
+  const float root = sum > 1e-30 && sum < 1e38 ? __fsqrt_rn((float)sum) : (float)sqrt(sum);
+  const float norm = root * fabsf(a.scale);
+  if (tell) *a.norm = norm;
   if (isinf(a.max_norm)) return a.scale;
   const float f = __fdiv_rn(a.max_norm, norm + 1e-6f);
   return (f < 1.f || isnan(f) ? f : 1.f) * a.scale;
 }
 
+template <int M>
+__device__ __forceinline__ double sum_of_parts(const Table<M>& a, double* tmp) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < a.nparts; i += kThreads) s += a.parts[i];
+  return block_sum<kThreads>(s, tmp);
+}
+
 template <typename T, int M>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<M> a) {
+__global__ void __launch_bounds__(kThreads, 2) squares_kernel(const __grid_constant__ Table<M> a) {
   op_wait();
   __shared__ double tmp[kThreads / 32];
-  constexpr int N = 16 / sizeof(T);
-  const float f = factor_of(a, tmp, a.part0 == 0 && blockIdx.x == 0);
-  for (uint32_t c = blockIdx.x; c < a.first[a.n]; c += gridDim.x) {
+  double sum = 0.0;
+  const uint32_t chunks = a.first[a.n];
+  const uint32_t c0 = share(chunks, blockIdx.x), c1 = share(chunks, blockIdx.x + 1);
+  int t = tensor_of(a, c0);
+  for (uint32_t c = c0; c < c1; ++c) {
+    while (c >= a.first[t + 1]) ++t;
+    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk;
+    sum += (double)squares<kThreads, 8>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kChunk));
+  }
+  sum = block_sum<kThreads>(sum, tmp);
+  if (threadIdx.x == 0) a.parts[a.part0 + blockIdx.x] = sum;
+}
+
+template <typename T, int M>
+__global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constant__ Table<M> a) {
+  op_wait();
+  __shared__ double tmp[kThreads / 32];
+  const float f = factor_of(a, sum_of_parts(a, tmp), a.part0 == 0 && blockIdx.x == 0 && threadIdx.x == 0);
+  const uint32_t chunks = a.first[a.n];
+  for (uint32_t d = blockIdx.x; d < chunks; d += gridDim.x) {
+    const uint32_t c = chunks - 1 - d;  // the end first: what was read last may still be in the L2
     const int t = tensor_of(a, c);
-    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk, e1 = min(a.t[t].n, e0 + kChunk);
-    const T* p = (const T*)a.t[t].in;
-    T* o = (T*)a.t[t].out;
-    walk<T>(
-        p, (((uintptr_t)p ^ (uintptr_t)o) & 15) == 0, e0, e1,
-        [&](uint64_t i) {
-          Pack<T, N> x = *reinterpret_cast<const Pack<T, N>*>(p + i);
-#pragma unroll
-          for (int k = 0; k < N; ++k) x.v[k] = from_f32<T>(to_f32(x.v[k]) * f);
-          st_pack<T, N>(o + i, x);
-        },
-        [&](uint64_t i) { o[i] = from_f32<T>(to_f32(p[i]) * f); });
+    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk;
+    scale<kThreads, 8>((const T*)a.t[t].in, (T*)a.t[t].out, e0, min(a.t[t].n, e0 + kChunk), f);
   }
 }
 
@@ -134,10 +179,32 @@ template <int M>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<M> a) {
   op_wait();
   __shared__ double tmp[kThreads / 32];
-  factor_of(a, tmp, true);
+  factor_of(a, sum_of_parts(a, tmp), threadIdx.x == 0);
 }
 
-uint64_t chunks_of(uint64_t n) { return (n + kChunk - 1) / kChunk; }
+// Few elements: one CTA, a warp for each piece of kSmallChunk elements.
+constexpr int kSmallThreads = 1024;
+constexpr uint64_t kSmallChunk = 1024, kSmallMost = 64 * 1024;
+template <typename T>
+__global__ void __launch_bounds__(kSmallThreads) clip_small_kernel(const __grid_constant__ Table<kFew> a, int write) {
+  op_wait();
+  __shared__ double tmp[kSmallThreads / 32];
+  constexpr int F = kSmallChunk * sizeof(T) / (32 * 16);  // a piece in one go
+  const uint32_t chunks = a.first[a.n], warp = threadIdx.x / 32;
+  double sum = 0.0;
+  for (uint32_t c = warp; c < chunks; c += kSmallThreads / 32) {
+    const int t = tensor_of(a, c);
+    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kSmallChunk;
+    sum += (double)squares<32, F>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kSmallChunk));
+  }
+  sum = block_sum<kSmallThreads>(sum, tmp);
+  const float f = factor_of(a, sum, threadIdx.x == 0);
+  for (uint32_t c = warp; write && c < chunks; c += kSmallThreads / 32) {
+    const int t = tensor_of(a, c);
+    const uint64_t e0 = (uint64_t)(c - a.first[t]) * kSmallChunk;
+    scale<32, F>((const T*)a.t[t].in, (T*)a.t[t].out, e0, min(a.t[t].n, e0 + kSmallChunk), f);
+  }
+}
 
 template <typename T, int M>
 purlin_status clip_t(const ClipTensor* t, size_t n, float scale, float max_norm, bool write, float* norm, double* partials,
@@ -152,17 +219,26 @@ purlin_status clip_t(const ClipTensor* t, size_t n, float scale, float max_norm,
   a.scale = scale;
   a.max_norm = max_norm;
   a.norm = norm;
+  uint64_t elements = 0;
+  for (size_t i = 0; i < n; ++i) elements += t[i].n;
+  const bool small = M == kFew && elements <= kSmallMost;
+  const uint64_t piece = small ? kSmallChunk : kChunk;
   auto fill = [&](size_t l) {
     a.n = (int)std::min<size_t>(M, n - l * M);
     uint64_t c = 0;
     for (int i = 0; i < a.n; ++i) {
       a.t[i] = t[l * M + i];
       a.first[i] = (uint32_t)c;
-      c += chunks_of(a.t[i].n);  // far below 2^32 for any memory
+      c += (a.t[i].n + piece - 1) / piece;  // far below 2^32 for any memory
     }
     a.first[a.n] = (uint32_t)c;
     return c;
   };
+  if constexpr (M == kFew)
+    if (small) {
+      fill(0);
+      return op_launch(clip_small_kernel<T>, 1, kSmallThreads, 0, s, a, (int)write);
+    }
   int parts = 0;
   for (size_t l = 0; l < launches; ++l) {
     const uint64_t c = fill(l);

@@ -10,6 +10,7 @@ library has not been built, loading it raises: there is no other code path.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -125,7 +126,7 @@ _SIGNATURES = {
     "purlin_embed_grad": (_i, [_vp, _vp, _sz, _i, _vp, _i, _sz, _sz, ctypes.c_float, _vp, _sz, _vp, _sz, _i, _sz,
                                ctypes.c_int64, _vp, _sz, _vp]),
     "purlin_clip_grad_norm_bytes": (_sz, []),
-    "purlin_clip_grad_norm": (_i, [_vp, _PP, _PP, _SZP, _sz, _i, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "purlin_clip_grad_norm": (_i, [_vp, _vp, _vp, _vp, _sz, _i, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -351,9 +352,18 @@ def purlin_clip_grad_norm_bytes() -> int:
 def purlin_clip_grad_norm(h, grads, outs, counts, dtype, scale, max_norm, norm, workspace, workspace_bytes,
                           stream=None) -> int:
     """outs: one buffer per gradient, or None for the norm alone."""
-    return load().purlin_clip_grad_norm(h, _ptr_array(grads), None if outs is None else _ptr_array(outs),
-                                        _size_array(counts), len(grads), dtype, scale, max_norm, _addr(norm),
-                                        _addr(workspace), workspace_bytes, _stream(stream))
+    n = len(grads)
+    if n != len(counts) or (outs is not None and n != len(outs)):
+        return PL_ERR_INVALID_ARG
+    # one array of 64-bit words for all three: a ctypes array's type is made anew for every length
+    words = [_addr(g) for g in grads]
+    words += counts
+    if outs is not None:
+        words += words[:n] if outs is grads else [_addr(o) for o in outs]
+    words = array.array("Q", words)
+    at = words.buffer_info()[0]
+    return load().purlin_clip_grad_norm(h, at, None if outs is None else at + 16 * n, at + 8 * n, n, dtype, scale,
+                                        max_norm, _addr(norm), _addr(workspace), workspace_bytes, _stream(stream))
 
 
 def purlin_status_get(h, stream=None):

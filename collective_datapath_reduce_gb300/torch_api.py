@@ -33,6 +33,7 @@ _DTYPES = {torch.float32: P.PL_F32, torch.bfloat16: P.PL_BF16}
 class Handle:
     def __init__(self, raw, world, device):
         self.raw, self.world, self.device = raw, world, device
+        self.workspaces = {}  # of the operators, by stream
 
     def __repr__(self):
         return f"purlin.Handle(world={self.world}, device={self.device})"
@@ -115,6 +116,7 @@ def initialize(world: int, device=None, stream=None) -> Handle:
 def finalize(handle: Handle, stream=None) -> None:
     st = P.purlin_finalize(handle.raw, _stream(stream, handle.device))
     handle.raw = None
+    handle.workspaces.clear()
     _check(st, "finalize")
 
 
@@ -197,8 +199,8 @@ def reduce_scatter_v(xs, outs, counts, handle: Handle, stream=None, reduction_mo
 #
 # Outputs are the caller's, as for the collectives.  Matrices are 2-D tensors
 # whose rows are packed (the last stride is 1) and any stride apart; vectors,
-# picks and places are contiguous.  Workspaces come from torch's allocator, on
-# the stream that the call runs on.
+# picks and places are contiguous.  Workspaces come from torch's allocator and
+# are kept by the handle, one for each stream.
 
 def _values(t, what):
     dt = _DTYPES.get(t.dtype)
@@ -245,17 +247,24 @@ def _two(t, what, name):
     return t.shape
 
 
-def _workspace(nbytes, stream, device):
-    """nbytes of device memory that later work on the call's stream may reuse
-    (torch's allocator hands a block on only in the order of its own stream)."""
+def _workspace(nbytes, stream, handle):
+    """At least nbytes of device memory for a call on `stream`.  The handle keeps
+    one block for each stream, used by that stream's calls one after the other;
+    it comes from torch's allocator on the same stream, so a block that is
+    replaced by a larger one is not handed on before its calls are done.  A
+    captured graph gets a block of its own, since it may replay anywhere."""
     if nbytes == 0:
         return None
-    if stream is None:
+    device = handle.device
+    if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    key = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device)
+    kept = handle.workspaces.get(key)
+    if kept is None or kept.numel() < nbytes:
+        with torch.cuda.stream(torch.cuda.ExternalStream(key, device=device)):
+            kept = handle.workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return kept
 
 
 def _call(fn, what, handle, stream, *args):
@@ -327,7 +336,7 @@ def expert_plan(ids, offsets, places, handle: Handle, stream=None):
     _packed(places, (T, k), torch.int32, what, "places")
     _packed(offsets, (E + 1,), torch.int32, what, "offsets")
     nbytes = P.purlin_expert_plan_bytes(T, k, E)
-    ws = _workspace(nbytes, stream, handle.device)
+    ws = _workspace(nbytes, stream, handle)
     _call(P.purlin_expert_plan, what, handle, stream, ids, T, k, E, offsets, places, ws, nbytes)
 
 
@@ -408,7 +417,7 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
     ldt = _matrix(grad_table, R, D, grad_table.dtype, what, "grad_table")
     ldb = _matrix(base, R, D, grad_table.dtype, what, "base") if base is not None else 0
     nbytes = P.purlin_embed_grad_bytes(n, R, D)
-    ws = _workspace(nbytes, stream, handle.device)
+    ws = _workspace(nbytes, stream, handle)
     _call(P.purlin_embed_grad, what, handle, stream, grad_out, ldx, dx, tokens, size, n, D, scale, base, ldb, grad_table,
           ldt, dt, R, int(first), ws, nbytes)
 
@@ -424,14 +433,15 @@ def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, strea
         raise ValueError(f"{what}: expected {len(grads)} outputs, got {len(outs)}")
     dt, counts = P.PL_F32, [t.numel() for t in grads]
     if counts:
+        dtype = grads[0].dtype
         dt = _values(grads[0], what)
-        kinds = {(t.dtype, t.is_cuda or t.is_pinned(), t.is_contiguous()) for t in grads}
-        if outs is not None and outs is not grads:
-            kinds |= {(t.dtype, t.is_cuda or t.is_pinned(), t.is_contiguous()) for t in outs}
-            if [t.numel() for t in outs] != counts:
-                raise ValueError(f"{what}: each output must have its gradient's size")
-        if kinds != {(grads[0].dtype, True, True)}:
-            raise ValueError(f"{what}: gradients and outputs must be contiguous CUDA (or pinned host) tensors of one dtype")
+        # where each tensor lives is checked by the library, for all of them
+        for side in (grads,) if outs is None or outs is grads else (grads, outs):
+            for t in side:
+                if t.dtype is not dtype or not t.is_contiguous():
+                    raise ValueError(f"{what}: gradients and outputs must be contiguous tensors of one dtype")
+        if outs is not None and outs is not grads and [t.numel() for t in outs] != counts:
+            raise ValueError(f"{what}: each output must have its gradient's size")
     nbytes = P.purlin_clip_grad_norm_bytes()
-    ws = _workspace(nbytes, stream, handle.device)
+    ws = _workspace(nbytes, stream, handle)
     _call(P.purlin_clip_grad_norm, what, handle, stream, grads, outs, counts, dt, scale, max_norm, norm, ws, nbytes)
