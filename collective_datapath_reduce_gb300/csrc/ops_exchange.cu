@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kSortThreads) plan_place_kernel(const __grid_c
     if (q < ipt) digit[q] = expert_of(a.ids, i0 + (uint64_t)(warp * ipt + q) * 32 + lane, a.slots, a.experts);
   rank_chunk(digit, local, ipt, a.experts + 1, cnt, [](int, uint32_t) {});
   op_wait();
+  op_next();
   sum_chunks(a.counts, gridDim.x, blockIdx.x, a.experts, base, before);
   uint32_t carry = 0, earlier = 0;  // picks with an expert: all, and those of earlier chunks
   for (int b0 = 0; b0 < a.experts; b0 += blockDim.x) {
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kSortThreads) plan_place_kernel(const __grid_c
 // All places, by one cluster.
 __global__ void __launch_bounds__(kClusterThreads) plan_cluster_kernel(const __grid_constant__ PlanArgs a, int ipt) {
   op_wait();
+  op_next();
   extern __shared__ uint16_t cnt[];
   __shared__ uint32_t hist[kSortBins + 1], base[kSortBins + 1], tmp[33];
   const int bins = a.experts + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

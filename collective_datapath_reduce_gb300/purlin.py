@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import os
 import re
 
@@ -192,11 +193,10 @@ def declared_symbols() -> list[str]:
 # ------------------------------------------------------------- marshalling
 
 def _addr(x) -> int:
-    if x is None:
-        return 0
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return 0 if x is None else int(x)
 
 
 def _stream(s):
@@ -283,8 +283,10 @@ def purlin_all_reduce_noalloc(world, src, dst, bytes_per_rank, dtype, device_sta
                                             _addr(device_status) or None, _stream(stream))
 
 
+@functools.lru_cache(maxsize=256)
 def make_routing(experts, top_k, scores=PL_SCORES_SOFTMAX, groups=1, kept_groups=1, group_best=1, renormalise=True,
                  scale=1.0) -> purlin_routing:
+    """The C struct; one for all calls with the same arguments, so not to be written to."""
     return purlin_routing(experts, top_k, int(scores), groups, kept_groups, group_best, int(renormalise), scale)
 
 
