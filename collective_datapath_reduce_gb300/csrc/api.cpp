@@ -769,7 +769,7 @@ const char* purlin_status_string(purlin_status s) {
     case PL_ERR_LAUNCH: return "kernel launch failed";
     case PL_ERR_TIMEOUT: return "a SNAC wait on the device ran out of time";
     case PL_ERR_FINALIZED: return "handle already finalized";
-    case PL_ERR_BOUNDS: return "a work item reached outside a rank buffer (checking build)";
+    case PL_ERR_BOUNDS: return "a place outside an operator's rows, or (checking build) a work item outside a rank buffer";
   }
   return "unknown status";
 }

@@ -2,7 +2,7 @@
 // the launch functions of ops_*.cu.
 #include <algorithm>
 #include <cmath>
-#include <new>
+#include <exception>
 #include <vector>
 
 #include "ops.h"
@@ -399,7 +399,7 @@ purlin_status purlin_clip_grad_norm(purlin_handle handle, const void* const* gra
     }
     return pl::launch_clip(t.data(), t.size(), dtype, scale, max_norm, outs != nullptr, (float*)const_cast<void*>(nq),
                            (double*)const_cast<void*>(wq), h.sm_count, (cudaStream_t)stream);
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {  // no memory for so many gradients
     return PL_ERR_INVALID_ARG;
   }
 }

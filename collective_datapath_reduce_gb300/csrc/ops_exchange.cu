@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_cons
             st_pack_once<T, V>(y + c.head + v * V, ld_row_if<T, true>(x[u] + c.head + v * V, p >= 0));
           } else {
             const uint64_t e = c.at<V>((uint32_t)(v - c.nv));
-            y[e] = from_f32<T>(ld1_if(x[u] + e, p >= 0));
+            y[e] = p >= 0 ? x[u][e] : from_f32<T>(0.f);
           }
         }
       }

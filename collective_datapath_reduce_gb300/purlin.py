@@ -193,10 +193,11 @@ def declared_symbols() -> list[str]:
 # ------------------------------------------------------------- marshalling
 
 def _addr(x) -> int:
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        return 0 if x is None else int(x)
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    return x.data_ptr()
 
 
 def _stream(s):

@@ -424,8 +424,9 @@ purlin_status purlin_embed_grad(purlin_handle h, const void* grad_out, size_t gr
  * + 1e-6)).  outs NULL: the norm alone.  outs[i] may be grads[i].  max_norm +inf
  * never clips.  A norm that is not finite follows the formula: infinite, the
  * factor is 0; NaN, every output is NaN.  Squares are added in binary32 within
- * a thread's share of 16384 elements and in binary64 from there.  grads, outs
- * and counts are host arrays, read during the call.  The workspace is 8-byte
+ * a thread's share of 16384 elements (in binary64 where they overflow it; those
+ * below its range count as 0) and in binary64 from there.  grads, outs and
+ * counts are host arrays, read during the call.  The workspace is 8-byte
  * aligned. */
 size_t purlin_clip_grad_norm_bytes(void);
 purlin_status purlin_clip_grad_norm(purlin_handle h, const void* const* grads, void* const* outs, const size_t* counts,

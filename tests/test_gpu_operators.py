@@ -284,6 +284,16 @@ def test_dispatch_and_combine(h, T, k, D, pad, off, dtype):
     assert dr.intact() and dw.intact()
 
 
+@pytest.mark.parametrize("D", [64, 67])
+def test_dispatch_copies_every_bit_pattern(h, D):
+    bits = torch.randint(-2**15, 2**15, (9, D), dtype=torch.int32, device=DEV).to(torch.int16)   # NaN payloads among them
+    places = O.plan(np.tile(np.arange(3), (9, 1)), 3)[1]
+    rows = torch.empty(27, D, dtype=torch.bfloat16, device=DEV)
+    purlin.dispatch_rows(bits.view(torch.bfloat16), ints(places), rows, h)
+    want = O.dispatch(bits.cpu().numpy(), places)
+    assert np.array_equal(rows.view(torch.int16).cpu().numpy(), want)
+
+
 def test_combine_with_a_weight_of_infinity_stays_in_its_row(h):
     places = ints(O.plan(np.array([[0], [1], [2]]), 3)[1])
     rows = torch.ones(3, 8, device=DEV)
@@ -468,6 +478,20 @@ def test_clip_of_nothing(h):
     z = [torch.zeros(100, device=DEV)]
     purlin.clip_grad_norm(z, z, 1.0, norm, h)
     assert norm.item() == 0.0 and (z[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_clip_of_values_whose_squares_overflow(h, dtype):
+    """The squares pass binary32, the norm does not."""
+    rng = np.random.default_rng(1)
+    for n in (100, 200000):
+        g, v = make(rng.standard_normal((1, n)) * 1e30, dtype)
+        norm, out = torch.empty(1, device=DEV), Guarded(1, n, dtype)
+        purlin.clip_grad_norm([g[0]], [out.view[0]], 1.0, norm, h)
+        want, want_norm = O.clip([v[0]], 1.0)
+        assert abs(norm.item() - want_norm) <= want_norm * 4 * E24     # all in 64 bits, rounded to 32
+        # the factor is 1 / norm, near 1e-33, and a product near 1e-3 rounds like any
+        close(out.view[0], want[0], np.abs(want[0]) * (U[dtype] + 12 * E24))
 
 
 def test_clip_with_values_that_are_not_finite(h):
