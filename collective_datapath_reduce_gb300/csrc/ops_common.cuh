@@ -238,13 +238,6 @@ __device__ __forceinline__ Pack<T, N> zero_pack() {
 
 __device__ __forceinline__ void op_status(uint32_t* status, uint32_t what) { atomicCAS(status, 0u, what); }
 
-// Widest access (16, 8, 4, 2 bytes) that divides every address and byte
-// count or stride or-ed into `bits`.
-inline int vec_bytes(uint64_t bits) {
-  const uint64_t low = bits & (~bits + 1);
-  return low == 0 || low > 16 ? 16 : (int)low;
-}
-
 constexpr int kRowThreads = 256;
 
 // Groups of threads that cover a row of nv vectors in the fewest rounds of at

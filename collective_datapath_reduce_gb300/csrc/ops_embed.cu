@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(kRowThreads) embed_kernel(const __grid_constan
 
 // ------------------------------------------------------- sort of the tokens
 
+// A whole number of T's size: rows that are copied or cleared, whatever they hold.
+template <typename T>
+using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+
 // One digit of the sort: (key, index) pairs, or the tokens themselves when
 // in_key is null.  Keys are rows of the table; rows = outside, sorted last.
 struct SortArgs {
@@ -175,30 +179,34 @@ __device__ __forceinline__ void cluster_sort(const SortArgs& a, int ipt, char* s
   }
 }
 
-// Row r of the table's gradient where no token names it: zero, or the base's,
-// by `lanes` threads in vectors of B bytes.
-template <int B>
-__device__ __forceinline__ void fill_row(const EmbedArgs& a, int elem, uint64_t r, int lane, int lanes) {
-  using W = uint16_t;
-  char* y = (char*)a.y + r * a.ldy * elem;
-  const char* b = (const char*)a.base + r * a.ldb * elem;
-  const uint64_t nv = a.width * elem / B;
+// Row r of the table's gradient where no token names it: zero, or the base's
+// bits, by `lanes` threads.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void fill_row(const EmbedArgs& a, uint64_t r, int lane, int lanes) {
+  constexpr int V = V16<T>;
+  T* y = (T*)a.y + r * a.ldy;
+  const T* b = (const T*)a.base + r * a.ldb;
+  const Cut c = cut_of<T, SHIFT>(y, a.width);
   if (!a.base) {
-    for (uint64_t v = lane; v < nv; v += lanes) st_pack_once<W, B / 2>((W*)(y + v * B), Pack<W, B / 2>{});
+    for (uint64_t v = lane; v < c.nv; v += lanes) st_pack_once<T, V>(y + c.head + v * V, Pack<T, V>{});
   } else {
 #pragma unroll 4
-    for (uint64_t v = lane; v < nv; v += lanes)
-      st_pack_once<W, B / 2>((W*)(y + v * B), ld_pack<W, B / 2>((const W*)(b + v * B)));
+    for (uint64_t v = lane; v < c.nv; v += lanes)
+      st_pack_once<T, V>(y + c.head + v * V, ld_row_if<T, SHIFT>(b + c.head + v * V, true));
+  }
+  for (uint32_t i = lane; SHIFT && i < c.beside; i += lanes) {
+    const uint64_t e = c.at<V>(i);
+    y[e] = a.base ? b[e] : T{};
   }
 }
 
 // Fills what no token names of rows r0 .. r1.  The rows that tokens name are
 // marked in a bitmap first, by a look at all tokens.
 constexpr uint64_t kBitmapRows = 1 << 18;
-template <int B>
-__device__ __forceinline__ void fill_rows(const EmbedArgs& a, int elem, uint64_t r0, uint64_t r1, uint32_t* bits) {
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void fill_rows(const EmbedArgs& a, uint64_t r0, uint64_t r1, uint32_t* bits) {
   int lanes = 32;  // per row
-  while (lanes > 1 && (uint64_t)lanes / 2 >= a.width * elem / B) lanes /= 2;
+  while (lanes > 1 && (uint64_t)lanes / 2 >= a.width / V16<T>) lanes /= 2;
   for (uint64_t s0 = r0; s0 < r1; s0 += kBitmapRows) {
     const uint32_t rows = (uint32_t)min(kBitmapRows, r1 - s0);
     __syncthreads();
@@ -211,14 +219,14 @@ __device__ __forceinline__ void fill_rows(const EmbedArgs& a, int elem, uint64_t
     }
     __syncthreads();
     for (uint32_t k = threadIdx.x / lanes; k < rows; k += blockDim.x / lanes)
-      if (!(bits[k / 32] >> (k % 32) & 1u)) fill_row<B>(a, elem, s0 + k, threadIdx.x % lanes, lanes);
+      if (!(bits[k / 32] >> (k % 32) & 1u)) fill_row<T, SHIFT>(a, s0 + k, threadIdx.x % lanes, lanes);
   }
 }
 
 // The first cluster sorts, the others fill: that needs no sorted tokens and
 // mostly takes longer than the sort.
-template <int B>
-__global__ void __launch_bounds__(kClusterThreads) sort_fill_kernel(const __grid_constant__ SortArgs a, int ipt, int elem) {
+template <typename T, bool SHIFT>
+__global__ void __launch_bounds__(kClusterThreads) sort_fill_kernel(const __grid_constant__ SortArgs a, int ipt) {
   op_wait();
   op_next();
   extern __shared__ char dyn[];
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(kClusterThreads) sort_fill_kernel(const __grid
     return;
   }
   const uint64_t part = blockIdx.x - skip, parts = gridDim.x - skip;
-  fill_rows<B>(a.e, elem, a.e.rows * part / parts, a.e.rows * (part + 1) / parts, (uint32_t*)dyn);
+  fill_rows<T, SHIFT>(a.e, a.e.rows * part / parts, a.e.rows * (part + 1) / parts, (uint32_t*)dyn);
 }
 
 // ------------------------------------------------------- sums of sorted rows
@@ -267,7 +275,7 @@ __device__ __forceinline__ void fill_searched(const SumArgs& a, uint64_t r0) {
   __syncthreads();
   const int warps = blockDim.x / 32;
   for (int k = threadIdx.x / 32; k < kFill; k += warps)
-    if (!(touched >> k & 1u)) fill_row<N * sizeof(TY)>(a.e, sizeof(TY), r0 + k, threadIdx.x % 32, 32);
+    if (!(touched >> k & 1u)) fill_row<Bits<TY>, N * sizeof(TY) != 16>(a.e, r0 + k, threadIdx.x % 32, 32);
 }
 
 template <typename TY, int N>
@@ -480,15 +488,12 @@ purlin_status launch_sort_fill(const SortArgs& a, bool fill, int elem, cudaStrea
   const size_t smem = std::max<size_t>(sorted, fill ? kBitmapRows / 8 : 0);
   constexpr int kMost = 8 * kClusterThreads * kSortIpt + kClusterThreads / 32 * 2 * kSortBins;
   const uint64_t rows = (uint64_t)(uintptr_t)e.y | (uint64_t)(uintptr_t)e.base | (e.ldy | e.ldb | e.width) * elem;
-  auto go = [&](auto b) {
-    constexpr int B = decltype(b)::value;
-    if (purlin_status st = op_smem((const void*)sort_fill_kernel<B>, smem, kMost)) return st;
-    return op_launch_cluster(c.ctas, sort_fill_kernel<B>, grid, kClusterThreads, smem, s, a, c.ipt, elem);
+  auto go = [&](auto fn) -> purlin_status {
+    if (purlin_status st = op_smem((const void*)fn, smem, kMost)) return st;
+    return op_launch_cluster(c.ctas, fn, grid, kClusterThreads, smem, s, a, c.ipt);
   };
-  const int b = vec_bytes(rows);
-  if (b == 16) return go(std::integral_constant<int, 16>());
-  if (b == 8) return go(std::integral_constant<int, 8>());
-  return b == 4 ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 2>());
+  if (elem == 4) return rows % 16 ? go(sort_fill_kernel<uint32_t, true>) : go(sort_fill_kernel<uint32_t, false>);
+  return rows % 16 ? go(sort_fill_kernel<uint16_t, true>) : go(sort_fill_kernel<uint16_t, false>);
 }
 
 }  // namespace

@@ -324,8 +324,8 @@ int shift_of(int n, int vpt) {
 
 template <typename T, int VPT>
 int vec_ok(const RouteArgs& a) {
-  const int need = std::min<int>(16, VPT * (int)sizeof(T));
-  return a.experts % VPT == 0 && vec_bytes((uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T)) >= need;
+  const uint64_t need = std::min<uint64_t>(16, VPT * sizeof(T));
+  return a.experts % VPT == 0 && ((uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T)) % need == 0;
 }
 
 }  // namespace

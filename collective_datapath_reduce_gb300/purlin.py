@@ -359,11 +359,10 @@ def purlin_clip_grad_norm(h, grads, outs, counts, dtype, scale, max_norm, norm, 
     if n != len(counts) or (outs is not None and n != len(outs)):
         return PL_ERR_INVALID_ARG
     # one array of 64-bit words for all three: a ctypes array's type is made anew for every length
-    words = [_addr(g) for g in grads]
-    words += counts
+    words = array.array("Q", map(_addr, grads))
+    words.extend(counts)
     if outs is not None:
-        words += words[:n] if outs is grads else [_addr(o) for o in outs]
-    words = array.array("Q", words)
+        words.extend(map(_addr, outs))
     at = words.buffer_info()[0]
     return load().purlin_clip_grad_norm(h, at, None if outs is None else at + 16 * n, at + 8 * n, n, dtype, scale,
                                         max_norm, _addr(norm), _addr(workspace), workspace_bytes, _stream(stream))

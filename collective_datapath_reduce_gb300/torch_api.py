@@ -12,6 +12,7 @@ counts to libpurlin_gb.so and raises on a non-OK status.
 from __future__ import annotations
 
 import enum
+import operator
 
 import torch
 
@@ -422,6 +423,10 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
           ldt, dt, R, int(first), ws, nbytes)
 
 
+_numel, _data_ptr, _is_contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+_dtype_of = operator.attrgetter("dtype")
+
+
 def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, stream=None):
     """norm[0] = |scale| x the 2-norm of all grads together; outs[i] = grads[i] x
     scale x min(1, max_norm / (norm + 1e-6)).  grads: contiguous tensors of any
@@ -431,17 +436,17 @@ def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, strea
     _packed(norm, (1,), torch.float32, what, "norm")
     if outs is not None and len(outs) != len(grads):
         raise ValueError(f"{what}: expected {len(grads)} outputs, got {len(outs)}")
-    dt, counts = P.PL_F32, [t.numel() for t in grads]
+    # whole columns at a time: for many tensors this is what the call takes
+    dt, counts = P.PL_F32, list(map(_numel, grads))
     if counts:
-        dtype = grads[0].dtype
         dt = _values(grads[0], what)
-        # where each tensor lives is checked by the library, for all of them
         for side in (grads,) if outs is None or outs is grads else (grads, outs):
-            for t in side:
-                if t.dtype is not dtype or not t.is_contiguous():
-                    raise ValueError(f"{what}: gradients and outputs must be contiguous tensors of one dtype")
-        if outs is not None and outs is not grads and [t.numel() for t in outs] != counts:
+            # where each tensor lives is checked by the library, for all of them
+            if set(map(_dtype_of, side)) != {grads[0].dtype} or not all(map(_is_contiguous, side)):
+                raise ValueError(f"{what}: gradients and outputs must be contiguous tensors of one dtype")
+        if outs is not None and outs is not grads and list(map(_numel, outs)) != counts:
             raise ValueError(f"{what}: each output must have its gradient's size")
     nbytes = P.purlin_clip_grad_norm_bytes()
     ws = _workspace(nbytes, stream, handle)
-    _call(P.purlin_clip_grad_norm, what, handle, stream, grads, outs, counts, dt, scale, max_norm, norm, ws, nbytes)
+    _call(P.purlin_clip_grad_norm, what, handle, stream, list(map(_data_ptr, grads)),
+          None if outs is None else list(map(_data_ptr, outs)), counts, dt, scale, max_norm, norm, ws, nbytes)
