@@ -1,9 +1,8 @@
 // Routing of tokens to experts, and its gradient.
 //
 // One warp holds one token's logits, VPT neighbouring experts in each lane's
-// registers, as keys: a binary32 value mapped to an unsigned integer of the
-// same order, so that the best of the row is one integer max across the warp
-// and ties fall to the lowest lane, which holds the lowest expert.
+// registers.  The best of the row is one maximum across the warp, and ties fall
+// to the lowest lane, which holds the lowest expert.
 #include <float.h>
 #include <math.h>
 
@@ -17,20 +16,16 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;  // tokens per CTA
 
-constexpr uint32_t kOff = 0x007FFFFFu;   // the key of -inf: may not be picked
-constexpr uint32_t kLook = 0xFFFFFFFFu;  // above every key: the lane has to look for its best again
-
-// Order-preserving map to unsigned.  NaN, the lesser of every maximum, becomes
-// -inf; adding +0 makes -0 and +0 one key.
-__device__ __forceinline__ uint32_t key_of_sum(float x) {
-  const int b = __float_as_int(fmaxf(x, -INFINITY));
-  return (uint32_t)(b ^ (b >> 31 | (int)0x80000000));
+// Largest value of the warp, in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
-__device__ __forceinline__ uint32_t key_of(float x) { return key_of_sum(__fadd_rn(x, 0.f)); }
 
-__device__ __forceinline__ float of_key(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
+// A key that can be compared: NaN, the lesser of every maximum, becomes -inf,
+// which may not be picked.
+__device__ __forceinline__ float key_of(float x) { return fmaxf(x, -INFINITY); }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -67,11 +62,11 @@ __device__ __forceinline__ void load_logits(const T* row, int lane, int experts,
 // Largest logit of the row, 0 where there is none; the sum of exp(x - best).
 template <int VPT>
 __device__ __forceinline__ void softmax_of(const float (&x)[VPT], int lane, int experts, float* best, float* sum) {
-  uint32_t m = kOff;
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) m = max(m, key_of(x[i]));
-  m = __reduce_max_sync(kAll, m);
-  *best = m > kOff ? of_key(m) : 0.f;
+  for (int i = 0; i < VPT; ++i) m = fmaxf(m, x[i]);
+  m = warp_max(m);
+  *best = m > -INFINITY ? m : 0.f;
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
@@ -96,13 +91,13 @@ __device__ __forceinline__ uint32_t kept_groups(float one, float two, int shift,
   }
   const float value = a.best == 2 && two > -INFINITY ? __fadd_rn(one, two) : one;
   const bool first = (lane & ((1 << shift) - 1)) == 0 && lane >> shift < a.groups;
-  uint32_t key = first ? key_of(value) : kOff;
+  float key = first ? key_of(value) : -INFINITY;
   uint32_t keep = 0;
   for (int r = 0; r < a.kept; ++r) {
-    const uint32_t top = __reduce_max_sync(kAll, key);
-    if (top <= kOff) break;
+    const float top = warp_max(key);
+    if (!(top > -INFINITY)) break;
     const uint32_t best = lowest(__ballot_sync(kAll, key == top));
-    if (best == 1u << lane) key = kOff;
+    if (best == 1u << lane) key = -INFINITY;
     keep |= best;
   }
   return keep;
@@ -110,25 +105,25 @@ __device__ __forceinline__ uint32_t kept_groups(float one, float two, int shift,
 
 // A lane's best two keys and their experts, equal ones in order.
 struct Two {
-  uint32_t k1, k2;
+  float k1, k2;
   int e1, e2;
 };
 template <int VPT>
-__device__ __forceinline__ Two best_two(const uint32_t (&key)[VPT], int e0) {
-  Two t = {kOff, kOff, 0, 0};
+__device__ __forceinline__ Two best_two(const float (&key)[VPT], int e0) {
+  Two t = {-INFINITY, -INFINITY, 0, 0};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const bool first = key[i] > t.k1, second = key[i] > t.k2;
-    t.k2 = first ? t.k1 : max(t.k2, key[i]);
+    t.k2 = first ? t.k1 : fmaxf(t.k2, key[i]);
     t.e2 = first ? t.e1 : second ? e0 + i : t.e2;
-    t.k1 = max(t.k1, key[i]);
+    t.k1 = fmaxf(t.k1, key[i]);
     t.e1 = first ? e0 + i : t.e1;
   }
   return t;
 }
 
 // The picks are taken one by one: each lane offers its best key left, one
-// integer max across the warp finds the best of the row.  A lane keeps its best
+// maximum across the warp finds the best of the row.  A lane keeps its best
 // two keys ready and searches its registers again only after its second pick.
 //
 // Bound by the instructions of a row, not by its bytes.  16384 tokens, 256
@@ -147,28 +142,39 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   if (t >= a.tokens) return;
   const T* row = (const T*)a.logits + t * a.ld;
   float x[VPT];
-  load_logits<T, VPT>(row, lane, a.experts, vec, x);
+  load_logits<T, VPT>(row, lane, a.experts, vec & 1, x);
   float best = 0.f, sum = 1.f;
   if (!a.sigmoid) softmax_of<VPT>(x, lane, a.experts, &best, &sum);
 
-  uint32_t key[VPT];
+  float key[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) key[i] = key_of(x[i]);
   if (a.bias && e0 < a.experts) {
+    float bias[VPT];
+    if (vec & 2) {
+      constexpr int N = VPT < 4 ? VPT : 4;
+#pragma unroll
+      for (int q = 0; q < VPT; q += N) {
+        const Pack<float, N> p = *reinterpret_cast<const Pack<float, N>*>(a.bias + e0 + q);
+#pragma unroll
+        for (int i = 0; i < N; ++i) bias[q + i] = p.v[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) bias[i] = e0 + i < a.experts ? __ldg(a.bias + e0 + i) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const float b = e0 + i < a.experts ? __ldg(a.bias + e0 + i) : 0.f;
       const float s = a.sigmoid ? sigmoid(x[i]) : __fdiv_rn(expf(__fsub_rn(x[i], best)), sum);
-      key[i] = key[i] > kOff ? key_of_sum(__fadd_rn(s, b)) : kOff;  // scores are +0 at least: the sum is never -0
+      key[i] = key[i] > -INFINITY ? key_of(__fadd_rn(s, bias[i])) : -INFINITY;
     }
   }
   // what counts for a group of the expert with this key: s + bias or the
   // logit, or, of a sum of two without a bias, s (softmax: times the sum)
   const bool by_score = a.best == 2 && !a.bias;
-  auto value = [&](uint32_t k) {
-    const float v = of_key(k);
-    if (!by_score || k <= kOff) return v;
-    return a.sigmoid ? sigmoid(v) : expf(__fsub_rn(v, best));
+  auto value = [&](float k) {
+    if (!by_score || !(k > -INFINITY)) return k;
+    return a.sigmoid ? sigmoid(k) : expf(__fsub_rn(k, best));
   };
 
   if (a.groups > 1 && a.group_shift < 0) {
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     int g = e0 / n, left = n - e0 % n;  // the group of expert e0 + i, and its experts from there on
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (!(keep >> (g << shift & 31) & 1u)) key[i] = kOff;
+      if (!(keep >> (g << shift & 31) & 1u)) key[i] = -INFINITY;
       if (--left == 0) {
         ++g;
         left = n;
@@ -198,36 +204,41 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
   Two b = best_two<VPT>(key, e0);
   if (a.groups > 1 && a.group_shift >= 0) {
     const uint32_t keep = kept_groups(value(b.k1), value(b.k2), a.group_shift, lane, a);
-    if (!(keep >> (lane & -1 << a.group_shift) & 1u)) b.k1 = kOff;
+    if (!(keep >> (lane & -1 << a.group_shift) & 1u)) b.k1 = -INFINITY;
   }
 
   int* pick = picks[warp];
-  int j = 0;
-  uint32_t last = 0;  // this lane's last pick
-  int last_e = 0;
+  int j = 0, last_e = 0;
+  float last = 0.f;    // this lane's last pick
+  bool ready = true;   // b.k2 is the best key behind b.k1
+  bool look = false;   // b.k1 is not known, and +inf until it is looked for
   while (j < a.top_k) {
-    const uint32_t top = __reduce_max_sync(kAll, b.k1);
-    if (top - kOff - 1 >= kLook - kOff - 1) {
-      if (top <= kOff) break;
-      if (b.k1 == kLook) {  // the best key behind the lane's last pick
-        b.k1 = kOff;
+    const float top = warp_max(b.k1);
+    if (fabsf(top) == INFINITY) {
+      if (top < 0.f) break;
+      if (__any_sync(kAll, look)) {
+        if (look) {  // the best key behind the lane's last pick
+          look = false;
+          b.k1 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const bool behind = key[i] < last || (key[i] == last && e0 + i > last_e);
-          if (behind && key[i] > b.k1) {
-            b.k1 = key[i];
-            b.e1 = e0 + i;
+          for (int i = 0; i < VPT; ++i) {
+            const bool behind = key[i] < last || (key[i] == last && e0 + i > last_e);
+            if (behind && key[i] > b.k1) {
+              b.k1 = key[i];
+              b.e1 = e0 + i;
+            }
           }
         }
+        continue;
       }
-      continue;
     }
     if (lowest(__ballot_sync(kAll, b.k1 == top)) == 1u << lane) {
       pick[j] = last_e = b.e1;
       last = b.k1;
-      b.k1 = b.k2;
+      look = !ready;
+      b.k1 = ready ? b.k2 : INFINITY;
       b.e1 = b.e2;
-      b.k2 = kLook;
+      ready = false;
     }
     ++j;
   }
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
   }
   float x[VPT], best = 0.f, sum = 1.f;
   if (!a.sigmoid) {
-    load_logits<T, VPT>(row, lane, a.experts, vec, x);
+    load_logits<T, VPT>(row, lane, a.experts, vec & 1, x);
     softmax_of<VPT>(x, lane, a.experts, &best, &sum);
   }
   float s = 0.f;
@@ -325,7 +336,10 @@ int shift_of(int n, int vpt) {
 template <typename T, int VPT>
 int vec_ok(const RouteArgs& a) {
   const uint64_t need = std::min<uint64_t>(16, VPT * sizeof(T));
-  return a.experts % VPT == 0 && ((uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T)) % need == 0;
+  const bool whole = a.experts % VPT == 0;  // every lane's experts exist or none
+  const int logits = whole && ((uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T)) % need == 0;
+  const int bias = whole && (uintptr_t)a.bias % std::min<uint64_t>(16, VPT * sizeof(float)) == 0;
+  return logits | bias << 1;
 }
 
 }  // namespace

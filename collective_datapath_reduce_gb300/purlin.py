@@ -200,6 +200,11 @@ def _addr(x) -> int:
     return x.data_ptr()
 
 
+def _addresses(seq):
+    """Addresses of a list of integers (as it is) or of tensors."""
+    return seq if set(map(type, seq)) <= {int} else map(_addr, seq)
+
+
 def _stream(s):
     if s is None:
         return None
@@ -359,10 +364,10 @@ def purlin_clip_grad_norm(h, grads, outs, counts, dtype, scale, max_norm, norm, 
     if n != len(counts) or (outs is not None and n != len(outs)):
         return PL_ERR_INVALID_ARG
     # one array of 64-bit words for all three: a ctypes array's type is made anew for every length
-    words = array.array("Q", map(_addr, grads))
+    words = array.array("Q", _addresses(grads))
     words.extend(counts)
     if outs is not None:
-        words.extend(map(_addr, outs))
+        words.extend(_addresses(outs))
     at = words.buffer_info()[0]
     return load().purlin_clip_grad_norm(h, at, None if outs is None else at + 16 * n, at + 8 * n, n, dtype, scale,
                                         max_norm, _addr(norm), _addr(workspace), workspace_bytes, _stream(stream))
