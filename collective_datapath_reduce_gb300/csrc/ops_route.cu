@@ -14,7 +14,7 @@ namespace pl {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 8;  // tokens per CTA
+constexpr int kWarps = 4;  // tokens per CTA (2, 4, 8, 16: 17.3, 17.5, 17.9, 19.1 us for the case at route_kernel)
 
 // Largest value of the warp, in every lane.
 __device__ __forceinline__ float warp_max(float x) {
@@ -126,12 +126,14 @@ __device__ __forceinline__ Two best_two(const float (&key)[VPT], int e0) {
 // maximum across the warp finds the best of the row.  A lane keeps its best
 // two keys ready and searches its registers again only after its second pick.
 //
-// Bound by the instructions of a row, not by its bytes.  16384 tokens, 256
-// experts, 8 picks, sigmoid, bias, 4 of 8 groups by their best two: 35 us with a
-// search at every pick, 22 us with two keys ready, 19 us with shifts for the
-// divisions by the group's lanes, and the pick found by its lane's bit and
-// passed through shared memory (bit scans and reductions run at half a warp
-// per cycle and SM).
+// Bound by the instructions of a row (about 900), not by its bytes (17 MB, 2.6
+// us).  16384 tokens, 256 experts, 8 picks, sigmoid, bias, 4 of 8 groups by their
+// best two: 35 us with a search at every pick, 22 us with two keys ready, 19 us
+// with shifts for the divisions by a group's lanes and the pick passed through
+// shared memory by the lane that offers it (a bit scan takes 4 cycles per SM, a
+// maximum or a ballot 1), 17.5 us with keys compared as they are, not mapped to
+// integers, and the bias read in vectors.  Of that a pick takes 0.6 us, the
+// sigmoids 3 us, the groups 3 us.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a, int vec) {
   op_wait();
@@ -351,7 +353,7 @@ purlin_status launch_route(const RouteArgs& in, int dtype, cudaStream_t s) {
     RouteArgs a = in;
     a.group_size = a.experts / a.groups;
     a.group_shift = shift_of(a.group_size, V);
-    // the groups' values, at most 32 KiB
+    // the groups' values, at most 16 KiB
     const size_t smem = a.groups > 1 && a.group_shift < 0 ? (size_t)kWarps * a.experts * sizeof(float) : 0;
     if (dtype == PL_F32) return op_launch(route_kernel<float, V>, grid, kWarps * 32, smem, s, a, vec_ok<float, V>(a));
     return op_launch(route_kernel<bf16, V>, grid, kWarps * 32, smem, s, a, vec_ok<bf16, V>(a));
