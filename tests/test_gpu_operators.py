@@ -341,7 +341,34 @@ def test_exchange_past_32_bit_offsets(h):
     y = torch.empty_like(x)
     purlin.combine_rows(rows, places, torch.full((T, k), 0.125, device=DEV), y, h)
     assert torch.equal(y, x)                       # eight eighths of one value are exact
+    grad_rows, grad_w = torch.empty_like(rows), torch.empty(T, k, device=DEV)
+    purlin.combine_rows_grad(rows, places, torch.full((T, k), 0.5, device=DEV), x, grad_rows, grad_w, h)
+    for a in range(0, T * k, 1 << 17):
+        assert torch.equal(grad_rows[a:a + (1 << 17)], rows[a:a + (1 << 17)] * 0.5)    # halves are exact
+    # every pick's product is the token's with itself: D squares near 1, in binary32
+    assert ((grad_w - x.float().square().sum(1, keepdim=True)).abs() <= 2 * D * D * E24 * 2).all()
+    assert torch.equal(grad_w, grad_w[:, :1].expand(-1, k))
     assert P.purlin_status_get(h.raw)[1] == P.PL_OK
+
+
+def test_route_past_32_bit_offsets(h):
+    """2.1 Gi logits: the last tokens are routed as they are alone."""
+    T, E, k = 2100007, 1024, 4
+    x = torch.empty(T, E, dtype=torch.bfloat16, device=DEV)
+    x[:-100].fill_(0.0)
+    x[-100:].normal_(generator=torch.Generator(device=DEV).manual_seed(3))
+    ids, w = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    purlin.route_experts(x, ids, w, h)
+    ids1, w1 = torch.empty(100, k, dtype=torch.int32, device=DEV), torch.empty(100, k, device=DEV)
+    purlin.route_experts(x[-100:].clone(), ids1, w1, h)
+    assert torch.equal(ids[-100:], ids1) and torch.equal(w[-100:], w1)
+    assert (ids[:-100] == torch.arange(k, device=DEV, dtype=torch.int32)).all() and (w[:-100] == 0.25).all()
+    grad, grad1 = torch.empty_like(x), torch.empty(100, E, dtype=torch.bfloat16, device=DEV)
+    dw = torch.ones(T, k, device=DEV)
+    dw[:, 0] = 2.0
+    purlin.route_experts_grad(x, ids, dw, grad, h)
+    purlin.route_experts_grad(x[-100:].clone(), ids1, dw[:100], grad1, h)
+    assert torch.equal(grad[-100:], grad1) and torch.equal(grad[0], grad[T // 2])
 
 
 # ----------------------------------------------------------------- embedding
@@ -421,6 +448,33 @@ def test_embed_gradient(h, case, dtypes):
         assert out.intact()
 
 
+def test_embed_past_32_bit_offsets(h):
+    """A table of 2.2 Gi elements: lookups near its end, and the gradient's rows."""
+    R, D = 530001, 4096
+    table = torch.empty(R, D, dtype=torch.bfloat16, device=DEV)
+    tokens = torch.tensor([R - 1, 0, R // 2, R - 1, R, 524288], device=DEV)
+    table[tokens[[0, 1, 2, 5]]] = torch.arange(1, 5, device=DEV, dtype=torch.bfloat16)[:, None].expand(-1, D)
+    out = torch.empty(6, D, dtype=torch.bfloat16, device=DEV)
+    purlin.embed(table, tokens, out, h)
+    assert (out == torch.tensor([1, 2, 3, 1, 0, 4], device=DEV)[:, None]).all()
+    table.fill_(9.0)
+    purlin.embed_grad(out, tokens, table, h)
+    want = torch.zeros(R, device=DEV)
+    want[tokens[[0, 1, 2, 5]]] = torch.tensor([2.0, 2, 3, 4], device=DEV)
+    for a in range(0, R, 1 << 16):
+        assert (table[a:a + (1 << 16)].float() == want[a:a + (1 << 16), None]).all()
+
+
+def test_embed_gradient_of_a_long_narrow_table(h):
+    """So many rows that a CTA marks its share in several pieces."""
+    R = 90000001
+    tokens = torch.tensor([0, R - 1, 45000000, 262144, 262143, R - 1], device=DEV)
+    grad = torch.full((R, 1), 7.0, dtype=torch.bfloat16, device=DEV)
+    purlin.embed_grad(torch.ones(6, 1, dtype=torch.bfloat16, device=DEV), tokens, grad, h)
+    at = grad[:, 0].nonzero()[:, 0]
+    assert at.tolist() == [0, 262143, 262144, 45000000, R - 1] and grad[at, 0].tolist() == [1, 1, 1, 1, 2]
+
+
 def test_embed_gradient_repeats_bit_for_bit(h):
     g = torch.Generator(device=DEV).manual_seed(2)
     dy = torch.randn(30000, 264, generator=g, device=DEV)
@@ -478,6 +532,15 @@ def test_clip_of_nothing(h):
     z = [torch.zeros(100, device=DEV)]
     purlin.clip_grad_norm(z, z, 1.0, norm, h)
     assert norm.item() == 0.0 and (z[0] == 0).all()
+
+
+def test_clip_past_32_bit_offsets(h):
+    n = 2200000003
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device=DEV)
+    norm = torch.empty(1, device=DEV)
+    purlin.clip_grad_norm([g], [g], 0.25 * math.sqrt(n), norm, h)     # half of the norm
+    assert abs(norm.item() - 0.5 * math.sqrt(n)) <= 0.5 * math.sqrt(n) * 4 * E24     # all partial sums are exact
+    assert (g == 0.25).all()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
