@@ -481,9 +481,8 @@ purlin_status op_begin(purlin_handle h, OpHandle* out) {
   return PL_OK;
 }
 
-purlin_status op_locate(const OpHandle& h, const void* p, const void** dev_p) {
-  bool host = false;
-  return locate(h.device, p, dev_p, &host);
+purlin_status op_locate(const OpHandle& h, const void* p, const void** dev_p, bool* host) {
+  return locate(h.device, p, dev_p, host);
 }
 
 }  // namespace pl

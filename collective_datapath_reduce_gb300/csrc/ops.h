@@ -22,7 +22,7 @@ struct OpHandle {
 // The handle is live and its device is current (api.cpp).
 purlin_status op_begin(purlin_handle h, OpHandle* out);
 // Where a caller's pointer lives, and the address the kernels use (api.cpp).
-purlin_status op_locate(const OpHandle& h, const void* p, const void** dev_p);
+purlin_status op_locate(const OpHandle& h, const void* p, const void** dev_p, bool* host);
 
 struct RouteArgs {
   const void* logits;
@@ -67,6 +67,7 @@ struct RowsArgs {
   uint64_t width;
   int top_k;
   uint32_t* status;
+  bool host;          // some rows are host memory
   // gradient of combine: x = expert rows, y = gradient of the expert rows
   const void* grad_y;
   uint64_t ldg;

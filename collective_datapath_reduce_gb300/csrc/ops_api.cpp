@@ -43,10 +43,13 @@ class Buffers {
     hi_[n_] = a + bytes;
     written_[n_++] = written;
     const void* q = nullptr;
-    if (purlin_status st = pl::op_locate(h_, (const void*)*p, &q)) return st;
+    if (purlin_status st = pl::op_locate(h_, (const void*)*p, &q, &host_)) return st;
     *p = (P*)const_cast<void*>(q);
     return PL_OK;
   }
+
+  // Some of them are host memory.
+  bool host() const { return host_; }
 
   // No written buffer overlaps another one.
   purlin_status apart() const {
@@ -60,7 +63,7 @@ class Buffers {
   static constexpr int kMost = 8;
   const pl::OpHandle& h_;
   uintptr_t lo_[kMost], hi_[kMost];
-  bool written_[kMost];
+  bool written_[kMost], host_ = false;
   int n_ = 0;
 };
 
@@ -230,6 +233,7 @@ purlin_status purlin_combine_rows(purlin_handle handle, const void* rows, size_t
   a.width = width;
   a.top_k = top_k;
   a.status = h.status;
+  a.host = b.host();
   return pl::launch_combine(a, dtype, (cudaStream_t)stream);
 }
 
@@ -359,6 +363,7 @@ purlin_status purlin_clip_grad_norm(purlin_handle handle, const void* const* gra
     size_t of;
   };
   try {
+    bool host = false;  // either kind goes
     std::vector<Span> spans;
     std::vector<pl::ClipTensor> t;
     spans.reserve(2 * n + 2);
@@ -368,7 +373,7 @@ purlin_status purlin_clip_grad_norm(purlin_handle handle, const void* const* gra
       if (!p || a + bytes < a) return PL_ERR_INVALID_ARG;
       if (a % align) return PL_ERR_ALIGNMENT;
       spans.push_back(Span{a, a + bytes, written, of});
-      return pl::op_locate(h, p, q);
+      return pl::op_locate(h, p, q, &host);
     };
     for (size_t i = 0; i < n; ++i) {
       if (counts[i] == 0) continue;

@@ -4,6 +4,7 @@
 // index, the sum an N-to-1 reduce Atom whose sources are.
 #include <type_traits>
 
+#include "kernels_bulk.cuh"
 #include "ops_common.cuh"
 #include "ops_sort.cuh"
 
@@ -290,6 +291,92 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_narrow_kernel(const __
   }
 }
 
+// The same through shared memory: one CTA for `tile` columns of one token.  Bulk
+// copies bring the 16-byte granules that lie whole in each row's piece, at
+// the piece's own address modulo 16, and threads the elements beside them, so
+// any alignment moves like any other and no registers wait for the rows.
+constexpr unsigned long long kBulkWaitNs = 2000000000ull;
+template <typename T, int J>
+__global__ void __launch_bounds__(kRowThreads) combine_bulk_kernel(const __grid_constant__ RowsArgs a, uint32_t tile,
+                                                                   uint32_t tiles, uint32_t stride) {
+  op_wait();
+  extern __shared__ __align__(16) char piece[];  // k pieces, `stride` bytes apart
+  __shared__ uint64_t bar;
+  __shared__ const T* src[PURLIN_MAX_TOP_K];     // the row's piece, or null
+  __shared__ float weight[PURLIN_MAX_TOP_K];
+  const int k = a.top_k, tid = threadIdx.x;
+  const uint64_t t = blockIdx.x / tiles, c0 = (uint64_t)(blockIdx.x % tiles) * tile;
+  const uint32_t n = (uint32_t)min((uint64_t)tile, a.width - c0);
+  if (tid < k) {
+    const uint64_t slot = t * k + tid;
+    const int64_t p = a.places[slot];
+    const bool in = (uint64_t)(p >= 0 ? p : ~p) < a.tokens * (uint64_t)k;
+    if (!in) op_status(a.status, PL_ERR_BOUNDS);
+    const bool live = in && p >= 0;
+    src[tid] = live ? (const T*)a.x + (uint64_t)p * a.ldx + c0 : nullptr;
+    weight[tid] = live ? (a.weights ? a.weights[slot] : 1.f) : 0.f;
+  }
+  if (tid == 0) mbar_init(&bar, 1);
+  __syncthreads();
+  // the granules of a piece: from b0 to b1, offsets from the piece's first byte
+  auto first = [](const T* p) { return (uint32_t)(16u - ((uintptr_t)p & 15u)) & 15u; };
+  auto last = [n](const T* p) { return (uint32_t)(n * sizeof(T) - (((uintptr_t)p + n * sizeof(T)) & 15u)); };
+  if (tid == 0) {
+    fence_async_shared();
+    fence_async_global();
+    uint32_t bytes = 0;
+    for (int j = 0; j < k; ++j)
+      if (src[j] && n * sizeof(T) >= 32) bytes += last(src[j]) - first(src[j]);
+    mbar_expect_tx(&bar, bytes);
+    for (int j = 0; j < k; ++j) {
+      const T* p = src[j];
+      if (!p || n * sizeof(T) < 32) continue;
+      const uint32_t b0 = first(p), size = last(p) - b0;  // a multiple of 16, and 16 at least
+      bulk_load(piece + (uint64_t)j * stride + ((uintptr_t)p & 15u) + b0, (const char*)p + b0, size, &bar);
+    }
+  }
+  // beside them: fewer than 16 bytes at each end, or all of a short piece
+  constexpr int B = 32 / sizeof(T);
+  for (int i = tid; i < k * B; i += blockDim.x) {
+    const T* p = src[i / B];
+    if (!p) continue;
+    const uint32_t r = i % B;
+    uint32_t e = r;
+    bool is = r < n;
+    if (n * sizeof(T) >= 32) {
+      const uint32_t head = first(p) / sizeof(T), tail = last(p) / sizeof(T);
+      e = r < head ? r : tail + r - head;
+      is = e < n;
+    }
+    if (is) ((T*)(piece + (uint64_t)(i / B) * stride + ((uintptr_t)p & 15u)))[e] = p[e];
+  }
+  if (!__syncthreads_and(mbar_wait(&bar, 0, kBulkWaitNs))) {
+    if (tid == 0) op_status(a.status, PL_ERR_TIMEOUT);
+    mbar_wait(&bar, 0, kBulkWaitNs);  // the copies in flight still write here
+    return;
+  }
+  T* y = (T*)a.y + t * a.ldy + c0;
+  for (int j0 = 0; j0 == 0 || j0 < k; j0 += J) {
+    const T* s[J];
+    float w[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bool is = j0 + j < k && src[j0 + j];
+      // a dropped pick reads another's piece, and adds nothing of it
+      s[j] = is ? (const T*)(piece + (uint64_t)(j0 + j) * stride + ((uintptr_t)src[j0 + j] & 15u)) : nullptr;
+      w[j] = is ? weight[j0 + j] : 0.f;
+    }
+    for (uint32_t e = tid; e < n; e += blockDim.x) {
+      float acc = j0 ? ((float*)(piece + (uint64_t)k * stride))[e] : 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (s[j]) acc = __fmaf_rn(w[j], to_f32(s[j][e]), acc);
+      if (j0 + J < k) ((float*)(piece + (uint64_t)k * stride))[e] = acc;
+      else y[e] = from_f32<T>(acc);
+    }
+  }
+}
+
 // grad_rows[place_j] = w_j dy, grad_w_j = <rows[place_j], dy>: dy is read once
 // for J picks, and J rows are in flight in each thread.  The products' parts
 // are joined in a fixed order, by lanes and then by warps.  Rows are stored
@@ -466,6 +553,18 @@ purlin_status combine_t(const RowsArgs& a, cudaStream_t s) {
   const bool narrow = !aligned<T>(a);
   return with_int<8>(rows_in_flight(a.top_k), [&](auto each) {
     constexpr int J = decltype(each)::value;
+    // rows of 1 KiB or more, in device memory, through shared memory: 40 KiB a CTA
+    // (the sums of more than 8 picks take a binary32 row of their own there)
+    if (narrow && !a.host && a.width * sizeof(T) >= 1024) {
+      const uint64_t each = (uint64_t)a.top_k * sizeof(T) + (a.top_k > 8 ? 4 : 0);
+      const uint32_t tile = (uint32_t)std::min<uint64_t>(a.width, (40 * 1024 - 32 * a.top_k) / each);
+      const uint64_t tiles = (a.width + tile - 1) / tile;
+      const uint32_t even = (uint32_t)((a.width + tiles - 1) / tiles);
+      const uint32_t stride = (uint32_t)((even * sizeof(T) + 31) & ~(size_t)15);
+      const size_t smem = (size_t)stride * a.top_k + (a.top_k > 8 ? (size_t)even * 4 : 0);
+      if (purlin_status st = op_smem((const void*)combine_bulk_kernel<T, J>, smem, 48 * 1024)) return st;
+      return op_launch(combine_bulk_kernel<T, J>, a.tokens * tiles, kRowThreads, smem, s, a, even, (uint32_t)tiles, stride);
+    }
     if (narrow) {
       constexpr int S = sizeof(T) == 4 ? 2 : 4;
       const RowShape c((a.width + S - 1) / S);
