@@ -248,10 +248,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(const __grid_co
   }
 }
 
-// The same for rows that are not 16-byte aligned: S elements of a thread, tpt
-// apart, of J rows each in flight.  Cutting aligned vectors out of the rows'
-// granules moves fewer requests but waits longer for each (41 against 25
-// us for 3001 tokens, 6 rows of 1537 binary32 values).
+// The same for rows that are not 16-byte aligned, and short or in host memory: S
+// elements of a thread, tpt apart, of J rows each in flight.  Cutting aligned
+// vectors out of the rows' granules moves fewer requests but waits longer for
+// each (41 against 25 us for 3001 tokens, 6 rows of 1537 binary32 values).
 template <typename T, int S, int J>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_narrow_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
@@ -294,7 +294,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_narrow_kernel(const __
 // The same through shared memory: one CTA for `tile` columns of one token.  Bulk
 // copies bring the 16-byte granules that lie whole in each row's piece, at
 // the piece's own address modulo 16, and threads the elements beside them, so
-// any alignment moves like any other and no registers wait for the rows.
+// any alignment moves like any other and no registers wait for the rows.  (3001
+// tokens of width 1537: 6 picks, binary32, 24.3 us, by registers 25.3; 8 picks,
+// bf16, 23.2 against 29.5.  CTAs that stay and fetch the next token's rows during
+// the sums were slower, 38 to 46 us: the elements beside the granules then cost a
+// round trip in every round.)
 constexpr unsigned long long kBulkWaitNs = 2000000000ull;
 template <typename T, int J>
 __global__ void __launch_bounds__(kRowThreads) combine_bulk_kernel(const __grid_constant__ RowsArgs a, uint32_t tile,
