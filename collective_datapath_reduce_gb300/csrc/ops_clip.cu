@@ -191,9 +191,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   factor_of(a, sum_of_parts(a, tmp), threadIdx.x == 0);
 }
 
-// Few elements: one CTA, a warp for each piece of kSmallChunk elements.
+// Few elements: one CTA, a warp for each piece of kSmallChunk elements.  On the
+// device the two kernels are level (20000 values: 8.8 and 8.4 us) and later ahead
+// (60000: 13.7 and 8.4), but the second launch costs the host 2.5 us, and few
+// elements wait for the host.
 constexpr int kSmallThreads = 1024;
-constexpr uint64_t kSmallChunk = 1024, kSmallMost = 64 * 1024;
+constexpr uint64_t kSmallChunk = 1024, kSmallMost = 32 * 1024;
 template <typename T>
 __global__ void __launch_bounds__(kSmallThreads) clip_small_kernel(const __grid_constant__ Table<kFew> a, int write) {
   op_wait();

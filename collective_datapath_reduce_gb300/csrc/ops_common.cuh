@@ -255,7 +255,9 @@ struct RowShape {
   }
   uint64_t ctas(uint64_t tokens, int u) const { return (tokens + per * u - 1) / (per * u); }
 };
-// Several tokens per group pay off once the CTAs still fill the SMs twice.
+// Several tokens per group pay off where the CTAs still fill the SMs twice (1
+// pick of 2048 bf16 values, one token at a time and four: 300 tokens 2.4 and 3.0
+// us, 1300 tokens 4.3 and 3.6; embedding the same, 300: 2.4, 2.6, 5000: 8.8, 7.3).
 constexpr uint64_t kManyCtas = 2 * 152;
 
 }  // namespace pl

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(const __grid_co
   }
 }
 
-// The same for rows that are not 16-byte aligned, and short or in host memory: S
+// The same for rows that are not 16-byte aligned and short, or in host memory: S
 // elements of a thread, tpt apart, of J rows each in flight.  Cutting aligned
 // vectors out of the rows' granules moves fewer requests but waits longer for
 // each (41 against 25 us for 3001 tokens, 6 rows of 1537 binary32 values).
@@ -557,9 +557,12 @@ purlin_status combine_t(const RowsArgs& a, cudaStream_t s) {
   const bool narrow = !aligned<T>(a);
   return with_int<8>(rows_in_flight(a.top_k), [&](auto each) {
     constexpr int J = decltype(each)::value;
-    // rows of 1 KiB or more, in device memory, through shared memory: 40 KiB a CTA
-    // (the sums of more than 8 picks take a binary32 row of their own there)
-    if (narrow && !a.host && a.width * sizeof(T) >= 1024) {
+    // Long rows in device memory go through shared memory, 40 KiB a CTA (the sums
+    // of more than 8 picks take a binary32 row of their own there).  A CTA costs
+    // the same for a short row, by registers the time goes with the elements:
+    // 8000 tokens, 6 picks: binary32 of 513 columns 34 us, by registers 25; bf16 of
+    // 513 columns 32 and 30, of 1025 columns 37 and 47.
+    if (narrow && !a.host && a.width >= 768) {
       const uint64_t each = (uint64_t)a.top_k * sizeof(T) + (a.top_k > 8 ? 4 : 0);
       const uint32_t tile = (uint32_t)std::min<uint64_t>(a.width, (40 * 1024 - 32 * a.top_k) / each);
       const uint64_t tiles = (a.width + tile - 1) / tile;
