@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kClusterThreads) plan_cluster_kernel(const __g
 
 // ------------------------------------------------------------ rows by index
 
-
 // A CTA holds `per` groups of tpt threads (a multiple of 32); each group takes
 // U tokens and keeps one vector of each in flight.  The picks of the CTA's
 // tokens are read once, into shared memory.

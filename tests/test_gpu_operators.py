@@ -223,7 +223,8 @@ def test_route_gradient(h, T, E, k, pad, kind, renormalise, dtype):
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 32, 1024), (5, 3, 2), (17, 8, 128), (1000, 8, 7),
                                    (1024, 8, 256), (8193, 1, 64), (1025, 8, 1024), (20000, 8, 256), (200003, 6, 33),
-                                   (2048, 1, 16), (2049, 1, 16), (4097, 1, 1024), (32768, 2, 100), (65537, 1, 100)])
+                                   (2048, 1, 16), (2049, 1, 16), (4097, 1, 1024), (32768, 2, 100), (65537, 1, 100),
+                                   (3000, 8, 1024), (16384, 1, 7), (16385, 1, 1024)])
 def test_plan(h, T, k, E):
     rng = np.random.default_rng(T + k)
     ids = rng.integers(-1, E + 2, (T, k)) if E > 1 else rng.integers(0, 2, (T, k))
@@ -628,6 +629,36 @@ def test_other_streams_and_graphs_give_the_same(h):
         side.synchronize()
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+def test_streams_of_one_handle_need_no_order(h):
+    """The same handle on two streams at once: each has its workspace."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    jobs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for n in (30000, 50000):
+        tokens = (torch.rand(n, generator=g, device=DEV) ** 4 * 3000).to(torch.int64)
+        dy = torch.randn(n, 128, generator=g, device=DEV)
+        ids = torch.randint(0, 64, (n, 4), generator=g, device=DEV, dtype=torch.int32)
+        jobs.append((tokens, dy, ids))
+
+    def run(job, stream):
+        tokens, dy, ids = job
+        grad, offsets, places = torch.empty(3000, 128, device=DEV), torch.empty(65, dtype=torch.int32, device=DEV), torch.empty_like(ids)
+        clipped, norm = torch.empty_like(dy), torch.empty(1, device=DEV)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(5):
+            purlin.embed_grad(dy, tokens, grad, h, stream=stream)
+            purlin.expert_plan(ids, offsets, places, h, stream=stream)
+            purlin.clip_grad_norm([dy], [clipped], 1.0, norm, h, stream=stream)
+        return grad, offsets, places, clipped, norm
+    want = [run(j, None) for j in jobs]
+    torch.cuda.synchronize()
+    got = [run(j, s) for j, s in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        for a, b in zip(w, o):
+            assert torch.equal(a, b)
 
 
 def test_renormalised_weights_sum_to_one(h):
