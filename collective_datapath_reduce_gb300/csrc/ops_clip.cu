@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t share(uint32_t chunks, uint32_t b) {
 // Runs vec(vector, first element, whether there is one) for the 16-byte vectors
 // of elements [e0, e1) at p, F of a thread in flight at a time, and one(element)
 // for the elements beside them.
-template <int THREADS, int F, typename T, typename V, typename O>
+template <int THREADS, int F, Ld HOW, typename T, typename V, typename O>
 __device__ __forceinline__ void walk(const T* p, bool aligned, uint64_t e0, uint64_t e1, V vec, O one) {
   constexpr int N = 16 / sizeof(T);
   const uint32_t tid = threadIdx.x % THREADS;
@@ -71,7 +71,7 @@ __device__ __forceinline__ void walk(const T* p, bool aligned, uint64_t e0, uint
   for (uint32_t v = tid; v < nv; v += THREADS * F) {
     Pack<T, N> x[F];
 #pragma unroll
-    for (int u = 0; u < F; ++u) x[u] = ld_pack_if<T, N>(p + v0 + (uint64_t)(v + u * THREADS) * N, v + u * THREADS < nv);
+    for (int u = 0; u < F; ++u) x[u] = ld_pack_if<T, N, HOW>(p + v0 + (uint64_t)(v + u * THREADS) * N, v + u * THREADS < nv);
 #pragma unroll
     for (int u = 0; u < F; ++u) pin(x[u]);
 #pragma unroll
@@ -87,7 +87,7 @@ __device__ __forceinline__ void walk(const T* p, bool aligned, uint64_t e0, uint
 template <int THREADS, int F, typename T>
 __device__ __forceinline__ double squares(const T* p, uint64_t e0, uint64_t e1) {
   float s = 0.f;
-  walk<THREADS, F, T>(
+  walk<THREADS, F, Ld::kOnce, T>(
       p, true, e0, e1,
       [&](const auto& x, uint64_t, bool) {  // zeros where there is none
 #pragma unroll
@@ -96,7 +96,7 @@ __device__ __forceinline__ double squares(const T* p, uint64_t e0, uint64_t e1) 
       [&](uint64_t i) { s = __fmaf_rn(to_f32(p[i]), to_f32(p[i]), s); });
   if (s <= 1e38f) return (double)s;
   double w = 0.0;
-  walk<THREADS, 1, T>(
+  walk<THREADS, 1, Ld::kOnce, T>(
       p, true, e0, e1,
       [&](const auto& x, uint64_t, bool) {
         for (int k = 0; k < 16 / (int)sizeof(T); ++k) w += (double)to_f32(x.v[k]) * (double)to_f32(x.v[k]);
@@ -108,7 +108,7 @@ __device__ __forceinline__ double squares(const T* p, uint64_t e0, uint64_t e1) 
 // In place, an element is loaded and stored by the same thread, and by no other.
 template <int THREADS, int F, typename T>
 __device__ __forceinline__ void scale(const T* p, T* o, uint64_t e0, uint64_t e1, float f) {
-  walk<THREADS, F, T>(
+  walk<THREADS, F, Ld::kWritten, T>(
       p, (((uintptr_t)p ^ (uintptr_t)o) & 15) == 0, e0, e1,
       [&](auto& x, uint64_t i, bool on) {
 #pragma unroll

@@ -95,23 +95,23 @@ __device__ __forceinline__ Pack<T, N> ld_pack(const T* p) {
 
 // 16 bytes at p, or zeros where `on` is false: one predicated load.  Written as
 // a branch around a load and one around its use, the compiler joins the two,
-// and each load then waits for the one before (150 us instead of 79 for a sum of
-// 6 rows of 8 KiB for each of 8192 tokens).  KEEP: into the L1 too.
-template <bool KEEP = false>
+// and each load then waits for the one before (150 us instead of 71 for a sum of
+// 6 rows of 8 KiB for each of 8192 tokens).  KEPT: into the L1 too.  WRITTEN: of
+// memory that this kernel writes, not through the read-only path.
+enum class Ld { kOnce, kKept, kWritten };
+template <Ld HOW = Ld::kOnce>
 __device__ __forceinline__ uint4 ld16_if(const void* p, bool on) {
   uint4 v;
-  if (KEEP)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-        "mov.u32 %3, 0;\n\t@q ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((uint32_t)on));
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-        "mov.u32 %3, 0;\n\t@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((uint32_t)on));
+#define PL_LD16_IF(op)                                                                                               \
+  asm volatile(                                                                                                      \
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"          \
+      "mov.u32 %3, 0;\n\t@q " op " {%0,%1,%2,%3}, [%4];\n\t}"                                                       \
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)                                                               \
+      : "l"(p), "r"((uint32_t)on))
+  if constexpr (HOW == Ld::kOnce) PL_LD16_IF("ld.global.nc.L1::no_allocate.v4.u32");
+  else if constexpr (HOW == Ld::kKept) PL_LD16_IF("ld.global.nc.v4.u32");
+  else PL_LD16_IF("ld.global.v4.u32");
+#undef PL_LD16_IF
   return v;
 }
 
@@ -143,13 +143,14 @@ __device__ __forceinline__ void pin(Pack<T, N>& r) {
   }
 }
 
-template <typename T, int N>
+template <typename T, int N, Ld HOW = Ld::kOnce>
 __device__ __forceinline__ Pack<T, N> ld_pack_if(const T* p, bool on) {
   Pack<T, N> r;
   if constexpr (sizeof(T) * N == 16) {
-    const uint4 u = ld16_if(p, on);
+    const uint4 u = ld16_if<HOW>(p, on);
     memcpy(&r, &u, 16);
   } else {
+    static_assert(HOW == Ld::kOnce);
     memset(&r, 0, sizeof r);
     if (on) r = ld_pack<T, N>(p);
   }
@@ -171,7 +172,7 @@ __device__ __forceinline__ Pack<T, V16<T>> ld_row_if(const T* p, bool on) {
   } else {
     const uint32_t m = (uint32_t)((uintptr_t)p & 15u);
     const char* a = (const char*)p - m;
-    const uint4 A = ld16_if<true>(a, on), B = ld16_if<true>(a + 16, on && m);
+    const uint4 A = ld16_if<Ld::kKept>(a, on), B = ld16_if<Ld::kKept>(a + 16, on && m);
     u = m ? window16(A, B, m) : A;
   }
   memcpy(&r, &u, 16);

@@ -141,6 +141,9 @@ __device__ __forceinline__ void load_picks(const RowsArgs& a, uint64_t t0, int t
   __syncthreads();
 }
 
+// rows[place_j] = x, for all j: the token is read once.  Bound by DRAM: 8192 x
+// 4096 bf16, 8 picks, 92 us, 6.5 TB/s.  SHIFT (rows at any address): 4096 x 2049
+// bf16, 8 picks, 32 us, 4.7 TB/s, by 2-byte accesses 65.
 template <typename T, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
@@ -198,7 +201,8 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const __grid_cons
 
 // y = sum over j of w_j rows[place_j], in binary32, ascending j: J rows of U
 // tokens are in flight in each thread.  Four CTAs per SM: with the registers
-// that the compiler takes by itself (32), it spreads the loads out again.
+// that the compiler takes by itself (32), it spreads the loads out again.  Bound
+// by DRAM: 8192 x 4096 bf16, 4 / 6 / 8 picks, 52 / 71 / 89 us, 6.5 to 6.8 TB/s.
 template <typename T, int U, int J>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
@@ -383,7 +387,8 @@ __global__ void __launch_bounds__(kRowThreads) combine_bulk_kernel(const __grid_
 // grad_rows[place_j] = w_j dy, grad_w_j = <rows[place_j], dy>: dy is read once
 // for J picks, and J rows are in flight in each thread.  The products' parts
 // are joined in a fixed order, by lanes and then by warps.  Rows are stored
-// evict-first: as ordinary stores they cost a third more.
+// evict-first: as ordinary stores they cost a third more.  Bound by DRAM: 8192 x
+// 2048 bf16, 6 picks, 69 us, 6.3 TB/s (with 80 registers 75, with 128 94).
 template <typename T, int J>
 __global__ void __launch_bounds__(kRowThreads, 4) combine_grad_kernel(const __grid_constant__ RowsArgs a, int tpt) {
   op_wait();
@@ -440,7 +445,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_grad_kernel(const __gr
   }
 }
 
-// The same for rows that are not 16-byte aligned: one warp for each pick.
+// The same for rows that are not 16-byte aligned: one warp for each pick.  3001 x
+// 1537 binary32, 6 picks, 57 us, 4.2 TB/s: every granule is asked for twice, and
+// more of them in flight only push each other out of the L1 (68 us with four).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) combine_grad_shift_kernel(const __grid_constant__ RowsArgs a) {
   op_wait();

@@ -261,7 +261,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 // With s the scores, S the sum of the picked ones (+ 1e-20) and dw the
 // weights' gradient, ds_j = scale (dw_j - sum_l dw_l s_l / S) / S, or scale
 // dw_j without renormalising.  Softmax: dx_i = s_i (ds_i - sum_j s_j ds_j);
-// sigmoid: dx_i = ds_i s_i (1 - s_i).  The bias only chooses: no gradient.
+// sigmoid: dx_i = ds_i s_i (1 - s_i).  The bias only chooses: no gradient.  One
+// warp per token as in the forward pass; the picks' parts are added to the lanes
+// that hold their experts.  At 8191 x 60 bf16, 4 picks, 5 us: 2 MB in all, so two
+// round trips and the launch.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteArgs a, int vec) {
   op_wait();

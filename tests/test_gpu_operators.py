@@ -732,3 +732,27 @@ def test_tables_in_pinned_host_memory(h):
     out = torch.empty(5, 32, device=DEV)
     purlin.embed(table, tokens, out, h)
     assert torch.equal(out.cpu(), torch.cat([table[[3, 49]], torch.zeros(1, 32), table[[0, 3]]]))
+
+
+@pytest.mark.parametrize("D", [64, 801])
+def test_rows_in_pinned_host_memory(h, D):
+    places = O.plan(np.tile(np.arange(4), (20, 1)), 4)[1]
+    x = torch.randn(20, D)
+    rows, y = torch.empty(80, D).pin_memory(), torch.empty(20, D).pin_memory()
+    purlin.dispatch_rows(x.pin_memory(), ints(places), rows, h)
+    torch.cuda.synchronize()
+    assert np.array_equal(rows.numpy(), O.dispatch(x.numpy(), places))
+    purlin.combine_rows(rows, ints(places), torch.full((20, 4), 0.25, device=DEV), y, h)
+    torch.cuda.synchronize()
+    assert torch.equal(y, x)            # four quarters of one value are exact
+
+
+@pytest.mark.parametrize("n", [100, 30000])
+def test_embed_gradient_of_32_bit_tokens(h, n):
+    g = torch.Generator(device=DEV).manual_seed(8)
+    tokens = torch.randint(-5, 205, (n,), generator=g, device=DEV)
+    dy = torch.randn(n, 40, generator=g, device=DEV)
+    wide, narrow = torch.empty(200, 40, device=DEV), torch.empty(200, 40, device=DEV)
+    purlin.embed_grad(dy, tokens, wide, h)
+    purlin.embed_grad(dy, tokens.to(torch.int32), narrow, h)
+    assert torch.equal(wide, narrow)
