@@ -766,7 +766,7 @@ const char* purlin_status_string(purlin_status s) {
     case PL_ERR_WORKSPACE: return "workspace too small";
     case PL_ERR_CUDA: return "CUDA runtime error";
     case PL_ERR_LAUNCH: return "kernel launch failed";
-    case PL_ERR_TIMEOUT: return "a SNAC wait on the device ran out of time";
+    case PL_ERR_TIMEOUT: return "a wait on the device ran out of time";
     case PL_ERR_FINALIZED: return "handle already finalized";
     case PL_ERR_BOUNDS: return "a place outside an operator's rows, or (checking build) a work item outside a rank buffer";
   }

@@ -77,7 +77,7 @@ typedef enum {
   PL_ERR_WORKSPACE = 4,    /* caller-provided workspace too small for this call */
   PL_ERR_CUDA = 5,         /* a CUDA runtime call failed */
   PL_ERR_LAUNCH = 6,       /* the kernel could not be launched */
-  PL_ERR_TIMEOUT = 7,      /* device: a SNAC consume wait gave up */
+  PL_ERR_TIMEOUT = 7,      /* device: a wait (SNAC consume, an operator's bulk copies) gave up */
   PL_ERR_FINALIZED = 8,    /* the handle was finalized */
   PL_ERR_BOUNDS = 9        /* device: a place outside an operator's rows; in the checking build also
                               a work item that reached outside a rank buffer */
