@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) combine_grad_kernel(const __gr
     if (on && first < J && j0 + first < k) {
       float s = 0.f;
       for (int q = 0; q < tpt / 32; ++q) s += part[group * (tpt / 32) + q][first];
-      a.grad_weights[t * k + j0 + first] = s;
+      // a dropped pick's row went in as zeros, whose product with an infinite dy is NaN
+      a.grad_weights[t * k + j0 + first] = picks.row[group * k + j0 + first] >= 0 ? s : 0.f;
     }
     __syncthreads();
   }

@@ -1,0 +1,43 @@
+"""Values, handles and buffers at the edges of what the operators' header allows.
+
+Bounds as in test_gpu_operators.py."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators as O
+from collective_datapath_reduce_gb300 import torch_api as purlin
+from test_gpu_operators import DEV, DTYPES, E24, U, Guarded, close, h, ints, make  # noqa: F401 (h: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# widths of whole vectors at aligned addresses, and odd ones
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D,k", [(64, 3), (2048, 12), (67, 3), (801, 12)])
+def test_combine_gradient_of_a_dropped_pick_is_zero_whatever_the_token_holds(h, D, k, dtype):
+    rng = np.random.default_rng(D)
+    T = 5
+    ids = np.stack([rng.permutation(16)[:k] for _ in range(T)])
+    ids[1, 0] = ids[1, k - 1] = ids[3, 1] = -1
+    ids[4] = -1
+    places = O.plan(ids, 16)[1]
+    r, r64 = make(rng.standard_normal((T * k, D)), dtype)
+    w, w64 = make(rng.standard_normal((T, k)), torch.float32)
+    dy, dy64 = make(rng.standard_normal((T, D)), dtype)
+    dy[1, D // 2], dy[3, 0], dy[4, D - 1] = math.inf, math.nan, -math.inf
+    dr, dw = Guarded(T * k, D, dtype), Guarded(T, k, torch.float32)
+    purlin.combine_rows_grad(r, ints(places), w, dy, dr.view, dw.view, h)
+    dropped = torch.from_numpy(places < 0).to(DEV)
+    assert (dw.view[dropped] == 0).all()
+    assert (dr.view[torch.from_numpy(~places[places < 0]).to(DEV)] == 0).all()
+    assert not torch.isfinite(dw.view[[1, 3]][~dropped[[1, 3]]]).any()      # picks that are not dropped follow the formula
+    want_r, want_w = O.combine_grad(r64, places, w64, dy64)
+    size = O.combine_grad(np.abs(r64), places, np.abs(w64), np.abs(dy64))[1]
+    close(dw.view[[0, 2]], want_w[[0, 2]], size[[0, 2]] * (D + 2) * E24)
+    at = places[[0, 2]].ravel()
+    close(dr.view[torch.from_numpy(at).to(DEV)], want_r[at], np.abs(want_r[at]) * (U[dtype] + 2 * E24))
+    assert dr.intact() and dw.intact()
