@@ -5,7 +5,7 @@
 // Purlin 0.6.5 (PyPI page), "Host-side": create one context per communicator
 // with a workspace of staging and signal buffers, run collectives on a
 // stream, finalize after the last one.  Here the context owns the SNAC flag
-// array and a status word, and caches one plan per call shape.
+// array and status words, and caches one plan per call shape.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -56,6 +56,7 @@ struct purlin_ctx {
   bool ws_owned = false;
   int ws_grown = 0;             // times the library-owned workspace was enlarged
   uint32_t* ctl = nullptr;
+  uint32_t* op_status = nullptr;  // device status word of the operators (ops.h)
   uint32_t* flags = nullptr;
   size_t flag_cap = 0;
   std::mutex mu;
@@ -430,6 +431,21 @@ purlin_status check_handle(purlin_ctx* h) {
   return g_dead.count(h) ? PL_ERR_FINALIZED : PL_ERR_INVALID_ARG;
 }
 
+// The collectives' or else the operators' pending device error; clears both.
+cudaError_t take_status(purlin_ctx* h, uint32_t* status) {
+  uint32_t* const words[2] = {h->ctl + pl::kCtlStatus, h->op_status};
+  *status = 0;
+  for (uint32_t* w : words) {
+    uint32_t v = 0;
+    const uint32_t zero = 0;
+    cudaError_t e = cudaMemcpy(&v, w, sizeof v, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && v) e = cudaMemcpy(w, &zero, sizeof zero, cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return e;
+    if (!*status) *status = v;
+  }
+  return cudaSuccess;
+}
+
 purlin_status check_ptrs(const void* const* p, int n) {
   if (!p) return PL_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i)
@@ -477,7 +493,7 @@ purlin_status op_begin(purlin_handle h, OpHandle* out) {
   if (cur != h->device) return PL_ERR_INVALID_ARG;
   out->device = h->device;
   out->sm_count = h->sm_count;
-  out->status = h->ctl + kCtlStatus;
+  out->status = h->op_status;
   return PL_OK;
 }
 
@@ -543,9 +559,15 @@ purlin_status purlin_initialize(int world, void* workspace, size_t workspace_byt
   h->ctl = (uint32_t*)h->ws;
   h->flags = (uint32_t*)((char*)h->ws + pl::kCtlBytes);
   h->flag_cap = (h->ws_bytes - pl::kCtlBytes) / sizeof(uint32_t);
-  if ((e = cudaMemsetAsync(h->ws, 0, h->ws_bytes, s)) != cudaSuccess ||
+  // The operators' word is not the workspace's: the collectives stop at an
+  // error in theirs, and the workspace moves when it grows, while a captured
+  // operator keeps the address.
+  if ((e = cudaMalloc(&h->op_status, sizeof(uint32_t))) != cudaSuccess ||
+      (e = cudaMemsetAsync(h->op_status, 0, sizeof(uint32_t), s)) != cudaSuccess ||
+      (e = cudaMemsetAsync(h->ws, 0, h->ws_bytes, s)) != cudaSuccess ||
       (e = cudaStreamSynchronize(s)) != cudaSuccess) {
     if (h->ws_owned) cudaFree(h->ws);
+    cudaFree(h->op_status);
     return cuda_fail(e);
   }
   {
@@ -568,11 +590,11 @@ purlin_status purlin_finalize(purlin_handle h, purlin_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) result = cuda_fail(e);
   uint32_t status = 0;
-  if (cudaMemcpy(&status, h->ctl, sizeof status, cudaMemcpyDeviceToHost) == cudaSuccess && status)
-    result = (purlin_status)status;
+  if (take_status(h, &status) == cudaSuccess && status) result = (purlin_status)status;
   for (auto& kv : h->plans) free_plan(kv.second.get());
   h->plans.clear();
   if (h->ws_owned && h->ws) cudaFree(h->ws);
+  cudaFree(h->op_status);
   h->ws = nullptr;
   h->finalized = true;
   delete h;
@@ -747,12 +769,7 @@ purlin_status purlin_status_get(purlin_handle h, purlin_stream_t stream, int* de
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e);
   uint32_t v = 0;
-  if ((e = cudaMemcpy(&v, h->ctl, sizeof v, cudaMemcpyDeviceToHost)) != cudaSuccess) return cuda_fail(e);
-  if (v) {
-    const uint32_t zero = 0;
-    if ((e = cudaMemcpy(h->ctl, &zero, sizeof zero, cudaMemcpyHostToDevice)) != cudaSuccess)
-      return cuda_fail(e);
-  }
+  if ((e = take_status(h, &v)) != cudaSuccess) return cuda_fail(e);
   *device_status = (int)v;
   return PL_OK;
 }

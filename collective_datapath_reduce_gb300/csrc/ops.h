@@ -16,7 +16,7 @@ namespace pl {
 struct OpHandle {
   int device = 0;
   int sm_count = 0;
-  uint32_t* status = nullptr;  // device status word
+  uint32_t* status = nullptr;  // the operators' device status word
 };
 
 // The handle is live and its device is current (api.cpp).

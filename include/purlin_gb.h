@@ -320,7 +320,9 @@ purlin_status purlin_atom_reduce(purlin_handle h, const void* const* src, int ns
  *     them between calls, and the handle's own workspace is not used, so
  *     these calls need no order among each other.
  *   - Indices are read on the device and checked there: each operator says
- *     what one outside its range does.  None is followed out of a buffer. */
+ *     what one outside its range does.  None is followed out of a buffer.
+ *   - What an operator finds wrong on the device has a status word of its own,
+ *     which purlin_status_get reads too: it stops no collective. */
 #define PURLIN_MAX_EXPERTS 1024
 #define PURLIN_MAX_TOP_K 32
 #define PURLIN_MAX_GROUPS 32
@@ -437,7 +439,9 @@ purlin_status purlin_clip_grad_norm(purlin_handle h, const void* const* grads, v
 
 /* Wait for `stream`'s queued work, then report (and clear) the first error
  * recorded on the device since the last call: *device_status = PL_OK,
- * PL_ERR_TIMEOUT or PL_ERR_BOUNDS.  Returns PL_OK when the query itself worked. */
+ * PL_ERR_TIMEOUT or PL_ERR_BOUNDS.  Where the collectives and the operators
+ * each recorded one, the collectives' is reported, and both are cleared.
+ * Returns PL_OK when the query itself worked. */
 purlin_status purlin_status_get(purlin_handle h, purlin_stream_t stream, int* device_status);
 
 const char* purlin_status_string(purlin_status s);
