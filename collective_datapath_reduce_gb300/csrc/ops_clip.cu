@@ -137,9 +137,10 @@ __device__ __forceinline__ double block_sum(double s, double* tmp) {
 // The factor, given the sum of squares; one thread writes the norm.
 template <int M>
 __device__ __forceinline__ float factor_of(const Table<M>& a, double sum, bool tell) {
-  // binary64 square roots take long: only where the sum is outside binary32
-  const float root = sum > 1e-30 && sum < 1e38 ? __fsqrt_rn((float)sum) : (float)sqrt(sum);
-  const float norm = root * fabsf(a.scale);
+  // binary64 square roots take long: only where the sum is outside binary32,
+  // and then the scale too is applied before the rounding, which it may decide
+  const float norm = sum > 1e-30 && sum < 1e38 ? __fsqrt_rn((float)sum) * fabsf(a.scale)
+                                               : (float)(sqrt(sum) * (double)fabsf(a.scale));
   if (tell) *a.norm = norm;
   if (isinf(a.max_norm)) return a.scale;
   const float f = __fdiv_rn(a.max_norm, norm + 1e-6f);

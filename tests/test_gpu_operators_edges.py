@@ -41,3 +41,18 @@ def test_combine_gradient_of_a_dropped_pick_is_zero_whatever_the_token_holds(h, 
     at = places[[0, 2]].ravel()
     close(dr.view[torch.from_numpy(at).to(DEV)], want_r[at], np.abs(want_r[at]) * (U[dtype] + 2 * E24))
     assert dr.intact() and dw.intact()
+
+
+@pytest.mark.parametrize("n", [100, 300000])
+def test_clip_of_a_norm_that_only_its_scale_brings_into_range(h, n):
+    """The gradients' own norm is past binary32, scale times it is not."""
+    g, v = make(np.random.default_rng(2).uniform(-1.0, 1.0, (1, n)) * 3e38, torch.float32)
+    assert float(np.linalg.norm(v)) > 3.5e38
+    norm, out = torch.empty(1, device=DEV), Guarded(1, n, torch.float32)
+    purlin.clip_grad_norm([g[0]], [out.view[0]], 1e3, norm, h, scale=2.0 ** -10)
+    want, want_norm = O.clip([v[0]], 1e3, 2.0 ** -10)
+    assert abs(norm.item() - want_norm) <= want_norm * 4 * E24          # all in 64 bits, rounded to 32
+    # the factor is 1000 / the norm times the scale, above 1e-37: a binary32 value like any
+    close(out.view[0], want[0], np.abs(want[0]) * (U[torch.float32] + 12 * E24))
+    purlin.clip_grad_norm([g[0]], None, 1e3, norm, h, scale=0.0)
+    assert norm.item() == 0.0
