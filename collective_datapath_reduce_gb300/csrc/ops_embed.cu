@@ -298,6 +298,30 @@ __device__ __forceinline__ void finish(const SumArgs& a, uint64_t row, uint64_t 
   st_pack_once<TY, N>((TY*)a.e.y + row * a.e.ldy + c, o);
 }
 
+// N binary32 sums of the workspace, which is 16-byte aligned and no more: in
+// accesses of at most 16 bytes.
+template <int N>
+__device__ __forceinline__ void st_part(float* part, const float (&acc)[N]) {
+  constexpr int W = N < 4 ? N : 4;
+#pragma unroll
+  for (int q = 0; q < N; q += W) {
+    Pack<float, W> o;
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.v[i] = acc[q + i];
+    st_pack<float, W>(part + q, o);
+  }
+}
+template <int N>
+__device__ __forceinline__ void ld_part(const float* part, float (&x)[N]) {
+  constexpr int W = N < 4 ? N : 4;
+#pragma unroll
+  for (int q = 0; q < N; q += W) {
+    const Pack<float, W> r = *reinterpret_cast<const Pack<float, W>*>(part + q);
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[q + i] = r.v[i];
+  }
+}
+
 // One run's columns by one thread for each vector: 8 of the run's rows in flight,
 // added in the order of their places, and a token's sum written when its places
 // end.  Runs of equal length share out the tokens that occur often.  Bound by
@@ -349,11 +373,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const __grid_constant_
       if (!head && !more) {
         finish<TY, N>(a, k, c, acc);
       } else {
-        float* part = a.part + (run * 2 + (head ? 0 : 1)) * a.e.width + c;
-        Pack<float, N> o;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o.v[i] = acc[i];
-        st_pack<float, N>(part, o);
+        st_part<N>(a.part + (run * 2 + (head ? 0 : 1)) * a.e.width + c, acc);
       }
       head = false;
 #pragma unroll
@@ -385,18 +405,15 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(const __grid_constant
   if (c >= a.e.width) return;
   float acc[N];
   const float* part = a.part + (run * 2 + 1) * a.e.width + c;
-  {
-    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(part);
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = x.v[i];
-  }
+  ld_part<N>(part, acc);
   part += a.e.width;
   const uint32_t heads = reach;
 #pragma unroll 16
   for (uint32_t r = 0; r < heads; ++r) {
-    const Pack<float, N> x = *reinterpret_cast<const Pack<float, N>*>(part + (uint64_t)r * 2 * a.e.width);
+    float x[N];
+    ld_part<N>(part + (uint64_t)r * 2 * a.e.width, x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] += x.v[i];
+    for (int i = 0; i < N; ++i) acc[i] += x[i];
   }
   finish<TY, N>(a, k, c, acc);
 }

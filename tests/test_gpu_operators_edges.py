@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from oracle import operators as O
+from collective_datapath_reduce_gb300 import purlin as P
 from collective_datapath_reduce_gb300 import torch_api as purlin
 from test_gpu_operators import DEV, DTYPES, E24, U, Guarded, close, h, ints, make  # noqa: F401 (h: a fixture)
 
@@ -56,3 +57,31 @@ def test_clip_of_a_norm_that_only_its_scale_brings_into_range(h, n):
     close(out.view[0], want[0], np.abs(want[0]) * (U[torch.float32] + 12 * E24))
     purlin.clip_grad_norm([g[0]], None, 1e3, norm, h, scale=0.0)
     assert norm.item() == 0.0
+
+
+@pytest.mark.parametrize("dtypes", [(x, t) for x in DTYPES for t in DTYPES], ids=str)
+@pytest.mark.parametrize("n,D", [(300, 2304), (9000, 64)])
+def test_embed_gradient_with_a_workspace_that_is_just_16_byte_aligned(h, n, D, dtypes):
+    """What the header asks of the workspace; several runs, so that parts of sums go through it."""
+    R, s = 40, torch.cuda.current_stream().cuda_stream
+    g = torch.Generator(device=DEV).manual_seed(n)
+    dy = torch.randn(n, D, generator=g, device=DEV).to(dtypes[0])
+    tokens = torch.randint(0, R, (n,), generator=g, device=DEV)
+    tokens[::2] = 7
+    kinds = [P.PL_F32 if t is torch.float32 else P.PL_BF16 for t in dtypes]
+    need = P.purlin_embed_grad_bytes(n, R, D)
+    raw = torch.full((need + 128,), 0xA5, dtype=torch.uint8, device=DEV)
+    assert raw.data_ptr() % 32 == 0
+    outs = []
+    for off in (32, 48):
+        out = Guarded(R, D, dtypes[1])
+        ws = raw[off:off + need]
+        assert P.purlin_embed_grad(h.raw, dy, D, kinds[0], tokens, 8, n, D, 1.0, None, 0, out.view, D, kinds[1], R, 0, ws,
+                                   need, s) == P.PL_OK
+        assert out.intact() and (raw[:off] == 0xA5).all() and (raw[off + need:] == 0xA5).all()
+        raw.fill_(0xA5)
+        outs.append(out.view)
+    assert torch.equal(outs[0], outs[1])
+    want = O.embed_grad(dy.double().cpu().numpy(), tokens.cpu().numpy(), R)
+    size = O.embed_grad(dy.double().abs().cpu().numpy(), tokens.cpu().numpy(), R)
+    close(outs[1], want, np.abs(want) * (U[dtypes[1]] + E24) + size * (n + 2) * E24)
