@@ -249,22 +249,32 @@ def _two(t, what, name):
 
 
 def _workspace(nbytes, stream, handle):
-    """At least nbytes of device memory for a call on `stream`.  The handle keeps
-    one block for each stream, used by that stream's calls one after the other;
-    it comes from torch's allocator on the same stream, so a block that is
-    replaced by a larger one is not handed on before its calls are done.  A
-    captured graph gets a block of its own, since it may replay anywhere."""
+    """At least nbytes of device memory for a call on `stream`, taken with that
+    stream current."""
     if nbytes == 0:
         return None
     device = handle.device
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     index = device.index if device.index is not None else torch.cuda.current_device()
-    key = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    key = current if stream is None else _stream(stream, device)
+    if key == current and torch.cuda.current_device() == index:
+        return _block(nbytes, key, handle)
+    with torch.cuda.stream(torch.cuda.ExternalStream(key, device=device)):
+        return _block(nbytes, key, handle)
+
+
+def _block(nbytes, key, handle):
+    """The handle keeps one block for each stream, the largest that a call
+    needed, until it is finalised; that stream's calls use it one after the
+    other.  It comes from torch's allocator on the same stream, so a block that
+    is replaced by a larger one is not handed on before its calls are done.  A
+    captured call gets a block of its own, since the graph may replay anywhere:
+    the graph's pool hands it on to later calls on the same stream only."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=handle.device)
     kept = handle.workspaces.get(key)
     if kept is None or kept.numel() < nbytes:
-        with torch.cuda.stream(torch.cuda.ExternalStream(key, device=device)):
-            kept = handle.workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        kept = handle.workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=handle.device)
     return kept
 
 
