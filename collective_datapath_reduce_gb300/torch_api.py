@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import enum
 import operator
+import threading
 
 import torch
 
@@ -35,6 +36,7 @@ class Handle:
     def __init__(self, raw, world, device):
         self.raw, self.world, self.device = raw, world, device
         self.workspaces = {}  # of the operators, by stream
+        self.lock = threading.RLock()  # held from taking one of them until the call's launches are queued
 
     def __repr__(self):
         return f"purlin.Handle(world={self.world}, device={self.device})"
@@ -201,7 +203,8 @@ def reduce_scatter_v(xs, outs, counts, handle: Handle, stream=None, reduction_mo
 # Outputs are the caller's, as for the collectives.  Matrices are 2-D tensors
 # whose rows are packed (the last stride is 1) and any stride apart; vectors,
 # picks and places are contiguous.  Workspaces come from torch's allocator and
-# are kept by the handle, one for each stream.
+# are kept by the handle, one for each stream.  Threads may call the operators
+# on one handle at once.
 
 def _values(t, what):
     dt = _DTYPES.get(t.dtype)
@@ -291,6 +294,13 @@ def _call(fn, what, handle, stream, *args):
     _check(fn(handle.raw, *args, stream), what)
 
 
+def _call_in_workspace(fn, what, handle, stream, nbytes, *args):
+    """_call with a workspace and its size behind args.  A call is several
+    launches on one block, so no other thread's may come between them."""
+    with handle.lock:
+        _call(fn, what, handle, stream, *args, _workspace(nbytes, stream, handle), nbytes)
+
+
 def route_experts(logits, ids, weights, handle: Handle, bias=None, scores=Scores.SOFTMAX, groups=1, kept_groups=1,
                   group_best=1, renormalise=True, scale=1.0, stream=None):
     """ids[t, j], weights[t, j] = token t's j-th best expert and its weight.
@@ -347,8 +357,7 @@ def expert_plan(ids, offsets, places, handle: Handle, stream=None):
     _packed(places, (T, k), torch.int32, what, "places")
     _packed(offsets, (E + 1,), torch.int32, what, "offsets")
     nbytes = P.purlin_expert_plan_bytes(T, k, E)
-    ws = _workspace(nbytes, stream, handle)
-    _call(P.purlin_expert_plan, what, handle, stream, ids, T, k, E, offsets, places, ws, nbytes)
+    _call_in_workspace(P.purlin_expert_plan, what, handle, stream, nbytes, ids, T, k, E, offsets, places)
 
 
 def dispatch_rows(x, places, rows, handle: Handle, stream=None):
@@ -428,9 +437,8 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
     ldt = _matrix(grad_table, R, D, grad_table.dtype, what, "grad_table")
     ldb = _matrix(base, R, D, grad_table.dtype, what, "base") if base is not None else 0
     nbytes = P.purlin_embed_grad_bytes(n, R, D)
-    ws = _workspace(nbytes, stream, handle)
-    _call(P.purlin_embed_grad, what, handle, stream, grad_out, ldx, dx, tokens, size, n, D, scale, base, ldb, grad_table,
-          ldt, dt, R, int(first), ws, nbytes)
+    _call_in_workspace(P.purlin_embed_grad, what, handle, stream, nbytes, grad_out, ldx, dx, tokens, size, n, D, scale,
+                       base, ldb, grad_table, ldt, dt, R, int(first))
 
 
 _numel, _data_ptr, _is_contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
@@ -457,6 +465,5 @@ def clip_grad_norm(grads, outs, max_norm, norm, handle: Handle, scale=1.0, strea
         if outs is not None and outs is not grads and list(map(_numel, outs)) != counts:
             raise ValueError(f"{what}: each output must have its gradient's size")
     nbytes = P.purlin_clip_grad_norm_bytes()
-    ws = _workspace(nbytes, stream, handle)
-    _call(P.purlin_clip_grad_norm, what, handle, stream, list(map(_data_ptr, grads)),
-          None if outs is None else list(map(_data_ptr, outs)), counts, dt, scale, max_norm, norm, ws, nbytes)
+    _call_in_workspace(P.purlin_clip_grad_norm, what, handle, stream, nbytes, list(map(_data_ptr, grads)),
+                       None if outs is None else list(map(_data_ptr, outs)), counts, dt, scale, max_norm, norm)

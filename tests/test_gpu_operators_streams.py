@@ -1,5 +1,7 @@
 """Operators with workspaces on streams that the caller names, captured and eager, against the same calls in order."""
 
+import threading
+
 import pytest
 import torch
 
@@ -81,3 +83,28 @@ def test_a_captured_stream_that_is_not_current(h):
     for _ in range(2):
         graph.replay()
         same(job.taken(), want)
+
+
+def test_threads_on_one_stream(h):
+    jobs = [Job(n, n) for n in (30000, 50000, 40000, 60000)]
+    wants = []
+    for j in jobs:
+        j.run(h)
+        wants.append(j.taken())
+    start, failures = threading.Barrier(len(jobs)), []
+
+    def work(job):
+        try:
+            start.wait()
+            for _ in range(10):
+                job.run(h)
+        except Exception as e:  # told to the main thread
+            failures.append(e)
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failures
+    torch.cuda.synchronize()
+    got = [j.taken() for j in jobs]
+    for g, want in zip(got, wants):
+        same(g, want)

@@ -1,6 +1,8 @@
 """Which block of memory an operator's call works in: by its own stream, whatever stream is current (CPU)."""
 
 import contextlib
+import threading
+import time
 import types
 
 import pytest
@@ -78,3 +80,32 @@ def test_one_block_for_each_stream_that_grows(cuda, h):
     c = purlin._workspace(101, 1, h)
     assert c is not a and cuda.allocated_on(c) == 1 and purlin._workspace(100, None, h) is c
     assert purlin._workspace(100, 2, h) is b
+
+
+def test_threads_on_one_stream_do_not_share_a_block_in_the_middle_of_a_call(cuda, h, monkeypatch):
+    """A call is several launches: another thread's between them may not use the same block."""
+    busy, clashes, calls = set(), [], []
+
+    def plan(raw, ids, tokens, top_k, experts, offsets, places, ws, nbytes, stream):
+        if id(ws) in busy:
+            clashes.append(threading.get_ident())
+        busy.add(id(ws))
+        time.sleep(0.02)                  # as the library does, without the interpreter's lock
+        busy.discard(id(ws))
+        calls.append(stream)
+        return 0
+
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(purlin.P, "purlin_expert_plan_bytes", lambda *a: 64)
+    monkeypatch.setattr(purlin.P, "purlin_expert_plan", plan)
+    ids, offsets, places = (torch.zeros(s, dtype=torch.int32) for s in ((8, 2), 5, (8, 2)))
+    start = threading.Barrier(4)
+
+    def work():
+        start.wait()
+        for _ in range(3):
+            purlin.expert_plan(ids, offsets, places, h)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(calls) == 12 and not clashes
