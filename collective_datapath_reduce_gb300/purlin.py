@@ -13,6 +13,7 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import operator
 import os
 import re
 
@@ -289,11 +290,20 @@ def purlin_all_reduce_noalloc(world, src, dst, bytes_per_rank, dtype, device_sta
                                             _addr(device_status) or None, _stream(stream))
 
 
+_index = operator.index
+
+
 @functools.lru_cache(maxsize=256)
+def _routing(*values) -> purlin_routing:
+    return purlin_routing(*values)
+
+
 def make_routing(experts, top_k, scores=PL_SCORES_SOFTMAX, groups=1, kept_groups=1, group_best=1, renormalise=True,
                  scale=1.0) -> purlin_routing:
-    """The C struct; one for all calls with the same arguments, so not to be written to."""
-    return purlin_routing(experts, top_k, int(scores), groups, kept_groups, group_best, int(renormalise), scale)
+    """The C struct; one for all calls with the same values, so not to be written to."""
+    # plain numbers: a tensor would be told from another by its identity, whatever it holds by then
+    return _routing(_index(experts), _index(top_k), int(scores), _index(groups), _index(kept_groups), _index(group_best),
+                    int(renormalise), float(scale))
 
 
 def purlin_route_experts(h, logits, stride, dtype, bias, tokens, routing, ids, weights, stream=None) -> int:
