@@ -198,7 +198,7 @@ def _addr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return x.data_ptr()
+    return int(x.data_ptr())
 
 
 def _addresses(seq):

@@ -29,3 +29,23 @@ def test_routing_takes_each_kind_of_number():
 def test_routing_refuses_what_is_no_such_number(kw):
     with pytest.raises((TypeError, ValueError)):
         P.make_routing(8, 2, **kw)
+
+
+class Buffer:
+    """An object with data_ptr() that is not a tensor's."""
+
+    def __init__(self, address):
+        self.address = address
+
+    def data_ptr(self):
+        return self.address
+
+
+@pytest.mark.parametrize("kind", [int, np.int64, np.uint64])
+def test_addresses_of_any_kind_of_whole_number(kind):
+    at = [Buffer(kind(4096 * (i + 1))) for i in range(2)]
+    assert list(P._ptr_array(at)) == [4096, 8192]
+    assert P._addr(at[0]) == 4096 and type(P._addr(at[0])) is int
+    # on its way to the library, which is told of no handle
+    assert P.purlin_all_reduce(None, at, at, 16, P.PL_F32) == P.PL_ERR_INVALID_ARG
+    assert P.purlin_atom_copy(None, at[0], at[1:], 16) == P.PL_ERR_INVALID_ARG
