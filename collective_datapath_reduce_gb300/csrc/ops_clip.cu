@@ -83,11 +83,12 @@ __device__ __forceinline__ void walk(const T* p, bool aligned, uint64_t e0, uint
 }
 
 // Squares of elements [e0, e1) at p, this thread's part: in binary32, or, where
-// they do not fit (or are not numbers), once more in binary64.
-template <int THREADS, int F, typename T>
+// they do not fit (or are not numbers), once more in binary64.  HOW: kWritten
+// where the same kernel writes in place later.
+template <int THREADS, int F, Ld HOW, typename T>
 __device__ __forceinline__ double squares(const T* p, uint64_t e0, uint64_t e1) {
   float s = 0.f;
-  walk<THREADS, F, Ld::kOnce, T>(
+  walk<THREADS, F, HOW, T>(
       p, true, e0, e1,
       [&](const auto& x, uint64_t, bool) {  // zeros where there is none
 #pragma unroll
@@ -96,7 +97,7 @@ __device__ __forceinline__ double squares(const T* p, uint64_t e0, uint64_t e1) 
       [&](uint64_t i) { s = __fmaf_rn(to_f32(p[i]), to_f32(p[i]), s); });
   if (s <= 1e38f) return (double)s;
   double w = 0.0;
-  walk<THREADS, 1, Ld::kOnce, T>(
+  walk<THREADS, 1, HOW, T>(
       p, true, e0, e1,
       [&](const auto& x, uint64_t, bool) {
         for (int k = 0; k < 16 / (int)sizeof(T); ++k) w += (double)to_f32(x.v[k]) * (double)to_f32(x.v[k]);
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) squares_kernel(const __grid_const
   for (uint32_t c = c0; c < c1; ++c) {
     while (c >= a.first[t + 1]) ++t;
     const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk;
-    sum += squares<kThreads, 8>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kChunk));
+    sum += squares<kThreads, 8, Ld::kOnce>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kChunk));
   }
   sum = block_sum<kThreads>(sum, tmp);
   if (threadIdx.x == 0) a.parts[a.part0 + blockIdx.x] = sum;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kSmallThreads) clip_small_kernel(const __grid_
   for (uint32_t c = warp; c < chunks; c += kSmallThreads / 32) {
     const int t = tensor_of(a, c);
     const uint64_t e0 = (uint64_t)(c - a.first[t]) * kSmallChunk;
-    sum += squares<32, F>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kSmallChunk));
+    sum += squares<32, F, Ld::kWritten>((const T*)a.t[t].in, e0, min(a.t[t].n, e0 + kSmallChunk));
   }
   sum = block_sum<kSmallThreads>(sum, tmp);
   const float f = factor_of(a, sum, threadIdx.x == 0);

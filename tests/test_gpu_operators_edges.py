@@ -85,3 +85,28 @@ def test_embed_gradient_with_a_workspace_that_is_just_16_byte_aligned(h, n, D, d
     want = O.embed_grad(dy.double().cpu().numpy(), tokens.cpu().numpy(), R)
     size = O.embed_grad(dy.double().abs().cpu().numpy(), tokens.cpu().numpy(), R)
     close(outs[1], want, np.abs(want) * (U[dtypes[1]] + E24) + size * (n + 2) * E24)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes", [(5, 1, 300), (4001, 1025, 7, 16384), (40000, 3)])
+def test_clip_in_place_again_and_again(h, sizes, dtype):
+    """Each call reads what the one before wrote to the same place; elsewhere it gives the same bits."""
+    g = torch.Generator(device=DEV).manual_seed(sum(sizes))
+    flat = torch.randn(sum(sizes) + 64 * len(sizes), generator=g, device=DEV).to(dtype)
+    starts = [sum(sizes[:i]) + 3 * i for i in range(len(sizes))]      # any alignment
+    here = [flat[a:a + n] for a, n in zip(starts, sizes)]
+    there = [t.clone() for t in here]
+    norm, same = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    for _ in range(12):
+        purlin.clip_grad_norm(here, here, 0.5, norm, h, scale=1.5)
+        new = [torch.empty_like(t) for t in there]
+        before = sum(float((t.double() ** 2).sum()) for t in there) ** 0.5 * 1.5
+        purlin.clip_grad_norm(there, new, 0.5, same, h, scale=1.5)
+        there = new
+        # 32 squares at most are added in binary32 by one thread, the rest in 64 bits
+        assert abs(same.item() - before) <= before * (32 + 4) * E24
+        # the tensors lie at other addresses modulo 16 here, so their threads' shares differ
+        assert abs(norm.item() - same.item()) <= before * 2 * (32 + 4) * E24
+        for t, u in zip(here, there):
+            assert ((t.double() - u.double()).abs() <= u.double().abs() * (4 * U[dtype] + 200 * E24)).all()
+        there = [t.clone() for t in here]
