@@ -135,13 +135,15 @@ __device__ __forceinline__ double block_sum(double s, double* tmp) {
   return s;
 }
 
+// Apart, so that it is a call that is not made and no work whose result is not taken.
+__device__ __noinline__ float wide_norm(double sum, float size) { return (float)(sqrt(sum) * (double)size); }
+
 // The factor, given the sum of squares; one thread writes the norm.
 template <int M>
 __device__ __forceinline__ float factor_of(const Table<M>& a, double sum, bool tell) {
   // binary64 square roots take long: only where the sum is outside binary32,
   // and then the scale too is applied before the rounding, which it may decide
-  const float norm = sum > 1e-30 && sum < 1e38 ? __fsqrt_rn((float)sum) * fabsf(a.scale)
-                                               : (float)(sqrt(sum) * (double)fabsf(a.scale));
+  const float size = fabsf(a.scale), norm = sum > 1e-30 && sum < 1e38 ? __fsqrt_rn((float)sum) * size : wide_norm(sum, size);
   if (tell) *a.norm = norm;
   if (isinf(a.max_norm)) return a.scale;
   const float f = __fdiv_rn(a.max_norm, norm + 1e-6f);
