@@ -198,7 +198,8 @@ def _addr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    at = x.data_ptr()
+    return at if type(at) is int else int(at)
 
 
 def _addresses(seq):
@@ -302,8 +303,8 @@ def make_routing(experts, top_k, scores=PL_SCORES_SOFTMAX, groups=1, kept_groups
                  scale=1.0) -> purlin_routing:
     """The C struct; one for all calls with the same values, so not to be written to."""
     # plain numbers: a tensor would be told from another by its identity, whatever it holds by then
-    return _routing(_index(experts), _index(top_k), int(scores), _index(groups), _index(kept_groups), _index(group_best),
-                    int(renormalise), float(scale))
+    return _routing(_index(experts), _index(top_k), _index(scores), _index(groups), _index(kept_groups),
+                    _index(group_best), 1 if renormalise else 0, float(scale))
 
 
 def purlin_route_experts(h, logits, stride, dtype, bias, tokens, routing, ids, weights, stream=None) -> int:

@@ -253,14 +253,14 @@ def _two(t, what, name):
 
 def _workspace(nbytes, stream, handle):
     """At least nbytes of device memory for a call on `stream`, taken with that
-    stream current."""
+    stream current.  The handle's device is current already."""
     if nbytes == 0:
         return None
     device = handle.device
     index = device.index if device.index is not None else torch.cuda.current_device()
     current = torch._C._cuda_getCurrentRawStream(index)
     key = current if stream is None else _stream(stream, device)
-    if key == current and torch.cuda.current_device() == index:
+    if key == current:
         return _block(nbytes, key, handle)
     with torch.cuda.stream(torch.cuda.ExternalStream(key, device=device)):
         return _block(nbytes, key, handle)
@@ -297,8 +297,17 @@ def _call(fn, what, handle, stream, *args):
 def _call_in_workspace(fn, what, handle, stream, nbytes, *args):
     """_call with a workspace and its size behind args.  A call is several
     launches on one block, so no other thread's may come between them."""
+    if nbytes == 0:
+        return _call(fn, what, handle, stream, *args, None, 0)
+    index = handle.device.index
+    if index is None or torch.cuda.current_device() != index:
+        with _on(handle), handle.lock:
+            ws = _workspace(nbytes, stream, handle)
+            return _check(fn(handle.raw, *args, ws, nbytes, _stream(stream, handle.device)), what)
+    key = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, handle.device)
     with handle.lock:
-        _call(fn, what, handle, stream, *args, _workspace(nbytes, stream, handle), nbytes)
+        ws = _block(nbytes, key, handle) if stream is None else _workspace(nbytes, key, handle)
+        _check(fn(handle.raw, *args, ws, nbytes, key), what)
 
 
 def route_experts(logits, ids, weights, handle: Handle, bias=None, scores=Scores.SOFTMAX, groups=1, kept_groups=1,
