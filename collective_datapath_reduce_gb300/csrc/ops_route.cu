@@ -172,11 +172,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     }
   }
   // what counts for a group of the expert with this key: s + bias or the
-  // logit, or, of a sum of two without a bias, s (softmax: times the sum)
+  // logit, or, of a sum of two without a bias, s (softmax: times the sum, and
+  // +inf for a logit of +inf, whose s is none)
   const bool by_score = a.best == 2 && !a.bias;
   auto value = [&](float k) {
     if (!by_score || !(k > -INFINITY)) return k;
-    return a.sigmoid ? sigmoid(k) : expf(__fsub_rn(k, best));
+    return a.sigmoid ? sigmoid(k) : k == INFINITY ? k : expf(__fsub_rn(k, best));
   };
 
   if (a.groups > 1 && a.group_shift < 0) {

@@ -335,7 +335,8 @@ typedef enum { PL_SCORES_SOFTMAX = 0, PL_SCORES_SIGMOID = 1 } purlin_scores;
  * else by their logits, which are in the scores' order; equal ones by number.
  * With groups > 1 the experts stand in that many equal runs; a group counts as
  * its best expert (group_best 1) or as the sum of its two best (2; of s +
- * bias, or of s), and only the kept_groups best groups take part.  The top_k
+ * bias, or of s, where a logit of +inf counts as +inf in the softmax, which has
+ * no s for it), and only the kept_groups best groups take part.  The top_k
  * best experts are picked.  A pick's weight is scale x s, with renormalise
  * scale x s / (the sum of the picks' s + 1e-20). */
 typedef struct {

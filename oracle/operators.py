@@ -57,6 +57,8 @@ def route(logits, top_k, kind="softmax", bias=None, groups=1, kept_groups=1, gro
         note(key)
         if groups > 1:
             of = s if bias is None and group_best == 2 else key
+            if of is s and kind == "softmax":
+                of = np.where(key == np.inf, key, np.where(np.max(key) == np.inf, 0.0, s))  # the limit, as s has none
             value = [group_score(np.where(key[g * n:(g + 1) * n] > -np.inf, of[g * n:(g + 1) * n], -np.inf), group_best)
                      for g in range(groups)]
             note(value)

@@ -110,3 +110,24 @@ def test_clip_in_place_again_and_again(h, sizes, dtype):
         for t, u in zip(here, there):
             assert ((t.double() - u.double()).abs() <= u.double().abs() * (4 * U[dtype] + 200 * E24)).all()
         there = [t.clone() for t in here]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("E,groups,kept", [(32, 4, 4), (32, 4, 2), (60, 3, 3), (60, 3, 1), (256, 8, 8), (256, 8, 3), (1000, 5, 1),
+                                            (256, 32, 32), (256, 32, 5)])
+def test_route_keeps_the_group_of_an_infinite_logit(h, E, groups, kept, dtype):
+    """Without groups the expert is the first pick; its group counts as infinite, not as nothing."""
+    x = np.stack([np.random.default_rng(E + t).permutation(np.linspace(-3.0, 3.0, E)) for t in range(5)])
+    x[0, E // 2] = x[1, E - 1] = x[2, 0] = x[2, E // 3] = x[3, 5] = np.inf
+    xs, x64 = make(x, dtype)
+    for kind, scores in (("softmax", purlin.Scores.SOFTMAX), ("sigmoid", purlin.Scores.SIGMOID)):
+        for best in (1, 2):
+            ids, w = Guarded(5, 4, torch.int32), Guarded(5, 4, torch.float32)
+            purlin.route_experts(xs, ids.view, w.view, h, scores=scores, groups=groups, kept_groups=kept, group_best=best)
+            assert ids.intact() and w.intact()
+            want = O.route(x64, 4, kind, None, groups, kept, best)[0]
+            got = ids.view.cpu().numpy()
+            if kind == "softmax" or kept == groups or best == 1:
+                assert got[:, 0].tolist() == [E // 2, E - 1, 0, 5, int(np.argmax(x64[4])) if best == 1 or kept == groups else got[4, 0]]
+            assert np.array_equal(got, want), (kind, best)
+            assert torch.isnan(w.view[:4, 0]).all() == (kind == "softmax") and torch.isfinite(w.view[4]).all()
