@@ -105,9 +105,11 @@ __device__ __forceinline__ void snac_finish(const KArgs& a, uint32_t epoch, bool
 // previous kernel on the stream has retired its CTAs, without waiting for
 // the full completion of that grid; grid_dep_wait() returns once that kernel
 // has completed and its writes are visible (at once for a plain launch), so
-// every kernel calls it before it touches global memory.  No kernel triggers
-// its dependents early (griddepcontrol.launch_dependents): measured on a
-// GB300 that gained nothing over this.
+// every kernel calls it before it touches global memory.  No kernel of a
+// collective triggers its dependents early (griddepcontrol.launch_dependents):
+// measured on a GB300 that gained nothing over this.  Some operators' kernels do
+// (op_next), each after its own wait, so that a kernel launched behind one still
+// finds everything before it complete once grid_dep_wait() returns.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Checking build (PURLIN_DEBUG): true when every byte item `it` reads and

@@ -51,7 +51,7 @@ struct PlanArgs {
   int experts;
   int32_t* offsets;
   int32_t* places;
-  uint32_t* counts;  // workspace: one row of experts + 1 counts per CTA
+  uint32_t* counts;  // workspace: one row of `experts` counts per CTA
 };
 size_t expert_plan_bytes(uint64_t slots, int experts);
 purlin_status launch_expert_plan(const PlanArgs& a, cudaStream_t s);

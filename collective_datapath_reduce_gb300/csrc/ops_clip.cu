@@ -7,10 +7,11 @@
 // binary64.
 //
 // Past the L2 the values have to be read twice and written once: 238 M binary32
-// values in 180 tensors take 147 + 287 us, 6.5 and 6.6 TB/s.  Shares in one
-// piece for each CTA (300 us), evict-first stores (295 us) and the opposite
-// order (291 us) were no faster in the second kernel; in the first one, shares in
-// one piece beat strided ones (163 us) because a share looks its tensor up once.
+// values in 180 tensors take 138 + 290 us, 6.9 and 6.6 TB/s.  In the first
+// kernel shares in one piece for each CTA beat strided ones (163 us) because a
+// share looks its tensor up once; in the second they were slower (300 us).  Its
+// stores are evict-first: 428 us in all against 430 with ordinary ones, in place
+// 434 against 426.
 #include <math.h>
 
 #include <type_traits>
@@ -181,7 +182,10 @@ __global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constan
   const float f = factor_of(a, sum_of_parts(a, tmp), a.part0 == 0 && blockIdx.x == 0 && threadIdx.x == 0);
   const uint32_t chunks = a.first[a.n];
   for (uint32_t d = blockIdx.x; d < chunks; d += gridDim.x) {
-    const uint32_t c = chunks - 1 - d;  // the end first: what was read last may still be in the L2
+    // The end first: the SMs hold half of squares_kernel's CTAs at once, so the
+    // second half of the list was read last, and some of it is still in the L2
+    // (from the start 433 against 428 us; 26 M values 54 against 53).
+    const uint32_t c = chunks - 1 - d;
     const int t = tensor_of(a, c);
     const uint64_t e0 = (uint64_t)(c - a.first[t]) * kChunk;
     scale<kThreads, 8>((const T*)a.t[t].in, (T*)a.t[t].out, e0, min(a.t[t].n, e0 + kChunk), f);

@@ -54,8 +54,8 @@ inline purlin_status op_launch(void (*fn)(P...), uint64_t grid, int threads, siz
 }
 
 // Lets `fn` take `need` bytes of dynamic shared memory, where that and its (at
-// most 12 KiB) static memory are past the
-// 48 KiB that every kernel may take: the limit is raised to `most`, the same each time.
+// most 12 KiB) static memory are past the 48 KiB that every kernel may take: the
+// limit is raised to `most`, the same each time.
 inline purlin_status op_smem(const void* fn, size_t need, int most) {
   if (need <= 36 * 1024 || cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess)
     return PL_OK;

@@ -76,7 +76,8 @@ using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
 
 // More tokens than a cluster sorts: one digit of the sort in two launches (about
 // 9 us, most of it the launches and the wait of one for the other), of (key,
-// index) pairs, or the tokens themselves when in_key is null.  Keys are rows of the table; rows = outside, sorted last.
+// index) pairs, or the tokens themselves when in_key is null.  Keys are rows of
+// the table; rows = outside, sorted last.
 struct SortArgs {
   EmbedArgs e;
   const uint32_t *in_key, *in_idx;

@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_bulk_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const bool is = j0 + j < k && src[j0 + j];
-      // a dropped pick reads another's piece, and adds nothing of it
+      // a dropped pick has no piece and is skipped
       s[j] = is ? (const T*)(piece + (uint64_t)(j0 + j) * stride + ((uintptr_t)src[j0 + j] & 15u)) : nullptr;
       w[j] = is ? weight[j0 + j] : 0.f;
     }

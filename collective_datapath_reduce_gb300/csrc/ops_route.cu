@@ -126,7 +126,7 @@ __device__ __forceinline__ Two best_two(const float (&key)[VPT], int e0) {
 // maximum across the warp finds the best of the row.  A lane keeps its best
 // two keys ready and searches its registers again only after its second pick.
 //
-// Bound by the instructions of a row (about 900), not by its bytes (17 MB, 2.6
+// Bound by the instructions of a row (860), not by its bytes (17 MB, 2.6
 // us).  16384 tokens, 256 experts, 8 picks, sigmoid, bias, 4 of 8 groups by their
 // best two: 35 us with a search at every pick, 22 us with two keys ready, 19 us
 // with shifts for the divisions by a group's lanes and the pick passed through

@@ -5,10 +5,11 @@
 // A CTA takes a chunk of items; a warp takes a run of the chunk's items in
 // order, 32 at a time, so an item's place among its equals is: equals in earlier
 // chunks + in earlier warps + in earlier steps of its warp + in lower lanes.
-// (The kernel that counts lets the one that places start at once; that one does
-// what needs no counts and then waits for them.  What it reads before is older
-// than the counting kernel, which lets it start only after its own op_wait.)  Lanes with equal digits find each other with one match; only
-// the lowest of them touches the warp's counter, so no atomics order anything.
+// Lanes with equal digits find each other with one match; only the lowest of
+// them touches the warp's counter, so no atomics order anything.  (The kernel
+// that counts lets the one that places start at once; that one does what needs
+// no counts and then waits for them.  What it reads before is older than the
+// counting kernel, which lets it start only after its own op_wait.)
 #pragma once
 
 #include <cooperative_groups.h>

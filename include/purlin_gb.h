@@ -313,7 +313,9 @@ purlin_status purlin_atom_reduce(purlin_handle h, const void* const* src, int ns
  *   - Strides count elements from one row's start to the next's, and are at
  *     least the row's width.  Rows may have any width and any alignment to
  *     their element; 16-byte aligned rows are the fast path.
- *   - Written buffers must not overlap any other, except where said.
+ *   - Written buffers must not overlap any other, except where said, each
+ *     from its first row's start to its last row's end: columns of one matrix
+ *     as input and output are refused.
  *   - Workspaces are the caller's: at least as many bytes as the _bytes
  *     function of the same name gives, used until the call's work on the
  *     stream is done; too few return PL_ERR_WORKSPACE.  Nothing is kept in
