@@ -13,8 +13,9 @@
 
 namespace pl {
 
-// The start of every kernel here: the launch may begin while the previous
-// kernel of the stream drains; its writes are visible after this.
+// Every kernel here calls it before it writes, or reads what the stream's
+// previous kernel writes: the launch may begin while that one drains, and its
+// writes are visible after this.
 __device__ __forceinline__ void op_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the stream's next kernel start as soon as every CTA here has started;
