@@ -106,4 +106,79 @@ size_t clip_bytes();
 purlin_status launch_clip(const ClipTensor* t, size_t n, int dtype, float scale, float max_norm, bool write, float* norm,
                           double* partials, int sm_count, cudaStream_t s);
 
+struct NormArgs {
+  const void* x;       // the rows; gradient: the rows that were normalised
+  uint64_t ldx;
+  const void* residual;  // or nullptr
+  uint64_t ldr;
+  const void* weight;  // or nullptr
+  const void* bias;    // or nullptr
+  void* y;             // gradient: of x
+  uint64_t ldy;
+  void* total;         // or nullptr
+  uint64_t ldt;
+  float* stats;        // mean and 1 / deviation of each row; forward: or nullptr
+  uint64_t tokens, width;
+  float eps;
+  // gradient only
+  const void* grad_y;
+  uint64_t ldg;
+  const void* grad_total;  // or nullptr
+  uint64_t ldgt;
+  void* grad_weight;   // or nullptr
+  void* grad_bias;     // or nullptr
+  float* parts;        // workspace
+};
+size_t norm_grad_bytes(uint64_t tokens, uint64_t width);
+purlin_status launch_norm(const NormArgs& a, int dtype, int w_dtype, cudaStream_t s);
+purlin_status launch_norm_grad(const NormArgs& a, int dtype, int w_dtype, cudaStream_t s);
+
+struct BalanceArgs {
+  const void* logits;
+  uint64_t ld;
+  uint64_t tokens;
+  int experts, top_k, sigmoid;
+  float scale;
+  const int32_t* ids;
+  int32_t* counts;
+  float* sums;
+  float* loss;         // or nullptr
+  uint32_t* parts;     // workspace
+  // gradient only (sums are then read)
+  const float* grad_loss;  // or nullptr
+  const void* base;        // or nullptr
+  uint64_t ldb;
+  void* grad_logits;
+  uint64_t ldg;
+};
+size_t balance_bytes(uint64_t tokens, int experts);
+purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s);
+purlin_status launch_balance_join(const BalanceArgs& a, cudaStream_t s);
+purlin_status launch_balance_grad(const BalanceArgs& a, int dtype, cudaStream_t s);
+
+struct DistilArgs {
+  const void* logits;
+  uint64_t ld;
+  uint64_t tokens, width;
+  int64_t first, vocabulary;
+  const void* ids;
+  int wide_ids, picks;
+  const void* teacher;
+  int teacher_bf16;
+  float temperature, scale;
+  float log2e_per_temperature;
+  float* loss;         // with stats, or
+  float* stats;
+  float* parts;        // instead of them
+  // gradient only (stats are then read)
+  const float* grad_loss;
+  void* grad_logits;
+  uint64_t ldg;
+  // join only (parts are then read)
+  int ranks;
+};
+purlin_status launch_distil(const DistilArgs& a, int dtype, cudaStream_t s);
+purlin_status launch_distil_join(const DistilArgs& a, cudaStream_t s);
+purlin_status launch_distil_grad(const DistilArgs& a, int dtype, cudaStream_t s);
+
 }  // namespace pl

@@ -60,7 +60,7 @@ class Buffers {
   }
 
  private:
-  static constexpr int kMost = 8;
+  static constexpr int kMost = 12;
   const pl::OpHandle& h_;
   uintptr_t lo_[kMost], hi_[kMost];
   bool written_[kMost], host_ = false;
@@ -84,6 +84,39 @@ purlin_status check_routing(const purlin_routing* r) {
 purlin_status check_picks(size_t tokens, int top_k) {
   if (top_k < 1 || top_k > PURLIN_MAX_TOP_K) return PL_ERR_INVALID_ARG;
   return tokens > (size_t)0x7FFFFFFF / (size_t)top_k ? PL_ERR_UNSUPPORTED : PL_OK;
+}
+
+// `a` is `b` itself: read and written row by row in place.
+bool same(const void* a, size_t a_stride, const void* b, size_t b_stride) { return a && a == b && a_stride == b_stride; }
+
+purlin_status check_scores(int experts, int top_k, int scores, float scale) {
+  if (experts < 1 || experts > PURLIN_MAX_EXPERTS) return PL_ERR_INVALID_ARG;
+  if (top_k < 1 || top_k > PURLIN_MAX_TOP_K || top_k > experts) return PL_ERR_INVALID_ARG;
+  if (scores != PL_SCORES_SOFTMAX && scores != PL_SCORES_SIGMOID) return PL_ERR_UNSUPPORTED;
+  return std::isfinite(scale) ? PL_OK : PL_ERR_INVALID_ARG;
+}
+
+// The values that both directions of the distillation share.
+purlin_status distil_args(const purlin_distillation* d, size_t tokens, pl::DistilArgs* a) {
+  if (!d) return PL_ERR_INVALID_ARG;
+  if (d->picks < 1 || d->picks > PURLIN_MAX_PICKS) return PL_ERR_INVALID_ARG;
+  if (d->id_bytes != 4 && d->id_bytes != 8) return PL_ERR_UNSUPPORTED;
+  if (check_dtype(d->teacher_dtype)) return PL_ERR_UNSUPPORTED;
+  if (!(d->temperature >= 1e-30f && d->temperature <= 1e30f) || !std::isfinite(d->scale)) return PL_ERR_INVALID_ARG;
+  if (d->first < 0 || d->vocabulary < d->first || (uint64_t)(d->vocabulary - d->first) < d->width) return PL_ERR_INVALID_ARG;
+  if (tokens > SIZE_MAX / PURLIN_MAX_PICKS / 8) return PL_ERR_INVALID_ARG;
+  *a = {};
+  a->tokens = tokens;
+  a->width = d->width;
+  a->first = d->first;
+  a->vocabulary = d->vocabulary;
+  a->wide_ids = d->id_bytes == 8;
+  a->picks = d->picks;
+  a->teacher_bf16 = d->teacher_dtype == PL_BF16;
+  a->temperature = d->temperature;
+  a->scale = d->scale;
+  a->log2e_per_temperature = (float)(1.4426950408889634 / (double)d->temperature);
+  return PL_OK;
 }
 
 pl::RouteArgs route_args(const purlin_routing* r, size_t tokens) {
@@ -407,6 +440,286 @@ purlin_status purlin_clip_grad_norm(purlin_handle handle, const void* const* gra
   } catch (const std::exception&) {  // no memory for so many gradients
     return PL_ERR_INVALID_ARG;
   }
+}
+
+purlin_status purlin_layer_norm(purlin_handle handle, const void* x, size_t x_stride, const void* residual,
+                                size_t residual_stride, size_t tokens, size_t width, purlin_dtype dtype,
+                                const void* weight, const void* bias, purlin_dtype weight_dtype, float eps, void* y,
+                                size_t y_stride, void* total, size_t total_stride, float* stats,
+                                purlin_stream_t stream) {
+  pl::OpHandle h;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = check_dtype(weight_dtype))) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return PL_ERR_INVALID_ARG;
+  const uint64_t es = size_of(dtype), ws = size_of(weight_dtype);
+  // y and the total may lie on x or on the residual, one on each
+  const bool x_y = same(x, x_stride, y, y_stride), x_t = same(x, x_stride, total, total_stride);
+  const bool r_y = same(residual, residual_stride, y, y_stride), r_t = same(residual, residual_stride, total, total_stride);
+  Buffers b(h);
+  if ((!x_y && !x_t && (st = b.add(&x, false, tokens, width, x_stride, es))) ||
+      (residual && !r_y && !r_t && (st = b.add(&residual, false, tokens, width, residual_stride, es))) ||
+      (weight && (st = b.add(&weight, false, 1, width, width, ws))) ||
+      (bias && (st = b.add(&bias, false, 1, width, width, ws))) || (st = b.add(&y, true, tokens, width, y_stride, es)) ||
+      (total && (st = b.add(&total, true, tokens, width, total_stride, es))) ||
+      (stats && (st = b.add(&stats, true, tokens, 2, 2, 4))) || (st = b.apart()))
+    return st;
+  if (tokens == 0 || width == 0) return PL_OK;
+  pl::NormArgs a = {};
+  a.x = x_y ? y : x_t ? total : x;
+  a.ldx = x_stride;
+  a.residual = r_y ? y : r_t ? total : residual;
+  a.ldr = residual_stride;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.ldy = y_stride;
+  a.total = total;
+  a.ldt = total_stride;
+  a.stats = stats;
+  a.tokens = tokens;
+  a.width = width;
+  a.eps = eps;
+  return pl::launch_norm(a, dtype, weight_dtype, (cudaStream_t)stream);
+}
+
+size_t purlin_layer_norm_grad_bytes(size_t tokens, size_t width) {
+  return width > 0x7FFFFFFFu ? 0 : pl::norm_grad_bytes(tokens, width);
+}
+
+purlin_status purlin_layer_norm_grad(purlin_handle handle, const void* grad_y, size_t grad_y_stride, const void* x,
+                                     size_t x_stride, const float* stats, size_t tokens, size_t width,
+                                     purlin_dtype dtype, const void* weight, purlin_dtype weight_dtype,
+                                     const void* grad_total, size_t grad_total_stride, void* grad_x,
+                                     size_t grad_x_stride, void* grad_weight, void* grad_bias, void* workspace,
+                                     size_t workspace_bytes, purlin_stream_t stream) {
+  pl::OpHandle h;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = check_dtype(weight_dtype))) return st;
+  if (width > 0x7FFFFFFFu) return PL_ERR_UNSUPPORTED;
+  const uint64_t es = size_of(dtype), ws = size_of(weight_dtype);
+  const size_t need = grad_weight || grad_bias ? pl::norm_grad_bytes(tokens, width) : 0;
+  if (workspace_bytes < need) return PL_ERR_WORKSPACE;
+  // grad_x may lie on one of the three that have its rows
+  const bool on_x = same(x, x_stride, grad_x, grad_x_stride), on_g = same(grad_y, grad_y_stride, grad_x, grad_x_stride);
+  const bool on_t = same(grad_total, grad_total_stride, grad_x, grad_x_stride);
+  Buffers b(h);
+  if ((!on_g && (st = b.add(&grad_y, false, tokens, width, grad_y_stride, es))) ||
+      (!on_x && (st = b.add(&x, false, tokens, width, x_stride, es))) ||
+      (grad_total && !on_t && (st = b.add(&grad_total, false, tokens, width, grad_total_stride, es))) ||
+      (st = b.add(&stats, false, tokens, 2, 2, 4)) || (weight && (st = b.add(&weight, false, 1, width, width, ws))) ||
+      (st = b.add(&grad_x, true, tokens, width, grad_x_stride, es)) ||
+      (grad_weight && (st = b.add(&grad_weight, true, 1, width, width, ws))) ||
+      (grad_bias && (st = b.add(&grad_bias, true, 1, width, width, ws))) ||
+      (st = b.add(&workspace, true, 1, need / 4, need / 4, 4)) || (st = b.apart()))
+    return st;
+  if (width == 0) return PL_OK;
+  pl::NormArgs a = {};
+  a.x = on_x ? grad_x : x;
+  a.ldx = x_stride;
+  a.stats = const_cast<float*>(stats);
+  a.tokens = tokens;
+  a.width = width;
+  a.weight = weight;
+  a.grad_y = on_g ? grad_x : grad_y;
+  a.ldg = grad_y_stride;
+  a.grad_total = on_t ? grad_x : grad_total;
+  a.ldgt = grad_total_stride;
+  a.y = grad_x;
+  a.ldy = grad_x_stride;
+  a.grad_weight = grad_weight;
+  a.grad_bias = grad_bias;
+  a.parts = (float*)workspace;
+  return pl::launch_norm_grad(a, dtype, weight_dtype, (cudaStream_t)stream);
+}
+
+size_t purlin_balance_loss_bytes(size_t tokens, int experts) {
+  return experts < 1 || experts > PURLIN_MAX_EXPERTS ? 0 : pl::balance_bytes(tokens, experts);
+}
+
+purlin_status purlin_balance_loss(purlin_handle handle, const void* logits, size_t stride, purlin_dtype dtype,
+                                  const int32_t* ids, size_t tokens, int top_k, int experts, purlin_scores scores,
+                                  float scale, int32_t* counts, float* sums, float* loss, void* workspace,
+                                  size_t workspace_bytes, purlin_stream_t stream) {
+  pl::OpHandle h;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = check_scores(experts, top_k, scores, scale)) ||
+      (st = check_picks(tokens, top_k)))
+    return st;
+  const uint64_t E = (uint64_t)experts, k = (uint64_t)top_k;
+  const size_t need = pl::balance_bytes(tokens, experts);
+  if (workspace_bytes < need) return PL_ERR_WORKSPACE;
+  Buffers b(h);
+  if ((st = b.add(&logits, false, tokens, E, stride, size_of(dtype))) || (st = b.add(&ids, false, tokens, k, k, 4)) ||
+      (st = b.add(&counts, true, 1, E, E, 4)) || (st = b.add(&sums, true, 1, 2 * E + 1, 2 * E + 1, 4)) ||
+      (loss && (st = b.add(&loss, true, 1, 1, 1, 4))) || (st = b.add(&workspace, true, 1, need / 4, need / 4, 4)) ||
+      (st = b.apart()))
+    return st;
+  pl::BalanceArgs a = {};
+  a.logits = logits;
+  a.ld = stride;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.top_k = top_k;
+  a.sigmoid = scores == PL_SCORES_SIGMOID;
+  a.scale = scale;
+  a.ids = ids;
+  a.counts = counts;
+  a.sums = sums;
+  a.loss = loss;
+  a.parts = (uint32_t*)workspace;
+  return pl::launch_balance(a, dtype, (cudaStream_t)stream);
+}
+
+purlin_status purlin_balance_join(purlin_handle handle, const float* sums, int experts, float scale, float* loss,
+                                  purlin_stream_t stream) {
+  pl::OpHandle h;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_scores(experts, 1, PL_SCORES_SOFTMAX, scale))) return st;
+  const uint64_t n = 2 * (uint64_t)experts + 1;
+  Buffers b(h);
+  if ((st = b.add(&sums, false, 1, n, n, 4)) || (st = b.add(&loss, true, 1, 1, 1, 4)) || (st = b.apart())) return st;
+  pl::BalanceArgs a = {};
+  a.experts = experts;
+  a.scale = scale;
+  a.sums = const_cast<float*>(sums);
+  a.loss = loss;
+  return pl::launch_balance_join(a, (cudaStream_t)stream);
+}
+
+purlin_status purlin_balance_loss_grad(purlin_handle handle, const void* logits, size_t stride, purlin_dtype dtype,
+                                       const int32_t* ids, size_t tokens, int top_k, int experts, purlin_scores scores,
+                                       float scale, const float* sums, const float* grad_loss, const void* base,
+                                       size_t base_stride, void* grad_logits, size_t grad_stride,
+                                       purlin_stream_t stream) {
+  pl::OpHandle h;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = check_scores(experts, top_k, scores, scale)) ||
+      (st = check_picks(tokens, top_k)))
+    return st;
+  const uint64_t E = (uint64_t)experts, k = (uint64_t)top_k, es = size_of(dtype);
+  const bool in_place = same(base, base_stride, grad_logits, grad_stride);
+  Buffers b(h);
+  if ((st = b.add(&logits, false, tokens, E, stride, es)) || (st = b.add(&ids, false, tokens, k, k, 4)) ||
+      (st = b.add(&sums, false, 1, 2 * E + 1, 2 * E + 1, 4)) ||
+      (grad_loss && (st = b.add(&grad_loss, false, 1, 1, 1, 4))) ||
+      (base && !in_place && (st = b.add(&base, false, tokens, E, base_stride, es))) ||
+      (st = b.add(&grad_logits, true, tokens, E, grad_stride, es)) || (st = b.apart()))
+    return st;
+  if (tokens == 0) return PL_OK;
+  pl::BalanceArgs a = {};
+  a.logits = logits;
+  a.ld = stride;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.top_k = top_k;
+  a.sigmoid = scores == PL_SCORES_SIGMOID;
+  a.scale = scale;
+  a.ids = ids;
+  a.sums = const_cast<float*>(sums);
+  a.grad_loss = grad_loss;
+  a.base = in_place ? grad_logits : base;
+  a.ldb = base_stride;
+  a.grad_logits = grad_logits;
+  a.ldg = grad_stride;
+  return pl::launch_balance_grad(a, dtype, (cudaStream_t)stream);
+}
+
+purlin_status purlin_distil_loss(purlin_handle handle, const void* logits, size_t stride, purlin_dtype dtype,
+                                 size_t tokens, const purlin_distillation* d, const void* ids, const void* teacher,
+                                 float* loss, float* stats, purlin_stream_t stream) {
+  pl::OpHandle h;
+  pl::DistilArgs a;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = distil_args(d, tokens, &a))) return st;
+  if (d->first != 0 || (uint64_t)d->vocabulary != d->width) return PL_ERR_INVALID_ARG;  // purlin_distil_parts
+  const uint64_t k = (uint64_t)d->picks;
+  Buffers b(h);
+  if ((st = b.add(&logits, false, tokens, d->width, stride, size_of(dtype))) ||
+      (st = b.add(&ids, false, tokens, k, k, d->id_bytes)) ||
+      (st = b.add(&teacher, false, tokens, k, k, size_of(d->teacher_dtype))) ||
+      (st = b.add(&loss, true, 1, tokens, tokens, 4)) || (st = b.add(&stats, true, tokens, 2, 2, 4)) || (st = b.apart()))
+    return st;
+  if (tokens == 0) return PL_OK;
+  a.logits = logits;
+  a.ld = stride;
+  a.ids = ids;
+  a.teacher = teacher;
+  a.loss = loss;
+  a.stats = stats;
+  return pl::launch_distil(a, dtype, (cudaStream_t)stream);
+}
+
+purlin_status purlin_distil_parts(purlin_handle handle, const void* logits, size_t stride, purlin_dtype dtype,
+                                  size_t tokens, const purlin_distillation* d, const void* ids, const void* teacher,
+                                  float* parts, purlin_stream_t stream) {
+  pl::OpHandle h;
+  pl::DistilArgs a;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = distil_args(d, tokens, &a))) return st;
+  const uint64_t k = (uint64_t)d->picks;
+  Buffers b(h);
+  if ((st = b.add(&logits, false, tokens, d->width, stride, size_of(dtype))) ||
+      (st = b.add(&ids, false, tokens, k, k, d->id_bytes)) ||
+      (st = b.add(&teacher, false, tokens, k, k, size_of(d->teacher_dtype))) ||
+      (st = b.add(&parts, true, tokens, 4, 4, 4)) || (st = b.apart()))
+    return st;
+  if ((uintptr_t)parts & 7u) return PL_ERR_ALIGNMENT;
+  if (tokens == 0) return PL_OK;
+  a.logits = logits;
+  a.ld = stride;
+  a.ids = ids;
+  a.teacher = teacher;
+  a.parts = parts;
+  return pl::launch_distil(a, dtype, (cudaStream_t)stream);
+}
+
+purlin_status purlin_distil_join(purlin_handle handle, const float* parts, int ranges, size_t tokens, float temperature,
+                                 float scale, float* loss, float* stats, purlin_stream_t stream) {
+  pl::OpHandle h;
+  pl::DistilArgs a;
+  purlin_status st;
+  const purlin_distillation d = {0, 0, 0, 1, 8, PL_F32, temperature, scale};
+  if ((st = pl::op_begin(handle, &h)) || (st = distil_args(&d, tokens, &a))) return st;
+  if (ranges < 1 || (uint64_t)ranges > UINT64_MAX / 16 / std::max<uint64_t>(1, tokens)) return PL_ERR_INVALID_ARG;
+  Buffers b(h);
+  if ((st = b.add(&parts, false, (uint64_t)ranges * tokens, 4, 4, 4)) || (st = b.add(&loss, true, 1, tokens, tokens, 4)) ||
+      (st = b.add(&stats, true, tokens, 2, 2, 4)) || (st = b.apart()))
+    return st;
+  if (tokens == 0) return PL_OK;
+  a.parts = const_cast<float*>(parts);
+  a.ranks = ranges;
+  a.loss = loss;
+  a.stats = stats;
+  return pl::launch_distil_join(a, (cudaStream_t)stream);
+}
+
+purlin_status purlin_distil_loss_grad(purlin_handle handle, const void* logits, size_t stride, purlin_dtype dtype,
+                                      size_t tokens, const purlin_distillation* d, const void* ids, const void* teacher,
+                                      const float* stats, const float* grad_loss, void* grad_logits, size_t grad_stride,
+                                      purlin_stream_t stream) {
+  pl::OpHandle h;
+  pl::DistilArgs a;
+  purlin_status st;
+  if ((st = pl::op_begin(handle, &h)) || (st = check_dtype(dtype)) || (st = distil_args(d, tokens, &a))) return st;
+  const uint64_t k = (uint64_t)d->picks, es = size_of(dtype);
+  const bool in_place = same(logits, stride, grad_logits, grad_stride);
+  Buffers b(h);
+  if ((!in_place && (st = b.add(&logits, false, tokens, d->width, stride, es))) ||
+      (st = b.add(&ids, false, tokens, k, k, d->id_bytes)) ||
+      (st = b.add(&teacher, false, tokens, k, k, size_of(d->teacher_dtype))) ||
+      (st = b.add(&stats, false, tokens, 2, 2, 4)) || (st = b.add(&grad_loss, false, 1, tokens, tokens, 4)) ||
+      (st = b.add(&grad_logits, true, tokens, d->width, grad_stride, es)) || (st = b.apart()))
+    return st;
+  if (tokens == 0 || d->width == 0) return PL_OK;
+  a.logits = in_place ? grad_logits : logits;
+  a.ld = stride;
+  a.ids = ids;
+  a.teacher = teacher;
+  a.stats = const_cast<float*>(stats);
+  a.grad_loss = grad_loss;
+  a.grad_logits = grad_logits;
+  a.ldg = grad_stride;
+  return pl::launch_distil_grad(a, dtype, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,372 @@
+// The balance of the experts' load: how often each was picked and what share of
+// the tokens' scores it has, the loss that couples the two, and its gradient.
+#include <math.h>
+
+#include <type_traits>
+
+#include "ops_common.cuh"
+
+namespace pl {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kWarps = 8;            // of a CTA, a token each at a time
+constexpr int kThreads = kWarps * 32;
+constexpr int kCluster = 8;          // CTAs whose sums are added through shared memory
+constexpr int kMostClusters = 38;    // two CTAs on each of 152 SMs
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+  return x;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// A word of the shared memory of the cluster's CTA `rank`, where p is in this one's.
+__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// N neighbouring values in each lane; those past `width` read `none`.
+template <typename T, int N>
+__device__ __forceinline__ void ld_lane(const T* p, int width, bool vec, float none, float (&x)[N]) {
+  const int e0 = (threadIdx.x & 31) * N;
+  constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
+  if (vec) {
+    if (e0 < width) {
+#pragma unroll
+      for (int q = 0; q < N; q += M) {
+        const Pack<T, M> r = *reinterpret_cast<const Pack<T, M>*>(p + e0 + q);
+#pragma unroll
+        for (int i = 0; i < M; ++i) x[q + i] = to_f32(r.v[i]);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = none;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e0 + i < width ? to_f32(p[e0 + i]) : none;
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void st_lane(T* p, int width, bool vec, const float (&x)[N]) {
+  const int e0 = (threadIdx.x & 31) * N;
+  constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
+  if (vec) {
+    if (e0 >= width) return;
+#pragma unroll
+    for (int q = 0; q < N; q += M) {
+      Pack<T, M> r;
+#pragma unroll
+      for (int i = 0; i < M; ++i) r.v[i] = from_f32<T>(x[q + i]);
+      st_pack(p + e0 + q, r);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (e0 + i < width) p[e0 + i] = from_f32<T>(x[i]);
+  }
+}
+
+// A token's logits become its scores as shares of one; `slope` is what a
+// score's derivative has beside them, 1 - sigmoid.  A row of nothing but -inf
+// has shares of 0.
+template <int N>
+__device__ __forceinline__ void shares(float (&x)[N], int sigmoid, float (&slope)[N]) {
+  float s = 0.f;
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = expf(-x[i]);
+      x[i] = __frcp_rn(1.f + e);
+      slope[i] = e < 1.f ? e * x[i] : 1.f - x[i];  // where s is near 1, the difference would be rounding
+      s += x[i];
+    }
+    s = warp_sum(s) + 1e-20f;
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = expf(x[i] - m);
+      slope[i] = 1.f;
+      s += x[i];
+    }
+    s = warp_sum(s);
+    if (s == 0.f) s = 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __fdiv_rn(x[i], s);
+}
+
+// The loss of picks C, shares P and N tokens: scale x E x sum C P / (sum C x N).
+__device__ __forceinline__ float loss_of(const BalanceArgs& a, float picks, float dot, float tokens) {
+  const float all = picks * tokens;
+  return all > 0.f ? a.scale * (float)a.experts * __fdiv_rn(dot, all) : 0.f;
+}
+
+// A cluster's CTAs take the experts in turn, `at(e, which)` being an expert's picks (0) or
+// shares (1), and `tokens` the tokens: they write the outputs.  tmp: 2 x 8 words.
+template <typename A>
+__device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float* tmp, A at) {
+  const uint32_t rank = cluster_rank();
+  float picks = 0.f, dot = 0.f;
+  for (int e = (int)rank * kThreads + threadIdx.x; e < a.experts; e += kCluster * kThreads) {
+    const uint32_t c = __float_as_uint(at(e, 0));
+    const float p = at(e, 1);
+    a.counts[e] = (int32_t)c;
+    a.sums[e] = (float)c;
+    a.sums[a.experts + e] = p;
+    picks += (float)c;
+    dot = __fmaf_rn((float)c, p, dot);
+  }
+  if (rank == 0 && threadIdx.x == 0) a.sums[2 * a.experts] = tokens;
+  if (!a.loss) return;
+  picks = warp_sum(picks);
+  dot = warp_sum(dot);
+  if ((threadIdx.x & 31) == 0) {
+    tmp[threadIdx.x >> 5] = picks;
+    tmp[kWarps + (threadIdx.x >> 5)] = dot;
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x < 32) {
+    picks = dot = 0.f;
+    for (int i = threadIdx.x; i < kCluster * kWarps; i += 32) {
+      picks += __uint_as_float(ld_cluster(tmp + i % kWarps, i / kWarps));
+      dot += __uint_as_float(ld_cluster(tmp + kWarps + i % kWarps, i / kWarps));
+    }
+    picks = warp_sum(picks);
+    dot = warp_sum(dot);
+    if (threadIdx.x == 0) *a.loss = loss_of(a, picks, dot, tokens);
+  }
+  cluster_sync();  // before a CTA ends whose memory is read
+}
+
+// A warp holds a token, N neighbouring experts in each lane, and adds its
+// shares to the lane's sums; picks are counted in shared memory.  The warps'
+// sums are added in order, then the cluster's CTAs'.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int clusters) {
+  op_wait();
+  extern __shared__ float dyn[];   // [kWarps][experts] shares, whose first row the CTA's become; [experts] picks
+  __shared__ uint32_t tokens_of[kWarps];
+  __shared__ float tmp[2 * kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  uint32_t* picks = (uint32_t*)(dyn + kWarps * E);
+  for (int e = threadIdx.x; e < E; e += kThreads) picks[e] = 0;
+  __syncthreads();
+  float sum[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = 0.f;
+  uint32_t counted = 0;
+  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (uint64_t)gridDim.x * kWarps) {
+    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+    const bool on = id >= 0 && id < E;
+    if (!__any_sync(kAll, on)) continue;  // padding: its logits may be anything
+    if (on) atomicAdd(picks + id, 1u);
+    float x[N], slope[N];
+    ld_lane<T, N>((const T*)a.logits + t * a.ld, E, vec, -INFINITY, x);
+    shares<N>(x, a.sigmoid, slope);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] += x[i];
+    ++counted;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane * N + i < E) dyn[warp * E + lane * N + i] = sum[i];
+  if (lane == 0) tokens_of[warp] = counted;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    float s = dyn[e];
+    for (int w = 1; w < kWarps; ++w) s += dyn[w * E + e];
+    dyn[e] = s;
+  }
+  cluster_sync();
+  uint32_t tokens = 0;
+  for (int i = 0; i < kCluster * kWarps; ++i) tokens += ld_cluster(tokens_of + i % kWarps, i / kWarps);
+  auto at = [&](int e, int which) {
+    if (which == 0) {
+      uint32_t c = 0;
+      for (int r = 0; r < kCluster; ++r) c += ld_cluster(picks + e, r);
+      return __uint_as_float(c);
+    }
+    float s = 0.f;
+    for (int r = 0; r < kCluster; ++r) s += __uint_as_float(ld_cluster(dyn + e, r));
+    return s;
+  };
+  if (clusters == 1) {
+    finish(a, (float)tokens, tmp, at);
+  } else {
+    uint32_t* out = a.parts + (uint64_t)(blockIdx.x / kCluster) * (2 * E + 1);
+    for (int e = (int)cluster_rank() * kThreads + threadIdx.x; e < E; e += kCluster * kThreads) {
+      out[e] = __float_as_uint(at(e, 0));
+      out[E + e] = __float_as_uint(at(e, 1));
+    }
+    if (cluster_rank() == 0 && threadIdx.x == 0) out[2 * E] = tokens;
+  }
+  cluster_sync();
+}
+
+// The clusters' sums, added in order.
+__global__ void __launch_bounds__(kThreads) balance_parts_kernel(const __grid_constant__ BalanceArgs a, int clusters) {
+  op_wait();
+  __shared__ float tmp[2 * kWarps];
+  const int E = a.experts, row = 2 * E + 1;
+  uint32_t tokens = 0;
+  for (int p = 0; p < clusters; ++p) tokens += a.parts[(uint64_t)p * row + 2 * E];
+  finish(a, (float)tokens, tmp, [&](int e, int which) {
+    if (which == 0) {
+      uint32_t c = 0;
+      for (int p = 0; p < clusters; ++p) c += a.parts[(uint64_t)p * row + e];
+      return __uint_as_float(c);
+    }
+    float s = 0.f;
+    for (int p = 0; p < clusters; ++p) s += __uint_as_float(a.parts[(uint64_t)p * row + E + e]);
+    return s;
+  });
+  cluster_sync();
+}
+
+// The sum of the picks that `sums` hold, in every thread of the CTA.
+__device__ __forceinline__ float all_picks(const float* sums, int experts, float* tmp) {
+  float s = 0.f;
+  for (int e = threadIdx.x; e < experts; e += kThreads) s += sums[e];
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = tmp[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) s += tmp[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) balance_join_kernel(const __grid_constant__ BalanceArgs a) {
+  op_wait();
+  __shared__ float tmp[2][kWarps];
+  const float picks = all_picks(a.sums, a.experts, tmp[0]);
+  float dot = 0.f;
+  for (int e = threadIdx.x; e < a.experts; e += kThreads) dot = __fmaf_rn(a.sums[e], a.sums[a.experts + e], dot);
+  dot = warp_sum(dot);
+  if ((threadIdx.x & 31) == 0) tmp[1][threadIdx.x >> 5] = dot;
+  __syncthreads();
+  dot = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) dot += tmp[1][w];
+  if (threadIdx.x == 0) *a.loss = loss_of(a, picks, dot, a.sums[2 * a.experts]);
+}
+
+// With p the shares and c_e = dL x scale x E x C_e / (sum C x N):  dx_j = p_j (c_j -
+// sum p c), for sigmoids times 1 - s_j.  A token without picks has none.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_constant__ BalanceArgs a, int vec) {
+  op_wait();
+  __shared__ float tmp[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  const float all = all_picks(a.sums, E, tmp) * a.sums[2 * E];
+  const float f = all > 0.f ? __fdiv_rn((a.grad_loss ? *a.grad_loss : 1.f) * a.scale * (float)E, all) : 0.f;
+  float c[N];
+  ld_lane<float, N>(a.sums, E, false, 0.f, c);
+#pragma unroll
+  for (int i = 0; i < N; ++i) c[i] *= f;
+  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (uint64_t)gridDim.x * kWarps) {
+    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+    float x[N], slope[N];
+    if (__any_sync(kAll, id >= 0 && id < E)) {
+      ld_lane<T, N>((const T*)a.logits + t * a.ld, E, vec, -INFINITY, x);
+      shares<N>(x, a.sigmoid, slope);
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) dot = __fmaf_rn(x[i], c[i], dot);
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = x[i] * (c[i] - dot) * slope[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = 0.f;
+    }
+    if (a.base) {
+      ld_lane<T, N>((const T*)a.base + t * a.ldb, E, vec, 0.f, slope);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += slope[i];
+    }
+    st_lane<T, N>((T*)a.grad_logits + t * a.ldg, E, vec, x);
+  }
+}
+
+// Experts of a lane: the smallest power of two that covers them with 32 lanes.
+template <typename F>
+purlin_status with_lanes(int experts, F f) {
+  if (experts <= 32) return f(std::integral_constant<int, 1>());
+  if (experts <= 64) return f(std::integral_constant<int, 2>());
+  if (experts <= 128) return f(std::integral_constant<int, 4>());
+  if (experts <= 256) return f(std::integral_constant<int, 8>());
+  if (experts <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+template <typename T, int N>
+bool even(const BalanceArgs& a) {
+  const uint64_t need = std::min<uint64_t>(16, N * sizeof(T));
+  uint64_t bits = (uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T);
+  if (a.grad_logits) bits |= (uint64_t)(uintptr_t)a.grad_logits | a.ldg * sizeof(T);
+  if (a.base) bits |= (uint64_t)(uintptr_t)a.base | a.ldb * sizeof(T);
+  return a.experts % N == 0 && bits % need == 0;  // every lane's experts exist or none
+}
+
+int clusters_of(uint64_t tokens) {
+  const uint64_t per = kCluster * kWarps;
+  return (int)std::max<uint64_t>(1, std::min<uint64_t>(kMostClusters, (tokens + per - 1) / per));
+}
+
+}  // namespace
+
+size_t balance_bytes(uint64_t tokens, int experts) {
+  const int clusters = clusters_of(tokens);
+  return clusters == 1 ? 0 : (size_t)clusters * (2 * (size_t)experts + 1) * sizeof(uint32_t);
+}
+
+purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
+  const int clusters = clusters_of(a.tokens);
+  const size_t smem = (size_t)(kWarps + 1) * a.experts * sizeof(float);
+  const purlin_status st = with_lanes(a.experts, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (dtype == PL_F32) return op_launch_cluster(kCluster, balance_kernel<float, N>, clusters * kCluster, kThreads, smem, s, a, (int)even<float, N>(a), clusters);
+    return op_launch_cluster(kCluster, balance_kernel<bf16, N>, clusters * kCluster, kThreads, smem, s, a, (int)even<bf16, N>(a), clusters);
+  });
+  if (st || clusters == 1) return st;
+  return op_launch_cluster(kCluster, balance_parts_kernel, kCluster, kThreads, 0, s, a, clusters);
+}
+
+purlin_status launch_balance_join(const BalanceArgs& a, cudaStream_t s) {
+  return op_launch(balance_join_kernel, 1, kThreads, 0, s, a);
+}
+
+purlin_status launch_balance_grad(const BalanceArgs& a, int dtype, cudaStream_t s) {
+  const uint64_t grid = std::min<uint64_t>((a.tokens + kWarps - 1) / kWarps, 152 * 8);
+  return with_lanes(a.experts, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (dtype == PL_F32) return op_launch(balance_grad_kernel<float, N>, grid, kThreads, 0, s, a, (int)even<float, N>(a));
+    return op_launch(balance_grad_kernel<bf16, N>, grid, kThreads, 0, s, a, (int)even<bf16, N>(a));
+  });
+}
+
+}  // namespace pl

@@ -1,0 +1,361 @@
+// Distillation from a teacher's top logits: the Kullback-Leibler divergence of a
+// token's distribution over the vocabulary from the teacher's over its picks,
+// and its gradient, over the whole vocabulary or a rank's range of it.
+//
+// With z the logits, t the teacher's, both over the temperature, q = softmax(t)
+// over the picks and p = softmax(z) over the vocabulary, the loss is sum q_k (log q_k
+// - log p_k).  A range gives m = max z, s = sum exp(z - m), c = the sum over its
+// picks of q_k (log q_k - (z_k - m)), and Q, the sum of their q_k; then, with M
+// and S those of all ranges, the loss is the sum of c_r - Q_r (m_r - M) + Q_r log S.
+// Differences from the maximum are taken before anything is scaled, so that rows
+// of the lowest value are rows like others.
+#include <math.h>
+
+#include "ops_common.cuh"
+
+namespace pl {
+namespace {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMostCluster = 8;    // CTAs of a token
+constexpr int kHeld = PURLIN_MAX_PICKS / kThreads;  // picks of a thread
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(const void* p, uint32_t rank, float2 v) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// 2^x; results below the smallest normal number are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A maximum and the sum of 2^(scale (x - maximum)) of the values behind it; a
+// maximum of -inf is that of no values, or of nothing but -inf.
+__device__ __forceinline__ float at_least(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float2 joined(float2 a, float2 b, float c) {
+  const float m = fmaxf(a.x, b.x), n = at_least(m);
+  return make_float2(m, __fmaf_rn(a.y, ex2((a.x - n) * c), b.y * ex2((b.x - n) * c)));
+}
+
+template <typename F>
+__device__ __forceinline__ float2 warp_all(float2 v, F f) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = f(v, make_float2(__shfl_xor_sync(kAll, v.x, d), __shfl_xor_sync(kAll, v.y, d)));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+  return x;
+}
+
+// A thread's picks of a token: where each stands in the range (-1: elsewhere, -2: no
+// pick), the teacher's logit and the student's.
+template <typename T>
+struct Picks {
+  int64_t at[kHeld];
+  float t[kHeld], z[kHeld];
+
+  __device__ __forceinline__ void load(const DistilArgs& a, uint64_t token, const T* row) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int k = threadIdx.x + j * kThreads;
+      at[j] = -2;
+      t[j] = -INFINITY;
+      z[j] = 0.f;
+      if (k >= a.picks) continue;
+      const uint64_t i = token * a.picks + k;
+      const int64_t id = a.wide_ids ? ((const int64_t*)a.ids)[i] : ((const int32_t*)a.ids)[i];
+      if (id < 0 || id >= a.vocabulary) continue;
+      t[j] = a.teacher_bf16 ? to_f32(((const bf16*)a.teacher)[i]) : ((const float*)a.teacher)[i];
+      at[j] = id >= a.first && (uint64_t)(id - a.first) < a.width ? id - a.first : -1;
+      if (at[j] >= 0) z[j] = to_f32(row[at[j]]);
+    }
+  }
+  __device__ __forceinline__ float best() const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) m = fmaxf(m, t[j]);
+    return m;
+  }
+  // exp of the teacher's logit against the best one, over the temperature
+  __device__ __forceinline__ float weight(int j, float best, float tau) const {
+    return at[j] == -2 ? 0.f : expf(__fdiv_rn(t[j] - at_least(best), tau));
+  }
+};
+
+// The elements of a row [0, width) that a CTA of `split` takes: whole 16-byte
+// vectors behind the `cut.head` elements before the first, split in equal parts;
+// the elements beside the vectors are the first CTA's.
+__device__ __forceinline__ uint64_t share(uint64_t nv, uint32_t rank, uint32_t split) { return nv * rank / split; }
+
+// One token, by a cluster of CTAs that share its row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant__ DistilArgs a, int split) {
+  op_wait();
+  constexpr int V = V16<T>, F = 4;
+  __shared__ float2 of_warp[kWarps], of_cta[kMostCluster];
+  __shared__ float best_of[kWarps];
+  __shared__ float sum_of[3][kWarps];
+  const uint64_t token = blockIdx.x / split;
+  const uint32_t rank = blockIdx.x % split, tid = threadIdx.x;
+  if (split > 1) cluster_arrive();  // that this CTA runs: others may write to its memory
+  const T* row = (const T*)a.logits + token * a.ld;
+  const float c = a.log2e_per_temperature;
+  const Cut cut = cut_of<T, true>(row, a.width);
+  const uint64_t v0 = share(cut.nv, rank, split), v1 = share(cut.nv, rank + 1, split);
+  const T* body = row + cut.head;
+
+  Picks<T> picks;
+  if (rank == 0) picks.load(a, token, row);
+  float m = -INFINITY, s = 0.f;
+  for (uint64_t v = v0 + tid; v < v1; v += F * kThreads) {
+    Pack<T, V> x[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u) x[u] = ld_pack_if<T, V>(body + (v + u * kThreads) * V, v + u * kThreads < v1);
+#pragma unroll
+    for (int u = 0; u < F; ++u) pin(x[u]);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < F; ++u)
+      if (v + u * kThreads < v1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, to_f32(x[u].v[i]));
+    const float n = at_least(top);
+    s *= ex2((m - n) * c);
+    m = top;
+#pragma unroll
+    for (int u = 0; u < F; ++u)
+      if (v + u * kThreads < v1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += ex2((to_f32(x[u].v[i]) - n) * c);
+  }
+  if (rank == 0 && tid < cut.beside) {
+    const float x = to_f32(row[cut.at<V>(tid)]);
+    s = __fmaf_rn(s, ex2((m - at_least(fmaxf(m, x))) * c), ex2((x - at_least(fmaxf(m, x))) * c));
+    m = fmaxf(m, x);
+  }
+  float2 ms = warp_all(make_float2(m, s), [c](float2 p, float2 q) { return joined(p, q, c); });
+  float best = rank == 0 ? warp_max(picks.best()) : 0.f;
+  if ((tid & 31) == 0) {
+    of_warp[tid >> 5] = ms;
+    best_of[tid >> 5] = best;
+  }
+  __syncthreads();
+  ms = of_warp[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) ms = joined(ms, of_warp[w], c);
+  if (split > 1) {
+    cluster_wait();
+    if (tid == 0) st_cluster(of_cta + rank, 0, ms);
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (rank) return;
+  if (split > 1) {
+    ms = of_cta[0];
+    for (int r = 1; r < split; ++r) ms = joined(ms, of_cta[r], c);
+  }
+  best = best_of[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) best = fmaxf(best, best_of[w]);
+
+  // the sums over the picks: e, and of those in the range e (log-ratio) and e
+  float all = 0.f, term = 0.f, mass = 0.f;
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const float e = picks.weight(j, best, a.temperature);
+    all += e;
+    if (picks.at[j] < 0 || e == 0.f) continue;
+    const float of_t = __fdiv_rn(picks.t[j] - at_least(best), a.temperature);
+    const float of_z = __fdiv_rn(picks.z[j] - at_least(ms.x), a.temperature);
+    term = __fmaf_rn(e, of_t - of_z, term);
+    mass += e;
+  }
+  all = warp_sum(all);
+  term = warp_sum(term);
+  mass = warp_sum(mass);
+  if ((tid & 31) == 0) {
+    sum_of[0][tid >> 5] = all;
+    sum_of[1][tid >> 5] = term;
+    sum_of[2][tid >> 5] = mass;
+  }
+  __syncthreads();
+  if (tid) return;
+  all = term = mass = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    all += sum_of[0][w];
+    term += sum_of[1][w];
+    mass += sum_of[2][w];
+  }
+  if (mass != 0.f) {  // NaN too
+    term = __fdiv_rn(__fmaf_rn(-mass, logf(all), term), all);
+    mass = __fdiv_rn(mass, all);
+  }
+  if (a.parts) {
+    reinterpret_cast<Pack<float, 2>*>(a.parts)[2 * token] = {ms.x, ms.y};
+    reinterpret_cast<Pack<float, 2>*>(a.parts)[2 * token + 1] = {term, mass};
+  } else {
+    a.loss[token] = mass == 0.f || ms.y == 0.f ? 0.f : a.scale * __fmaf_rn(mass, logf(ms.y), term);
+    a.stats[2 * token] = ms.x;
+    a.stats[2 * token + 1] = ms.y;
+  }
+}
+
+// The parts of all ranges of a token, one thread for a token.
+__global__ void __launch_bounds__(kThreads) distil_join_kernel(const __grid_constant__ DistilArgs a) {
+  op_wait();
+  const uint64_t token = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (token >= a.tokens) return;
+  const float c = a.log2e_per_temperature;
+  float2 ms = make_float2(-INFINITY, 0.f);
+  for (int r = 0; r < a.ranks; ++r) {
+    const float* p = a.parts + (r * a.tokens + token) * 4;
+    ms = joined(ms, make_float2(p[0], p[1]), c);
+  }
+  float loss = 0.f, mass = 0.f;
+  for (int r = 0; r < a.ranks; ++r) {
+    const float* p = a.parts + (r * a.tokens + token) * 4;
+    if (p[3] == 0.f) continue;
+    mass += p[3];
+    loss += __fmaf_rn(-p[3], __fdiv_rn(at_least(p[0]) - at_least(ms.x), a.temperature), p[2]);
+  }
+  a.loss[token] = mass == 0.f || ms.y == 0.f ? 0.f : a.scale * __fmaf_rn(mass, logf(ms.y), loss);
+  a.stats[2 * token] = ms.x;
+  a.stats[2 * token + 1] = ms.y;
+}
+
+// dz_j = G (Q p_j - the sum of q_k over the picks k of j), G = dL scale / temperature.
+// The row is written without the picks first, then the picks' places again, by
+// the CTA that wrote them, each by the first pick of its word.
+template <typename T, bool SHIFT>
+__global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_constant__ DistilArgs a, int split) {
+  op_wait();
+  constexpr int V = V16<T>, F = 4;
+  __shared__ float best_of[kWarps], sum_of[kWarps];
+  __shared__ int64_t id_of[PURLIN_MAX_PICKS];
+  __shared__ float q_of[PURLIN_MAX_PICKS];
+  const uint64_t token = blockIdx.x / split;
+  const uint32_t rank = blockIdx.x % split, tid = threadIdx.x;
+  const T* row = (const T*)a.logits + token * a.ld;
+  T* out = (T*)a.grad_logits + token * a.ldg;
+  const float c = a.log2e_per_temperature;
+  const Cut cut = cut_of<T, true>(out, a.width);
+  const uint64_t v0 = share(cut.nv, rank, split), v1 = share(cut.nv, rank + 1, split);
+
+  Picks<T> picks;
+  picks.load(a, token, row);
+  float best = warp_max(picks.best());
+  if ((tid & 31) == 0) best_of[tid >> 5] = best;
+  __syncthreads();
+  best = best_of[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) best = fmaxf(best, best_of[w]);
+  float e[kHeld], all = 0.f;
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    all += e[j] = picks.weight(j, best, a.temperature);
+    if (tid + j * kThreads < a.picks) {
+      id_of[tid + j * kThreads] = picks.at[j];
+      q_of[tid + j * kThreads] = e[j];
+    }
+  }
+  all = warp_sum(all);
+  if ((tid & 31) == 0) sum_of[tid >> 5] = all;
+  __syncthreads();  // the picks' logits are read before any gradient is written in their place
+  all = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += sum_of[w];
+  const float m = at_least(a.stats[2 * token]), total = a.stats[2 * token + 1];
+  const bool none = all == 0.f || total == 0.f;  // no picks, or nothing to take them from
+  const float G = none ? 0.f : __fdiv_rn(a.grad_loss[token] * a.scale, a.temperature);
+  const float f = none ? 0.f : __fdiv_rn(G, total) * __fdiv_rn(all, all);  // Q is 1, or NaN
+  auto grad = [&](float z) { return none ? 0.f : f * ex2((z - m) * c); };
+
+  const T* from = row + cut.head;
+  T* to = out + cut.head;
+  for (uint64_t v = v0 + tid; v < v1; v += F * kThreads) {
+    Pack<T, V> x[F];
+#pragma unroll
+    for (int u = 0; u < F; ++u) {
+      const bool on = v + u * kThreads < v1;
+      const T* p = from + (v + u * kThreads) * V;
+      if constexpr (SHIFT) x[u] = ld_row_if<T, true>(p, on);
+      else x[u] = ld_pack_if<T, V, Ld::kWritten>(p, on);
+    }
+#pragma unroll
+    for (int u = 0; u < F; ++u) pin(x[u]);
+#pragma unroll
+    for (int u = 0; u < F; ++u) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[u].v[i] = from_f32<T>(grad(to_f32(x[u].v[i])));
+      if (v + u * kThreads < v1) st_pack(to + (v + u * kThreads) * V, x[u]);
+    }
+  }
+  if (rank == 0 && tid < cut.beside) {
+    const uint64_t i = cut.at<V>(tid);
+    out[i] = from_f32<T>(grad(to_f32(row[i])));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int k = tid + j * kThreads;
+    if (k >= a.picks || picks.at[j] < 0 || none) continue;
+    const uint64_t i = (uint64_t)picks.at[j];
+    const bool beside = i < cut.head || i >= cut.head + cut.nv * V;
+    const uint64_t v = (i - cut.head) / V;
+    if (beside ? rank != 0 : v < v0 || v >= v1) continue;
+    float q = e[j];
+    bool first = true;
+    for (int o = 0; o < a.picks; ++o)
+      if (id_of[o] == picks.at[j] && o != k) {
+        first = first && o > k;
+        q += q_of[o];
+      }
+    if (first) out[i] = from_f32<T>(__fmaf_rn(-G, __fdiv_rn(q, all), grad(picks.z[j])));
+  }
+}
+
+// CTAs of a token: as many as bring the launch to `want`, in powers of two.
+int split_of(uint64_t tokens, uint64_t width, uint64_t want) {
+  int n = 1;
+  while (n < kMostCluster && tokens * n * 2 <= want && width / (n * 2) >= 1024) n *= 2;
+  return n;
+}
+
+}  // namespace
+
+purlin_status launch_distil(const DistilArgs& a, int dtype, cudaStream_t s) {
+  const int split = split_of(a.tokens, a.width, 4 * 152);
+  if (dtype == PL_F32) return op_launch_cluster(split, distil_kernel<float>, a.tokens * split, kThreads, 0, s, a, split);
+  return op_launch_cluster(split, distil_kernel<bf16>, a.tokens * split, kThreads, 0, s, a, split);
+}
+
+purlin_status launch_distil_join(const DistilArgs& a, cudaStream_t s) {
+  return op_launch(distil_join_kernel, (a.tokens + kThreads - 1) / kThreads, kThreads, 0, s, a);
+}
+
+purlin_status launch_distil_grad(const DistilArgs& a, int dtype, cudaStream_t s) {
+  const int split = split_of(a.tokens, a.width, 4 * 152);
+  const uint64_t es = dtype == PL_F32 ? 4 : 2;
+  // rows of both matrices at the same distance from a 16-byte boundary, all of them
+  const bool even = (((uintptr_t)a.logits ^ (uintptr_t)a.grad_logits) & 15) == 0 && ((a.ld - a.ldg) * es & 15) == 0;
+  auto go = [&](auto fn) { return op_launch(fn, a.tokens * split, kThreads, 0, s, a, split); };
+  if (dtype == PL_F32) return even ? go(distil_grad_kernel<float, false>) : go(distil_grad_kernel<float, true>);
+  return even ? go(distil_grad_kernel<bf16, false>) : go(distil_grad_kernel<bf16, true>);
+}
+
+}  // namespace pl

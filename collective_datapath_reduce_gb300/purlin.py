@@ -48,7 +48,7 @@ PATH_REGISTER, PATH_BULK = 1, 2
 PL_SCHED_ITEM, PL_SCHED_STREAM, PL_SCHED_QUEUE, PL_SCHED_QUEUE_GUIDED = 1, 2, 3, 4
 
 MAX_WORLD = 16
-MAX_EXPERTS, MAX_TOP_K, MAX_GROUPS = 1024, 32, 32
+MAX_EXPERTS, MAX_TOP_K, MAX_GROUPS, MAX_PICKS = 1024, 32, 32, 1024
 PL_SCORES_SOFTMAX, PL_SCORES_SIGMOID = 0, 1
 
 
@@ -76,11 +76,18 @@ class purlin_routing(ctypes.Structure):
                                             "renormalise")] + [("scale", ctypes.c_float)]
 
 
+class purlin_distillation(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_size_t), ("first", ctypes.c_int64), ("vocabulary", ctypes.c_int64),
+                ("picks", ctypes.c_int), ("id_bytes", ctypes.c_int), ("teacher_dtype", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _i = ctypes.c_int
+_f = ctypes.c_float
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _SZP = ctypes.POINTER(ctypes.c_size_t)
 
@@ -127,6 +134,19 @@ _SIGNATURES = {
     "purlin_embed_grad_bytes": (_sz, [_sz, _sz, _sz]),
     "purlin_embed_grad": (_i, [_vp, _vp, _sz, _i, _vp, _i, _sz, _sz, ctypes.c_float, _vp, _sz, _vp, _sz, _i, _sz,
                                ctypes.c_int64, _vp, _sz, _vp]),
+    "purlin_layer_norm": (_i, [_vp, _vp, _sz, _vp, _sz, _sz, _sz, _i, _vp, _vp, _i, _f, _vp, _sz, _vp, _sz, _vp, _vp]),
+    "purlin_layer_norm_grad_bytes": (_sz, [_sz, _sz]),
+    "purlin_layer_norm_grad": (_i, [_vp, _vp, _sz, _vp, _sz, _vp, _sz, _sz, _i, _vp, _i, _vp, _sz, _vp, _sz, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "purlin_balance_loss_bytes": (_sz, [_sz, _i]),
+    "purlin_balance_loss": (_i, [_vp, _vp, _sz, _i, _vp, _sz, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "purlin_balance_join": (_i, [_vp, _vp, _i, _f, _vp, _vp]),
+    "purlin_balance_loss_grad": (_i, [_vp, _vp, _sz, _i, _vp, _sz, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
+    "purlin_distil_loss": (_i, [_vp, _vp, _sz, _i, _sz, ctypes.POINTER(purlin_distillation), _vp, _vp, _vp, _vp, _vp]),
+    "purlin_distil_parts": (_i, [_vp, _vp, _sz, _i, _sz, ctypes.POINTER(purlin_distillation), _vp, _vp, _vp, _vp]),
+    "purlin_distil_join": (_i, [_vp, _vp, _i, _sz, _f, _f, _vp, _vp, _vp]),
+    "purlin_distil_loss_grad": (_i, [_vp, _vp, _sz, _i, _sz, ctypes.POINTER(purlin_distillation), _vp, _vp, _vp, _vp,
+                                     _vp, _sz, _vp]),
     "purlin_clip_grad_norm_bytes": (_sz, []),
     "purlin_clip_grad_norm": (_i, [_vp, _vp, _vp, _vp, _sz, _i, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
@@ -362,6 +382,82 @@ def purlin_embed_grad(h, grad_out, grad_out_stride, grad_out_dtype, tokens, toke
     return load().purlin_embed_grad(h, _addr(grad_out), grad_out_stride, grad_out_dtype, _addr(tokens), token_bytes, n,
                                     width, scale, _addr(base), base_stride, _addr(grad_table), grad_table_stride,
                                     grad_table_dtype, rows, first, _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def purlin_layer_norm(h, x, x_stride, residual, residual_stride, tokens, width, dtype, weight, bias, weight_dtype, eps,
+                      y, y_stride, total, total_stride, stats, stream=None) -> int:
+    return load().purlin_layer_norm(h, _addr(x), x_stride, _addr(residual), residual_stride, tokens, width, dtype,
+                                    _addr(weight), _addr(bias), weight_dtype, eps, _addr(y), y_stride, _addr(total),
+                                    total_stride, _addr(stats), _stream(stream))
+
+
+def purlin_layer_norm_grad_bytes(tokens, width) -> int:
+    return load().purlin_layer_norm_grad_bytes(tokens, width)
+
+
+def purlin_layer_norm_grad(h, grad_y, grad_y_stride, x, x_stride, stats, tokens, width, dtype, weight, weight_dtype,
+                           grad_total, grad_total_stride, grad_x, grad_x_stride, grad_weight, grad_bias, workspace,
+                           workspace_bytes, stream=None) -> int:
+    return load().purlin_layer_norm_grad(h, _addr(grad_y), grad_y_stride, _addr(x), x_stride, _addr(stats), tokens, width,
+                                         dtype, _addr(weight), weight_dtype, _addr(grad_total), grad_total_stride,
+                                         _addr(grad_x), grad_x_stride, _addr(grad_weight), _addr(grad_bias),
+                                         _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def purlin_balance_loss_bytes(tokens, experts) -> int:
+    return load().purlin_balance_loss_bytes(tokens, experts)
+
+
+def purlin_balance_loss(h, logits, stride, dtype, ids, tokens, top_k, experts, scores, scale, counts, sums, loss,
+                        workspace=None, workspace_bytes=0, stream=None) -> int:
+    return load().purlin_balance_loss(h, _addr(logits), stride, dtype, _addr(ids), tokens, top_k, experts, scores, scale,
+                                      _addr(counts), _addr(sums), _addr(loss), _addr(workspace), workspace_bytes,
+                                      _stream(stream))
+
+
+def purlin_balance_join(h, sums, experts, scale, loss, stream=None) -> int:
+    return load().purlin_balance_join(h, _addr(sums), experts, scale, _addr(loss), _stream(stream))
+
+
+def purlin_balance_loss_grad(h, logits, stride, dtype, ids, tokens, top_k, experts, scores, scale, sums, grad_loss, base,
+                             base_stride, grad_logits, grad_stride, stream=None) -> int:
+    return load().purlin_balance_loss_grad(h, _addr(logits), stride, dtype, _addr(ids), tokens, top_k, experts, scores,
+                                           scale, _addr(sums), _addr(grad_loss), _addr(base), base_stride,
+                                           _addr(grad_logits), grad_stride, _stream(stream))
+
+
+@functools.lru_cache(maxsize=256)
+def _distillation(*values) -> purlin_distillation:
+    return purlin_distillation(*values)
+
+
+def make_distillation(width, first, vocabulary, picks, id_bytes, teacher_dtype, temperature=1.0,
+                      scale=1.0) -> purlin_distillation:
+    """The C struct; one for all calls with the same values, so not to be written to."""
+    return _distillation(_index(width), _index(first), _index(vocabulary), _index(picks), id_bytes, teacher_dtype,
+                         float(temperature), float(scale))
+
+
+def purlin_distil_loss(h, logits, stride, dtype, tokens, d, ids, teacher, loss, stats, stream=None) -> int:
+    return load().purlin_distil_loss(h, _addr(logits), stride, dtype, tokens, ctypes.byref(d), _addr(ids), _addr(teacher),
+                                     _addr(loss), _addr(stats), _stream(stream))
+
+
+def purlin_distil_parts(h, logits, stride, dtype, tokens, d, ids, teacher, parts, stream=None) -> int:
+    return load().purlin_distil_parts(h, _addr(logits), stride, dtype, tokens, ctypes.byref(d), _addr(ids),
+                                      _addr(teacher), _addr(parts), _stream(stream))
+
+
+def purlin_distil_join(h, parts, ranges, tokens, temperature, scale, loss, stats, stream=None) -> int:
+    return load().purlin_distil_join(h, _addr(parts), ranges, tokens, temperature, scale, _addr(loss), _addr(stats),
+                                     _stream(stream))
+
+
+def purlin_distil_loss_grad(h, logits, stride, dtype, tokens, d, ids, teacher, stats, grad_loss, grad_logits, grad_stride,
+                            stream=None) -> int:
+    return load().purlin_distil_loss_grad(h, _addr(logits), stride, dtype, tokens, ctypes.byref(d), _addr(ids),
+                                          _addr(teacher), _addr(stats), _addr(grad_loss), _addr(grad_logits), grad_stride,
+                                          _stream(stream))
 
 
 def purlin_clip_grad_norm_bytes() -> int:

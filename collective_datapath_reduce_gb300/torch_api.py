@@ -450,6 +450,179 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
                        base, ldb, grad_table, ldt, dt, R, int(first))
 
 
+def _vector(t, n, dtype, what, name):
+    """Checks a vector of n columns that may be None."""
+    if t is not None:
+        _packed(t, (n,), dtype, what, name)
+
+
+def layer_norm(x, weight, bias, y, handle: Handle, residual=None, total=None, stats=None, eps=1e-5, stream=None):
+    """y = the layer norm of x + residual (rounded to their dtype, which total
+    receives), times weight, plus bias.  x, residual, total, y: tokens x width of
+    one dtype; weight, bias: width values of one dtype, or None for 1 and 0;
+    residual, total, stats may be None.  stats: float32, tokens x 2, each row's
+    mean and 1 / deviation, for the gradient.  y and total may each be x or
+    residual itself."""
+    what = "layer_norm"
+    T, D = _two(x, what, "x")
+    dt = _values(x, what)
+    ldx = _matrix(x, T, D, x.dtype, what, "x")
+    ldy = _matrix(y, T, D, x.dtype, what, "y")
+    ldr = _matrix(residual, T, D, x.dtype, what, "residual") if residual is not None else 0
+    ldt = _matrix(total, T, D, x.dtype, what, "total") if total is not None else 0
+    of = weight if weight is not None else bias
+    dw = P.PL_F32 if of is None else _values(of, what)
+    _vector(weight, D, of.dtype if of is not None else None, what, "weight")
+    _vector(bias, D, of.dtype if of is not None else None, what, "bias")
+    if stats is not None:
+        _packed(stats, (T, 2), torch.float32, what, "stats")
+    _call(P.purlin_layer_norm, what, handle, stream, x, ldx, residual, ldr, T, D, dt, weight, bias, dw, eps, y, ldy, total,
+          ldt, stats)
+
+
+def layer_norm_grad(grad_y, x, stats, weight, grad_x, grad_weight, grad_bias, handle: Handle, grad_total=None,
+                    stream=None):
+    """grad_x = the gradient of the normalised rows x (layer_norm's total, where
+    it had a residual, whose gradient it is too), plus grad_total; grad_weight
+    and grad_bias = those of weight and bias, in one dtype, each may be None.
+    weight: None for 1.  grad_x may be grad_y, x or grad_total itself."""
+    what = "layer_norm_grad"
+    T, D = _two(grad_y, what, "grad_y")
+    dt = _values(grad_y, what)
+    ldg = _matrix(grad_y, T, D, grad_y.dtype, what, "grad_y")
+    ldx = _matrix(x, T, D, grad_y.dtype, what, "x")
+    _packed(stats, (T, 2), torch.float32, what, "stats")
+    ldt = _matrix(grad_total, T, D, grad_y.dtype, what, "grad_total") if grad_total is not None else 0
+    ldo = _matrix(grad_x, T, D, grad_y.dtype, what, "grad_x")
+    of = next((t for t in (weight, grad_weight, grad_bias) if t is not None), None)
+    dw = P.PL_F32 if of is None else _values(of, what)
+    for t, name in ((weight, "weight"), (grad_weight, "grad_weight"), (grad_bias, "grad_bias")):
+        _vector(t, D, of.dtype if of is not None else None, what, name)
+    nbytes = P.purlin_layer_norm_grad_bytes(T, D) if grad_weight is not None or grad_bias is not None else 0
+    _call_in_workspace(P.purlin_layer_norm_grad, what, handle, stream, nbytes, grad_y, ldg, x, ldx, stats, T, D, dt, weight,
+                       dw, grad_total, ldt, grad_x, ldo, grad_weight, grad_bias)
+
+
+def balance_loss(logits, ids, counts, sums, loss, handle: Handle, scores=Scores.SOFTMAX, scale=1.0, stream=None):
+    """counts[e] = how many of the picks are expert e's; sums = the same, then the
+    sums of the experts' shares of the scores over the tokens that have picks,
+    then the number of these; loss[0] = scale x experts x the mean share of an
+    expert's scores times its share of the picks, added up.  logits and ids as in
+    route_experts; counts: int32, experts values; sums: float32, 2 x experts + 1;
+    loss: one float32, or None where the sums of several ranks are added first
+    (all_reduce, then balance_join)."""
+    what = "balance_loss"
+    T, E = _two(logits, what, "logits")
+    k = _two(ids, what, "ids")[1]
+    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    dt = _values(logits, what)
+    _packed(ids, (T, k), torch.int32, what, "ids")
+    _packed(counts, (E,), torch.int32, what, "counts")
+    _packed(sums, (2 * E + 1,), torch.float32, what, "sums")
+    if loss is not None:
+        _packed(loss, (1,), torch.float32, what, "loss")
+    nbytes = P.purlin_balance_loss_bytes(T, E)
+    _call_in_workspace(P.purlin_balance_loss, what, handle, stream, nbytes, logits, ld, dt, ids, T, k, E, int(scores), scale,
+                       counts, sums, loss)
+
+
+def balance_join(sums, loss, handle: Handle, scale=1.0, stream=None):
+    """loss[0] = balance_loss's of the sums, which may be those of all ranks."""
+    what = "balance_join"
+    if sums.dim() != 1 or sums.shape[0] < 3 or sums.shape[0] % 2 == 0:
+        raise ValueError(f"{what}: sums must hold 2 x experts + 1 values, got {tuple(sums.shape)}")
+    _packed(sums, sums.shape, torch.float32, what, "sums")
+    _packed(loss, (1,), torch.float32, what, "loss")
+    _call(P.purlin_balance_join, what, handle, stream, sums, sums.shape[0] // 2, scale, loss)
+
+
+def balance_loss_grad(logits, ids, sums, grad_loss, grad_logits, handle: Handle, scores=Scores.SOFTMAX, scale=1.0,
+                      base=None, stream=None):
+    """grad_logits = base + grad_loss[0] x the gradient of the loss that sums give,
+    the picks held fixed.  grad_loss: one float32, or None for 1.  base: like
+    grad_logits, or None for 0; base is grad_logits adds in place (to
+    route_experts_grad's, say)."""
+    what = "balance_loss_grad"
+    T, E = _two(logits, what, "logits")
+    k = _two(ids, what, "ids")[1]
+    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    dt = _values(logits, what)
+    _packed(ids, (T, k), torch.int32, what, "ids")
+    _packed(sums, (2 * E + 1,), torch.float32, what, "sums")
+    if grad_loss is not None:
+        _packed(grad_loss, (1,), torch.float32, what, "grad_loss")
+    ldb = _matrix(base, T, E, logits.dtype, what, "base") if base is not None else 0
+    ldg = _matrix(grad_logits, T, E, logits.dtype, what, "grad_logits")
+    _call(P.purlin_balance_loss_grad, what, handle, stream, logits, ld, dt, ids, T, k, E, int(scores), scale, sums,
+          grad_loss, base, ldb, grad_logits, ldg)
+
+
+def _teacher(logits, ids, teacher, what, first, vocabulary, temperature, scale):
+    """Checks what the distillation's calls share: (tokens, width, stride, dtype, the C struct)."""
+    T, R = _two(logits, what, "logits")
+    k = _two(ids, what, "ids")[1]
+    ld = _matrix(logits, T, R, logits.dtype, what, "logits")
+    dt = _values(logits, what)
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{what}: ids must be int32 or int64")
+    _packed(ids, (T, k), ids.dtype, what, "ids")
+    dq = _values(teacher, what)
+    _packed(teacher, (T, k), teacher.dtype, what, "teacher")
+    return T, R, ld, dt, P.make_distillation(R, first, first + R if vocabulary is None else vocabulary, k,
+                                             8 if ids.dtype is torch.int64 else 4, dq, temperature, scale)
+
+
+def distil_loss(logits, ids, teacher, loss, stats, handle: Handle, temperature=1.0, scale=1.0, stream=None):
+    """loss[t] = scale x the Kullback-Leibler divergence of the softmax of
+    logits[t] / temperature from that of teacher[t] / temperature over the words
+    ids[t]; ids outside the vocabulary are no picks, and a token without picks has
+    loss 0.  logits: tokens x vocabulary; ids (int32 or int64) and teacher
+    (float32 or bfloat16): tokens x picks; loss: float32, one for each token;
+    stats: float32, tokens x 2, for the gradient."""
+    what = "distil_loss"
+    T, _, ld, dt, d = _teacher(logits, ids, teacher, what, 0, None, temperature, scale)
+    _packed(loss, (T,), torch.float32, what, "loss")
+    _packed(stats, (T, 2), torch.float32, what, "stats")
+    _call(P.purlin_distil_loss, what, handle, stream, logits, ld, dt, T, d, ids, teacher, loss, stats)
+
+
+def distil_parts(logits, ids, teacher, parts, handle: Handle, first=0, vocabulary=None, temperature=1.0, stream=None):
+    """parts (float32, tokens x 4) = what distil_join needs of one range of the
+    vocabulary.  logits: tokens x words, those of the words first .. first +
+    words; vocabulary: the words of all ranges (None: this is the last)."""
+    what = "distil_parts"
+    T, _, ld, dt, d = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, 1.0)
+    _packed(parts, (T, 4), torch.float32, what, "parts")
+    _call(P.purlin_distil_parts, what, handle, stream, logits, ld, dt, T, d, ids, teacher, parts)
+
+
+def distil_join(parts, loss, stats, handle: Handle, temperature=1.0, scale=1.0, stream=None):
+    """loss and stats as distil_loss gives them, from the parts of all ranges:
+    ranges x tokens x 4, or (ranges x tokens) x 4, as all_gather leaves them."""
+    what = "distil_join"
+    T = loss.numel()
+    ranges = parts.numel() // (4 * T) if T else 1
+    if parts.shape[-1:] != (4,) or ranges == 0 or parts.numel() != 4 * T * ranges:
+        raise ValueError(f"{what}: parts must be ranges x {T} x 4, got {tuple(parts.shape)}")
+    _packed(parts, parts.shape, torch.float32, what, "parts")
+    _packed(loss, (T,), torch.float32, what, "loss")
+    _packed(stats, (T, 2), torch.float32, what, "stats")
+    _call(P.purlin_distil_join, what, handle, stream, parts, ranges, T, temperature, scale, loss, stats)
+
+
+def distil_loss_grad(logits, ids, teacher, stats, grad_loss, grad_logits, handle: Handle, first=0, vocabulary=None,
+                     temperature=1.0, scale=1.0, stream=None):
+    """grad_logits (like logits, or logits itself) = grad_loss[t] x the gradient of
+    loss[t], for a range's logits too, given the whole vocabulary's stats."""
+    what = "distil_loss_grad"
+    T, R, ld, dt, d = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, scale)
+    _packed(stats, (T, 2), torch.float32, what, "stats")
+    _packed(grad_loss, (T,), torch.float32, what, "grad_loss")
+    ldg = _matrix(grad_logits, T, R, logits.dtype, what, "grad_logits")
+    _call(P.purlin_distil_loss_grad, what, handle, stream, logits, ld, dt, T, d, ids, teacher, stats, grad_loss, grad_logits,
+          ldg)
+
+
 _numel, _data_ptr, _is_contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
 _dtype_of = operator.attrgetter("dtype")
 

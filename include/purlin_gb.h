@@ -303,8 +303,11 @@ purlin_status purlin_atom_reduce(purlin_handle h, const void* const* src, int ns
  * norm over many buffers.  Routing decides what an AllToAllV carries; plan,
  * dispatch and combine pack token rows by expert, as purlin_all_to_all_v wants
  * them, and sum them back; the embedding looks tokens up in one rank's range of
- * the vocabulary (an AllReduce sums the ranges' parts); the clip takes the
- * global norm of what a ReduceScatter or AllReduce left.
+ * the vocabulary (an AllReduce sums the ranges' parts); the layer norm stands
+ * behind the sum of a residual and what an AllReduce left; the balance loss looks
+ * at what routing picked; the distillation loss at the logits of a rank's range
+ * of the vocabulary; the clip takes the global norm of what a ReduceScatter or
+ * AllReduce left.
  *
  * The conventions at the top hold (pointers, streams, refusals before any
  * launch), with these additions:
@@ -437,6 +440,117 @@ size_t purlin_clip_grad_norm_bytes(void);
 purlin_status purlin_clip_grad_norm(purlin_handle h, const void* const* grads, void* const* outs, const size_t* counts,
                                     size_t n, purlin_dtype dtype, float scale, float max_norm, float* norm,
                                     void* workspace, size_t workspace_bytes, purlin_stream_t stream);
+
+/* Layer norm behind a residual sum.  t = x + residual, rounded to dtype (x
+ * alone where residual is NULL), which total receives unless NULL; with mean
+ * and variance those of t's row, y = (t - mean) / sqrt(variance + eps) x weight
+ * + bias.  weight and bias (width values of weight_dtype) may each be NULL: 1,
+ * and 0.  stats (tokens x 2, packed), unless NULL, receives each row's mean and
+ * 1 / sqrt(variance + eps), which the gradient reads.  y and total may each be x
+ * or residual itself (same stride).  The variance is the mean of the squares of
+ * the distances from the mean, in binary32: squares that overflow it make the
+ * row's y 0 or NaN. */
+purlin_status purlin_layer_norm(purlin_handle h, const void* x, size_t x_stride, const void* residual,
+                                size_t residual_stride, size_t tokens, size_t width, purlin_dtype dtype,
+                                const void* weight, const void* bias, purlin_dtype weight_dtype, float eps, void* y,
+                                size_t y_stride, void* total, size_t total_stride, float* stats,
+                                purlin_stream_t stream);
+
+/* Its gradient.  x: the rows that were normalised (total, where there was a
+ * residual); xh = (x - mean) / deviation by stats.  grad_x = the gradient of x by
+ * y, plus grad_total (that of total by other ways) unless NULL: that of the
+ * residual too.  grad_weight, grad_bias (width values of weight_dtype, each may be
+ * NULL) = the sums over all tokens of grad_y xh and of grad_y, 0 without tokens.
+ * grad_x may be grad_y, x or grad_total itself (same stride).  width below 2^31;
+ * the workspace 4-byte aligned, and none without grad_weight and grad_bias. */
+size_t purlin_layer_norm_grad_bytes(size_t tokens, size_t width);
+purlin_status purlin_layer_norm_grad(purlin_handle h, const void* grad_y, size_t grad_y_stride, const void* x,
+                                     size_t x_stride, const float* stats, size_t tokens, size_t width,
+                                     purlin_dtype dtype, const void* weight, purlin_dtype weight_dtype,
+                                     const void* grad_total, size_t grad_total_stride, void* grad_x,
+                                     size_t grad_x_stride, void* grad_weight, void* grad_bias, void* workspace,
+                                     size_t workspace_bytes, purlin_stream_t stream);
+
+/* The balance of the experts' load.  logits (tokens x experts) and ids (tokens x
+ * top_k, packed) as in purlin_route_experts; a token without a pick in [0,
+ * experts) is padding and does not count, whatever its logits.  A token's
+ * shares are the softmax of its logits, or its sigmoids over (their sum +
+ * 1e-20); a row of nothing but -inf has shares of 0.  counts (experts values) =
+ * how many picks each expert has; sums (2 x experts + 1) = the same, then the sum
+ * of each expert's shares over the tokens, then the number of tokens.  With C, S
+ * and N those, *loss = scale x experts x (sum of C S) / (sum of C x N), 0 where
+ * nothing counts: scale where all experts are alike.  loss NULL: none.  sums of
+ * ranks are added (purlin_all_reduce) for the loss and gradient of all their
+ * tokens.  The workspace is 4-byte aligned. */
+size_t purlin_balance_loss_bytes(size_t tokens, int experts);
+purlin_status purlin_balance_loss(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype,
+                                  const int32_t* ids, size_t tokens, int top_k, int experts, purlin_scores scores,
+                                  float scale, int32_t* counts, float* sums, float* loss, void* workspace,
+                                  size_t workspace_bytes, purlin_stream_t stream);
+
+/* *loss from sums, as above. */
+purlin_status purlin_balance_join(purlin_handle h, const float* sums, int experts, float scale, float* loss,
+                                  purlin_stream_t stream);
+
+/* grad_logits = base + *grad_loss x the gradient of the loss that sums give, the
+ * picks held fixed: 0 for a token without picks.  grad_loss NULL: 1.  base NULL:
+ * 0; it may be grad_logits itself (same stride).  Added in binary32, rounded
+ * once. */
+purlin_status purlin_balance_loss_grad(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype,
+                                       const int32_t* ids, size_t tokens, int top_k, int experts, purlin_scores scores,
+                                       float scale, const float* sums, const float* grad_loss, const void* base,
+                                       size_t base_stride, void* grad_logits, size_t grad_stride,
+                                       purlin_stream_t stream);
+
+/* Distillation from a teacher's top logits.  Every token has `picks` ids of the
+ * vocabulary and the teacher's logits for them (tokens x picks, packed); an id
+ * outside [0, vocabulary) is no pick.  logits (tokens x width) are the student's
+ * for the words first .. first + width, one rank's range of the vocabulary or all
+ * of it.  With q the softmax of the teacher's logits / temperature over the
+ * token's picks and p that of the student's over the vocabulary, the loss is
+ * scale x the sum over the picks of q (log q - log p): 0 for a token without
+ * picks (or whose picks all have logit -inf), whatever its logits, and for one
+ * whose student's logits are all -inf.  One pick is the cross entropy.  An id
+ * that a token has twice counts as two picks.  A logit of +inf or NaN makes its
+ * token's loss and gradient NaN. */
+#define PURLIN_MAX_PICKS 1024
+typedef struct {
+  size_t width;       /* words of the range */
+  int64_t first;      /* the first of them; first + width at most vocabulary */
+  int64_t vocabulary;
+  int picks;          /* 1 .. PURLIN_MAX_PICKS */
+  int id_bytes;       /* of one id, signed: 4 or 8 */
+  int teacher_dtype;  /* purlin_dtype */
+  float temperature;  /* 1e-30 .. 1e30 */
+  float scale;        /* not of the parts */
+} purlin_distillation;
+
+/* The whole vocabulary at once (first 0, width vocabulary).  stats (tokens x 2,
+ * packed) = each row's largest logit, and the sum of exp((logit - largest) /
+ * temperature), which the gradient reads. */
+purlin_status purlin_distil_loss(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype, size_t tokens,
+                                 const purlin_distillation* d, const void* ids, const void* teacher, float* loss,
+                                 float* stats, purlin_stream_t stream);
+
+/* One range's part (tokens x 4, packed, 8-byte aligned): largest logit and sum as
+ * above, over the range (-inf and 0 for no words), then over the picks in the
+ * range the sums of q (log q - (logit - largest) / temperature) and of q. */
+purlin_status purlin_distil_parts(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype, size_t tokens,
+                                  const purlin_distillation* d, const void* ids, const void* teacher, float* parts,
+                                  purlin_stream_t stream);
+
+/* loss and stats of the whole vocabulary from the parts of all its ranges
+ * (ranges x tokens x 4, as purlin_all_gather leaves them). */
+purlin_status purlin_distil_join(purlin_handle h, const float* parts, int ranges, size_t tokens, float temperature,
+                                 float scale, float* loss, float* stats, purlin_stream_t stream);
+
+/* grad_logits = grad_loss (one value for each token) x the loss's gradient by the
+ * range's logits, given stats of the whole vocabulary.  grad_logits may be logits
+ * itself (same stride).  Values below the smallest normal binary32 number are 0. */
+purlin_status purlin_distil_loss_grad(purlin_handle h, const void* logits, size_t stride, purlin_dtype dtype,
+                                      size_t tokens, const purlin_distillation* d, const void* ids, const void* teacher,
+                                      const float* stats, const float* grad_loss, void* grad_logits, size_t grad_stride,
+                                      purlin_stream_t stream);
 
 /* ------------------------------------------------------ status and tuning */
 

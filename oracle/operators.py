@@ -172,3 +172,124 @@ def clip(grads, max_norm, scale=1.0):
     norm = abs(scale) * math.sqrt(math.fsum(float(np.dot(g.ravel(), g.ravel())) for g in grads))
     factor = 1.0 if math.isinf(max_norm) else min(1.0, max_norm / (norm + 1e-6))
     return [g * (scale * factor) for g in grads], norm
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """(y, stats) of rows x."""
+    y, stats = np.zeros(x.shape), np.zeros((x.shape[0], 2))
+    for t, row in enumerate(x):
+        mean = math.fsum(row) / len(row)
+        rstd = 1.0 / math.sqrt(math.fsum((row - mean) ** 2) / len(row) + eps)
+        y[t] = (row - mean) * rstd * (1.0 if weight is None else weight) + (0.0 if bias is None else bias)
+        stats[t] = mean, rstd
+    return y, stats
+
+
+def layer_norm_grad(grad_y, x, stats, weight=None, grad_total=None):
+    """(grad_x, grad_weight, grad_bias), through each row's Jacobian."""
+    grad_x, grad_weight, grad_bias = np.zeros(x.shape), np.zeros(x.shape[1]), np.zeros(x.shape[1])
+    for t in range(x.shape[0]):
+        hat = (x[t] - stats[t, 0]) * stats[t, 1]
+        g = grad_y[t] * (1.0 if weight is None else weight)
+        grad_x[t] = stats[t, 1] * (g - g.mean() - hat * (g * hat).mean())
+        grad_weight += grad_y[t] * hat
+        grad_bias += grad_y[t]
+    return grad_x + (0.0 if grad_total is None else grad_total), grad_weight, grad_bias
+
+
+def shares_of(x, kind):
+    """A token's scores as shares of one."""
+    s = scores_of(x, kind)
+    return s / (s.sum() + 1e-20) if kind == "sigmoid" else s
+
+
+def balance(logits, ids, kind="softmax", scale=1.0):
+    """(counts, sums, loss)."""
+    T, E = logits.shape
+    counts, shares, tokens = np.zeros(E, dtype=np.int64), np.zeros(E), 0
+    for t in range(T):
+        live = [e for e in ids[t] if 0 <= e < E]
+        if live:
+            tokens += 1
+            shares += shares_of(logits[t], kind)
+            for e in live:
+                counts[e] += 1
+    sums = np.concatenate([counts, shares, [tokens]])
+    return counts, sums, balance_of(sums, scale)
+
+
+def balance_of(sums, scale=1.0):
+    E = len(sums) // 2
+    all_ = sums[:E].sum() * sums[2 * E]
+    return scale * E * np.dot(sums[:E], sums[E:2 * E]) / all_ if all_ > 0 else 0.0
+
+
+def balance_grad(logits, ids, sums, grad_loss=1.0, kind="softmax", scale=1.0):
+    T, E = logits.shape
+    out = np.zeros((T, E))
+    all_ = sums[:E].sum() * sums[2 * E]
+    for t in range(T):
+        if all_ > 0 and any(0 <= e < E for e in ids[t]):
+            c = grad_loss * scale * E * sums[:E] / all_
+            s, p = scores_of(logits[t], kind), shares_of(logits[t], kind)
+            jacobian = np.diag(p) - np.outer(p, p)          # of the shares by the scores' logarithms
+            out[t] = (c @ jacobian) * ((1 - s) if kind == "sigmoid" else 1.0)
+    return out
+
+
+def teacher_of(ids, teacher, vocabulary, temperature):
+    """q of one token's picks, 0 for those that are none."""
+    t = np.where((ids >= 0) & (ids < vocabulary), teacher, -np.inf) / temperature
+    return scores_of(t, "softmax") if np.isfinite(np.max(t)) or np.isnan(np.max(t)) else np.zeros(len(t))
+
+
+def distil_parts(logits, ids, teacher, first=0, vocabulary=None, temperature=1.0):
+    T, R = logits.shape
+    vocabulary = first + R if vocabulary is None else vocabulary
+    out = np.zeros((T, 4))
+    for t in range(T):
+        q = teacher_of(ids[t], teacher[t], vocabulary, temperature)
+        m = np.max(logits[t]) if R else -np.inf
+        ref = m if m > -np.inf else 0.0
+        s = np.exp((logits[t] - ref) / temperature).sum()
+        c = mass = 0.0
+        for k, i in enumerate(ids[t]):
+            if first <= i < first + R and q[k] > 0:
+                c += q[k] * (math.log(q[k]) - (logits[t, i - first] - ref) / temperature)
+                mass += q[k]
+        out[t] = m, s, c, mass
+    return out
+
+
+def distil_join(parts, temperature=1.0, scale=1.0):
+    """(loss, stats) from the parts of all ranges: ranges x tokens x 4."""
+    T = parts.shape[1]
+    loss, stats = np.zeros(T), np.zeros((T, 2))
+    for t in range(T):
+        M = parts[:, t, 0].max()
+        ref = M if M > -np.inf else 0.0
+        own = np.where(parts[:, t, 0] > -np.inf, parts[:, t, 0], 0.0)
+        S = sum(p[1] * math.exp((o - ref) / temperature) for p, o in zip(parts[:, t], own) if p[1] != 0)
+        mass = parts[:, t, 3].sum()
+        stats[t] = M, S
+        if S != 0 and mass != 0:
+            loss[t] = scale * (sum(p[2] - p[3] * (o - ref) / temperature for p, o in zip(parts[:, t], own) if p[3] != 0)
+                               + mass * math.log(S))
+    return loss, stats
+
+
+def distil_grad(logits, ids, teacher, stats, grad_loss, first=0, vocabulary=None, temperature=1.0, scale=1.0):
+    T, R = logits.shape
+    vocabulary = first + R if vocabulary is None else vocabulary
+    out = np.zeros((T, R))
+    for t in range(T):
+        q = teacher_of(ids[t], teacher[t], vocabulary, temperature)
+        if q.sum() == 0 or stats[t, 1] == 0:
+            continue
+        ref = stats[t, 0] if stats[t, 0] > -np.inf else 0.0
+        out[t] = q.sum() * np.exp((logits[t] - ref) / temperature) / stats[t, 1]
+        for k, i in enumerate(ids[t]):
+            if first <= i < first + R:
+                out[t, i - first] -= q[k]
+        out[t] *= grad_loss[t] * scale / temperature
+    return out
