@@ -10,10 +10,11 @@ namespace pl {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kWarps = 8;            // of a CTA, a token each at a time
+constexpr int kWarps = 16;           // of a CTA, a token each at a time
 constexpr int kThreads = kWarps * 32;
+constexpr int kRows = 8;             // warps whose sums have a row of shared memory
 constexpr int kCluster = 8;          // CTAs whose sums are added through shared memory
-constexpr int kMostClusters = 38;    // two CTAs on each of 152 SMs
+constexpr int kMostClusters = 38;    // two CTAs on each of 152 SMs, in the main
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -42,28 +43,28 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
   return v;
 }
 
-// N neighbouring values in each lane; those past `width` read `none`.
+// N neighbouring values in each lane; those past `width` are `none`.
 template <typename T, int N>
-__device__ __forceinline__ void ld_lane(const T* p, int width, bool vec, float none, float (&x)[N]) {
-  const int e0 = (threadIdx.x & 31) * N;
-  constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
-  if (vec) {
-    if (e0 < width) {
+struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Lane {
+  T v[N];
+  __device__ __forceinline__ void load(const T* p, int width, bool vec, float none) {
+    const int e0 = (threadIdx.x & 31) * N;
+    constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
+    if (vec) {
+      if (e0 < width) {
 #pragma unroll
-      for (int q = 0; q < N; q += M) {
-        const Pack<T, M> r = *reinterpret_cast<const Pack<T, M>*>(p + e0 + q);
-#pragma unroll
-        for (int i = 0; i < M; ++i) x[q + i] = to_f32(r.v[i]);
+        for (int q = 0; q < N; q += M)
+          *reinterpret_cast<Pack<T, M>*>(v + q) = *reinterpret_cast<const Pack<T, M>*>(p + e0 + q);
+        return;
       }
-      return;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = from_f32<T>(none);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = e0 + i < width ? p[e0 + i] : from_f32<T>(none);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = none;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = e0 + i < width ? to_f32(p[e0 + i]) : none;
   }
-}
+};
 template <typename T, int N>
 __device__ __forceinline__ void st_lane(T* p, int width, bool vec, const float (&x)[N]) {
   const int e0 = (threadIdx.x & 31) * N;
@@ -84,17 +85,25 @@ __device__ __forceinline__ void st_lane(T* p, int width, bool vec, const float (
   }
 }
 
+// 1 / x, within 1 ulp; of a number past 2^126, 0.
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // A token's logits become its scores as shares of one; `slope` is what a
 // score's derivative has beside them, 1 - sigmoid.  A row of nothing but -inf
-// has shares of 0.
-template <int N>
-__device__ __forceinline__ void shares(float (&x)[N], int sigmoid, float (&slope)[N]) {
+// has shares of 0.  No decision hangs on them, so the reciprocals need not be
+// the nearest numbers.
+template <typename T, int N>
+__device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, float (&x)[N], float (&slope)[N]) {
   float s = 0.f;
   if (sigmoid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float e = expf(-x[i]);
-      x[i] = __frcp_rn(1.f + e);
+      const float e = expf(-to_f32(row.v[i]));
+      x[i] = inverse(1.f + e);
       slope[i] = e < 1.f ? e * x[i] : 1.f - x[i];  // where s is near 1, the difference would be rounding
       s += x[i];
     }
@@ -102,20 +111,21 @@ __device__ __forceinline__ void shares(float (&x)[N], int sigmoid, float (&slope
   } else {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
+    for (int i = 0; i < N; ++i) m = fmaxf(m, to_f32(row.v[i]));
     m = warp_max(m);
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = expf(x[i] - m);
+      x[i] = expf(to_f32(row.v[i]) - m);
       slope[i] = 1.f;
       s += x[i];
     }
     s = warp_sum(s);
     if (s == 0.f) s = 1.f;
   }
+  s = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = __fdiv_rn(x[i], s);
+  for (int i = 0; i < N; ++i) x[i] *= s;
 }
 
 // The loss of picks C, shares P and N tokens: scale x E x sum C P / (sum C x N).
@@ -124,15 +134,18 @@ __device__ __forceinline__ float loss_of(const BalanceArgs& a, float picks, floa
   return all > 0.f ? a.scale * (float)a.experts * __fdiv_rn(dot, all) : 0.f;
 }
 
-// A cluster's CTAs take the experts in turn, `at(e, which)` being an expert's picks (0) or
-// shares (1), and `tokens` the tokens: they write the outputs.  tmp: 2 x 8 words.
+// The threads of a cluster's CTAs take the experts, at(e) being an expert's picks (as
+// bits) and shares, and `tokens` the tokens: they write the outputs.  tmp: two words
+// for each warp.
 template <typename A>
 __device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float* tmp, A at) {
   const uint32_t rank = cluster_rank();
   float picks = 0.f, dot = 0.f;
-  for (int e = (int)rank * kThreads + threadIdx.x; e < a.experts; e += kCluster * kThreads) {
-    const uint32_t c = __float_as_uint(at(e, 0));
-    const float p = at(e, 1);
+  // expert by expert to CTA by CTA, so that few experts too are shared
+  for (int e = (int)rank + kCluster * threadIdx.x; e < a.experts; e += kCluster * kThreads) {
+    const float2 v = at(e);
+    const uint32_t c = __float_as_uint(v.x);
+    const float p = v.y;
     a.counts[e] = (int32_t)c;
     a.sums[e] = (float)c;
     a.sums[a.experts + e] = p;
@@ -150,6 +163,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float
   cluster_sync();
   if (rank == 0 && threadIdx.x < 32) {
     picks = dot = 0.f;
+#pragma unroll
     for (int i = threadIdx.x; i < kCluster * kWarps; i += 32) {
       picks += __uint_as_float(ld_cluster(tmp + i % kWarps, i / kWarps));
       dot += __uint_as_float(ld_cluster(tmp + kWarps + i % kWarps, i / kWarps));
@@ -161,67 +175,100 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float
   cluster_sync();  // before a CTA ends whose memory is read
 }
 
+// A token of a warp: its picks, one in each of the first lanes, and its logits.
+// Fetched a token ahead: padding's logits are loaded too, and not used.
+template <typename T, int N>
+struct Token {
+  int id;
+  Lane<T, N> row;
+  __device__ __forceinline__ void load(const BalanceArgs& a, uint64_t t, int vec) {
+    const int lane = threadIdx.x & 31;
+    id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+    row.load((const T*)a.logits + t * a.ld, a.experts, vec, -INFINITY);
+  }
+};
+
 // A warp holds a token, N neighbouring experts in each lane, and adds its
 // shares to the lane's sums; picks are counted in shared memory.  The warps'
 // sums are added in order, then the cluster's CTAs'.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int clusters) {
+__global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int clusters) {
   op_wait();
-  extern __shared__ float dyn[];   // [kWarps][experts] shares, whose first row the CTA's become; [experts] picks
+  extern __shared__ float dyn[];   // [kRows][experts] shares, whose first row the CTA's become; [experts] picks
   __shared__ uint32_t tokens_of[kWarps];
   __shared__ float tmp[2 * kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
-  uint32_t* picks = (uint32_t*)(dyn + kWarps * E);
+  uint32_t* picks = (uint32_t*)(dyn + kRows * E);
+  const uint64_t step = (uint64_t)gridDim.x * kWarps;
+  // a cluster's CTAs take neighbouring tokens, warp by warp
+  uint64_t t = (uint64_t)blockIdx.x * kWarps + warp;
+  Token<T, N> now, next;
+  constexpr bool AHEAD = N <= 16;  // the registers of a token more
+  if (AHEAD && t < a.tokens) next.load(a, t, vec);
   for (int e = threadIdx.x; e < E; e += kThreads) picks[e] = 0;
   __syncthreads();
   float sum[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) sum[i] = 0.f;
   uint32_t counted = 0;
-  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (uint64_t)gridDim.x * kWarps) {
-    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-    const bool on = id >= 0 && id < E;
+  for (; t < a.tokens; t += step) {
+    if constexpr (AHEAD) {
+      now = next;
+      if (t + step < a.tokens) next.load(a, t + step, vec);
+    } else {
+      now.load(a, t, vec);
+    }
+    const bool on = now.id >= 0 && now.id < E;
     if (!__any_sync(kAll, on)) continue;  // padding: its logits may be anything
-    if (on) atomicAdd(picks + id, 1u);
+    if (on) atomicAdd(picks + now.id, 1u);
     float x[N], slope[N];
-    ld_lane<T, N>((const T*)a.logits + t * a.ld, E, vec, -INFINITY, x);
-    shares<N>(x, a.sigmoid, slope);
+    shares<T, N>(now.row, a.sigmoid, x, slope);
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] += x[i];
     ++counted;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (lane * N + i < E) dyn[warp * E + lane * N + i] = sum[i];
   if (lane == 0) tokens_of[warp] = counted;
-  __syncthreads();
+  // kRows warps at a time: the next ones add to what those before them left
+  for (int first = 0; first < kWarps; first += kRows) {
+    if (warp / kRows == first / kRows)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = lane * N + i;
+        if (e < E) dyn[warp % kRows * E + e] = sum[i] + (first ? dyn[warp % kRows * E + e] : 0.f);
+      }
+    __syncthreads();
+  }
   for (int e = threadIdx.x; e < E; e += kThreads) {
     float s = dyn[e];
-    for (int w = 1; w < kWarps; ++w) s += dyn[w * E + e];
+#pragma unroll
+    for (int w = 1; w < kRows; ++w) s += dyn[w * E + e];
     dyn[e] = s;
   }
   cluster_sync();
+  const uint32_t rank = cluster_rank();
   uint32_t tokens = 0;
-  for (int i = 0; i < kCluster * kWarps; ++i) tokens += ld_cluster(tokens_of + i % kWarps, i / kWarps);
-  auto at = [&](int e, int which) {
-    if (which == 0) {
-      uint32_t c = 0;
-      for (int r = 0; r < kCluster; ++r) c += ld_cluster(picks + e, r);
-      return __uint_as_float(c);
-    }
+  for (int i = lane; i < kCluster * kWarps; i += 32) tokens += ld_cluster(tokens_of + i % kWarps, i / kWarps);
+  tokens = __reduce_add_sync(kAll, tokens);
+  auto at = [&](int e) {
+    uint32_t c = 0;
     float s = 0.f;
-    for (int r = 0; r < kCluster; ++r) s += __uint_as_float(ld_cluster(dyn + e, r));
-    return s;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      c += ld_cluster(picks + e, r);
+      s += __uint_as_float(ld_cluster(dyn + e, r));
+    }
+    return make_float2(__uint_as_float(c), s);
   };
   if (clusters == 1) {
     finish(a, (float)tokens, tmp, at);
   } else {
     uint32_t* out = a.parts + (uint64_t)(blockIdx.x / kCluster) * (2 * E + 1);
-    for (int e = (int)cluster_rank() * kThreads + threadIdx.x; e < E; e += kCluster * kThreads) {
-      out[e] = __float_as_uint(at(e, 0));
-      out[E + e] = __float_as_uint(at(e, 1));
+    for (int e = (int)rank * kThreads + threadIdx.x; e < E; e += kCluster * kThreads) {
+      const float2 v = at(e);
+      out[e] = __float_as_uint(v.x);
+      out[E + e] = __float_as_uint(v.y);
     }
-    if (cluster_rank() == 0 && threadIdx.x == 0) out[2 * E] = tokens;
+    if (rank == 0 && threadIdx.x == 0) out[2 * E] = tokens;
   }
   cluster_sync();
 }
@@ -232,16 +279,17 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(const __grid_co
   __shared__ float tmp[2 * kWarps];
   const int E = a.experts, row = 2 * E + 1;
   uint32_t tokens = 0;
-  for (int p = 0; p < clusters; ++p) tokens += a.parts[(uint64_t)p * row + 2 * E];
-  finish(a, (float)tokens, tmp, [&](int e, int which) {
-    if (which == 0) {
-      uint32_t c = 0;
-      for (int p = 0; p < clusters; ++p) c += a.parts[(uint64_t)p * row + e];
-      return __uint_as_float(c);
-    }
+  for (int p = threadIdx.x & 31; p < clusters; p += 32) tokens += a.parts[(uint64_t)p * row + 2 * E];
+  tokens = __reduce_add_sync(kAll, tokens);
+  finish(a, (float)tokens, tmp, [&](int e) {
+    uint32_t c = 0;
     float s = 0.f;
-    for (int p = 0; p < clusters; ++p) s += __uint_as_float(a.parts[(uint64_t)p * row + E + e]);
-    return s;
+#pragma unroll 10
+    for (int p = 0; p < clusters; ++p) {
+      c += a.parts[(uint64_t)p * row + e];
+      s += __uint_as_float(a.parts[(uint64_t)p * row + E + e]);
+    }
+    return make_float2(__uint_as_float(c), s);
   });
   cluster_sync();
 }
@@ -277,22 +325,38 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(const __grid_con
 // With p the shares and c_e = dL x scale x E x C_e / (sum C x N):  dx_j = p_j (c_j -
 // sum p c), for sigmoids times 1 - s_j.  A token without picks has none.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_constant__ BalanceArgs a, int vec) {
+__global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(const __grid_constant__ BalanceArgs a, int vec) {
   op_wait();
   __shared__ float tmp[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  const uint64_t step = (uint64_t)gridDim.x * kWarps;
+  uint64_t t = (uint64_t)blockIdx.x * kWarps + warp;
+  Token<T, N> now, next;
+  Lane<T, N> base, next_base;
+  constexpr bool AHEAD = N <= 16;  // the registers of a token more
+  if (AHEAD && t < a.tokens) {
+    next.load(a, t, vec);
+    if (a.base) next_base.load((const T*)a.base + t * a.ldb, E, vec, 0.f);
+  }
   const float all = all_picks(a.sums, E, tmp) * a.sums[2 * E];
   const float f = all > 0.f ? __fdiv_rn((a.grad_loss ? *a.grad_loss : 1.f) * a.scale * (float)E, all) : 0.f;
   float c[N];
-  ld_lane<float, N>(a.sums, E, false, 0.f, c);
 #pragma unroll
-  for (int i = 0; i < N; ++i) c[i] *= f;
-  for (uint64_t t = (uint64_t)blockIdx.x * kWarps + warp; t < a.tokens; t += (uint64_t)gridDim.x * kWarps) {
-    const int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+  for (int i = 0; i < N; ++i) c[i] = lane * N + i < E ? f * a.sums[lane * N + i] : 0.f;
+  for (; t < a.tokens; t += step) {
+    if constexpr (AHEAD) {
+      now = next;
+      base = next_base;
+      if (t + step < a.tokens) {
+        next.load(a, t + step, vec);
+        if (a.base) next_base.load((const T*)a.base + (t + step) * a.ldb, E, vec, 0.f);
+      }
+    } else {
+      now.load(a, t, vec);
+    }
     float x[N], slope[N];
-    if (__any_sync(kAll, id >= 0 && id < E)) {
-      ld_lane<T, N>((const T*)a.logits + t * a.ld, E, vec, -INFINITY, x);
-      shares<N>(x, a.sigmoid, slope);
+    if (__any_sync(kAll, now.id >= 0 && now.id < E)) {
+      shares<T, N>(now.row, a.sigmoid, x, slope);
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) dot = __fmaf_rn(x[i], c[i], dot);
@@ -304,9 +368,9 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const __grid_con
       for (int i = 0; i < N; ++i) x[i] = 0.f;
     }
     if (a.base) {
-      ld_lane<T, N>((const T*)a.base + t * a.ldb, E, vec, 0.f, slope);
+      if (!AHEAD) base.load((const T*)a.base + t * a.ldb, E, vec, 0.f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] += slope[i];
+      for (int i = 0; i < N; ++i) x[i] += to_f32(base.v[i]);
     }
     st_lane<T, N>((T*)a.grad_logits + t * a.ldg, E, vec, x);
   }
@@ -333,7 +397,7 @@ bool even(const BalanceArgs& a) {
 }
 
 int clusters_of(uint64_t tokens) {
-  const uint64_t per = kCluster * kWarps;
+  const uint64_t per = kCluster * kWarps * 4;
   return (int)std::max<uint64_t>(1, std::min<uint64_t>(kMostClusters, (tokens + per - 1) / per));
 }
 
@@ -346,7 +410,7 @@ size_t balance_bytes(uint64_t tokens, int experts) {
 
 purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
   const int clusters = clusters_of(a.tokens);
-  const size_t smem = (size_t)(kWarps + 1) * a.experts * sizeof(float);
+  const size_t smem = (size_t)(kRows + 1) * a.experts * sizeof(float);
   const purlin_status st = with_lanes(a.experts, [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (dtype == PL_F32) return op_launch_cluster(kCluster, balance_kernel<float, N>, clusters * kCluster, kThreads, smem, s, a, (int)even<float, N>(a), clusters);
@@ -361,7 +425,7 @@ purlin_status launch_balance_join(const BalanceArgs& a, cudaStream_t s) {
 }
 
 purlin_status launch_balance_grad(const BalanceArgs& a, int dtype, cudaStream_t s) {
-  const uint64_t grid = std::min<uint64_t>((a.tokens + kWarps - 1) / kWarps, 152 * 8);
+  const uint64_t grid = std::min<uint64_t>((a.tokens + kWarps - 1) / kWarps, 152 * 2);
   return with_lanes(a.experts, [&](auto n) {
     constexpr int N = decltype(n)::value;
     if (dtype == PL_F32) return op_launch(balance_grad_kernel<float, N>, grid, kThreads, 0, s, a, (int)even<float, N>(a));

@@ -7,9 +7,9 @@ namespace pl {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kMostThreads = 512;   // of a row
-constexpr int kMostParts = 152;     // CTAs that leave sums of columns, at most
-constexpr int kMostWidth = 8192;    // that a gradient's CTA holds in its registers
+constexpr int kMostThreads = 512;
+constexpr int kSms = 152;
+constexpr int kMostWidth = 8192;  // that 512 threads hold in their registers
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -17,27 +17,104 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Sum over a row's threads, the same in each: a warp, or the whole CTA, whose
-// `tmp` (a word for each warp) no earlier sum has used.
-__device__ __forceinline__ float row_sum(float x, int tpr, float* tmp) {
-  x = warp_sum(x);
-  if (tpr == 32) return x;
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0.f;
-  for (int w = 0; w < tpr >> 5; ++w) x += tmp[w];
-  return x;
+__device__ __forceinline__ void group_barrier(int group, int tpr) {
+  if (tpr == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
 }
 
-// N elements from p; memory that this kernel may write in place, so not through
-// the read-only path.
-template <typename T, int N>
-__device__ __forceinline__ Pack<T, N> ld_in(const T* p, bool on) {
-  if constexpr (N > 1) return ld_pack_if<T, N, Ld::kWritten>(p, on);
-  Pack<T, N> r = zero_pack<T, N>();
-  if (on) r.v[0] = *p;
-  return r;
+// 16 bytes from global into shared memory, when they come.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows on their way into shared memory.  A CTA is `groups` groups of tpr
+// threads, a row each at a time; a group has `stages` slots, a row of each of n
+// matrices in every one, so that stages - 1 rows are under way while one is
+// worked on.  Aligned rows: a thread copies the vectors that it uses, and waits
+// for nobody else.  Others (SHIFT): the aligned granules that hold the row's
+// bytes, which the threads then share.
+struct Ring {
+  int n, stages, tpr, groups;
+  uint32_t granules;  // of a row's slot
+  uint32_t smem() const { return (uint32_t)(n * stages * groups) * granules * 16; }
+};
+
+template <typename T, bool SHIFT, int NV>
+struct Stream {
+  const Ring& r;
+  const char* base[3];
+  uint64_t ld[3];       // bytes
+  uint64_t tokens, row, step;  // the next row to fetch, and the distance to the one behind it
+  uint32_t bytes;       // of a row
+  int tid, group, slot_in, slot_out, done;
+
+  __device__ __forceinline__ Stream(const Ring& ring, uint64_t tokens, uint64_t width)
+      : r(ring), tokens(tokens), bytes((uint32_t)(width * sizeof(T))), slot_in(0), slot_out(0), done(0) {
+    tid = threadIdx.x % r.tpr;
+    group = threadIdx.x / r.tpr;
+    row = (uint64_t)blockIdx.x * r.groups + group;
+    step = (uint64_t)gridDim.x * r.groups;
+  }
+  __device__ __forceinline__ char* slot(char* smem, int stage, int m) const {
+    return smem + (uint64_t)((stage * r.n + m) * r.groups + group) * r.granules * 16;
+  }
+  // One more row, or an empty step behind the last.
+  __device__ __forceinline__ void fetch(char* smem) {
+    if (row < tokens) {
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        if (m >= r.n) break;
+        const char* p = base[m] + row * ld[m];
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(smem, slot_in, m));
+        if constexpr (SHIFT) {
+          const uint32_t off = (uint32_t)((uintptr_t)p & 15u), g = (off + bytes + 15) / 16;
+          for (uint32_t i = tid; i < g; i += r.tpr) copy16(to + i * 16, p - off + (uint64_t)i * 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const uint32_t i = tid + j * r.tpr;
+            if (i * 16 < bytes) copy16(to + i * 16, p + (uint64_t)i * 16);
+          }
+        }
+      }
+      row += step;
+    }
+    copies_close();
+    slot_in = slot_in + 1 == r.stages ? 0 : slot_in + 1;
+  }
+  __device__ __forceinline__ void begin(char* smem) {
+    for (int i = 1; i < r.stages; ++i) fetch(smem);
+  }
+  // Waits for the oldest row, then fetches one into the slot that the row before it left.
+  __device__ __forceinline__ int next(char* smem) {
+    if (r.stages == 2) copies_left<0>();
+    else if (r.stages == 3) copies_left<1>();
+    else copies_left<2>();
+    if (SHIFT) group_barrier(group, r.tpr);
+    const int at = slot_out;
+    fetch(smem);
+    slot_out = at + 1 == r.stages ? 0 : at + 1;
+    return at;
+  }
+  // The row's vector j of this thread, or its element j; zeros beside the row.
+  template <int N>
+  __device__ __forceinline__ Pack<T, N> get(char* smem, int stage, int m, uint64_t at_row, int j, bool on) const {
+    const char* s = slot(smem, stage, m);
+    Pack<T, N> v = zero_pack<T, N>();
+    if constexpr (!SHIFT) {
+      if (on) v = *reinterpret_cast<const Pack<T, N>*>(s + (tid + j * r.tpr) * 16);
+      return v;
+    }
+    const uint32_t off = (uint32_t)((uintptr_t)(base[m] + at_row * ld[m]) & 15u);
+    if (on) v.v[0] = *reinterpret_cast<const T*>(s + off + (tid + j * r.tpr) * sizeof(T));
+    return v;
+  }
+};
 
 // N columns of a weight or bias, or `none` where there is no such vector.
 template <typename W, int N>
@@ -57,69 +134,118 @@ __device__ __forceinline__ void ld_columns(const void* p, uint64_t c, bool on, f
 
 __device__ __forceinline__ float inverse(float variance, float eps) { return __frcp_rn(__fsqrt_rn(variance + eps)); }
 
-// A row in the registers of tpr threads, NV vectors of N elements in each: the
-// mean, then the squares of the distances from it, then the result.
+// Rows pass through a CTA's registers, NV vectors of N elements in each of a row's
+// threads, and its weights stay there.  A warp takes the mean of its part and
+// the squares of the distances from that; the warps' means and squares join to
+// the row's, (sum of squares) + n (mean of the part - mean)^2 each, behind one
+// barrier.
 template <typename T, typename W, int N, int NV>
-__global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constant__ NormArgs a, int tpr) {
+__global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Ring ring) {
   op_wait();
-  __shared__ float tmp[2][kMostThreads / 32];
-  const int tid = threadIdx.x % tpr;
-  const uint64_t row = (uint64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-  if (row >= a.tokens) return;
-  const T* x = (const T*)a.x + row * a.ldx;
-  Pack<T, N> p[NV];
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float2 tmp[2][kMostThreads / 32];
+  constexpr bool SHIFT = N == 1;
+  Stream<T, SHIFT, NV> in(ring, a.tokens, a.width);
+  in.base[0] = (const char*)a.x;
+  in.ld[0] = a.ldx * sizeof(T);
+  in.base[1] = (const char*)a.residual;
+  in.ld[1] = a.ldr * sizeof(T);
+  in.base[2] = nullptr;
+  in.ld[2] = 0;
+  uint64_t row = in.row;
+  const uint64_t step = in.step;
+  const int tid = in.tid, tpr = ring.tpr, warps = tpr >> 5, warp = tid >> 5;
+  const uint32_t D = (uint32_t)a.width;
+  in.begin(smem);
+  float w[NV][N], b[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const uint64_t c = (uint64_t)(tid + j * tpr) * N;
-    p[j] = ld_in<T, N>(x + c, c < a.width);
+    const uint32_t c = (uint32_t)(tid + j * tpr) * N;
+    ld_columns<W, N>(a.weight, c, c < D, 1.f, w[j]);
+    ld_columns<W, N>(a.bias, c, c < D, 0.f, b[j]);
   }
-  if (a.residual) {
-    const T* r = (const T*)a.residual + row * a.ldr;
-    Pack<T, N> q[NV];
+  // elements of this warp, and of any warp: those of vectors 32 warp + j tpr .. + 32
+  auto part = [&](int of) {
+    uint32_t n = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(tid + j * tpr) * N;
-      q[j] = ld_in<T, N>(r + c, c < a.width);
+      const uint32_t first = (uint32_t)(of * 32 + j * tpr) * N;
+      n += first < D ? min(D - first, 32u * N) : 0u;
     }
+    return n;
+  };
+  const float mine = (float)part(warp), per_mine = mine > 0.f ? __frcp_rn(mine) : 0.f, per = __frcp_rn((float)D);
+  // lane i joins warp i's
+  const int lane = tid & 31;
+  const float of_lane = lane < warps ? (float)part(lane) : 0.f, per_lane = of_lane > 0.f ? __frcp_rn(of_lane) : 0.f;
+  int turn = 0;
+  for (; row < a.tokens; row += step) {
+    const int at = in.next(smem);
+    float v[NV][N], s = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const bool on = (uint32_t)(tid + j * tpr) * N < D;
+      const Pack<T, N> p = in.template get<N>(smem, at, 0, row, j, on);
+      if (a.residual) {
+        const Pack<T, N> q = in.template get<N>(smem, at, 1, row, j, on);
 #pragma unroll
-      for (int i = 0; i < N; ++i) p[j].v[i] = from_f32<T>(to_f32(p[j].v[i]) + to_f32(q[j].v[i]));
-  }
-  float s = 0.f;
+        for (int i = 0; i < N; ++i) v[j][i] = to_f32(from_f32<T>(to_f32(p.v[i]) + to_f32(q.v[i])));
+      } else {
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+        for (int i = 0; i < N; ++i) v[j][i] = to_f32(p.v[i]);
+      }
 #pragma unroll
-    for (int i = 0; i < N; ++i) s += to_f32(p[j].v[i]);
-  const float mean = __fdiv_rn(row_sum(s, tpr, tmp[0]), (float)a.width);
-  s = 0.f;
+      for (int i = 0; i < N; ++i) s += v[j][i];
+    }
+    s = warp_sum(s);
+    float mean = s * per_mine, squares = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const bool on = (uint64_t)(tid + j * tpr) * N < a.width;
+    for (int j = 0; j < NV; ++j) {
+      const bool on = (uint32_t)(tid + j * tpr) * N < D;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = to_f32(p[j].v[i]) - mean;
-      if (on) s = __fmaf_rn(d, d, s);
+      for (int i = 0; i < N; ++i) {
+        const float d = v[j][i] - mean;
+        if (on) squares = __fmaf_rn(d, d, squares);
+      }
+    }
+    squares = warp_sum(squares);
+    if (warps > 1) {
+      float2* t = tmp[turn] + in.group * warps;
+      turn ^= 1;
+      if (lane == 0) t[warp] = make_float2(s, squares);
+      group_barrier(in.group, tpr);
+      const float2 of = lane < warps ? t[lane] : make_float2(0.f, 0.f);
+      mean = warp_sum(of.x) * per;
+      const float d = __fmaf_rn(of.x, per_lane, -mean);
+      squares = warp_sum(__fmaf_rn(of_lane * d, d, of.y));
+    }
+    const float rstd = inverse(squares * per, a.eps);
+    if (a.stats && tid == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint32_t c = (uint32_t)(tid + j * tpr) * N;
+      if (c >= D) break;
+      Pack<T, N> o;
+      if (a.total) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(v[j][i]);
+        st_pack((T*)a.total + row * a.ldt + c, o);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(__fmaf_rn((v[j][i] - mean) * rstd, w[j][i], b[j][i]));
+      st_pack((T*)a.y + row * a.ldy + c, o);
     }
   }
-  const float rstd = inverse(__fdiv_rn(row_sum(s, tpr, tmp[1]), (float)a.width), a.eps);
-  if (a.stats && tid == 0) {
-    a.stats[2 * row] = mean;
-    a.stats[2 * row + 1] = rstd;
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint64_t c = (uint64_t)(tid + j * tpr) * N;
-    if (c >= a.width) break;
-    if (a.total) st_pack((T*)a.total + row * a.ldt + c, p[j]);
-    float w[N], b[N];
-    ld_columns<W, N>(a.weight, c, true, 1.f, w);
-    ld_columns<W, N>(a.bias, c, true, 0.f, b);
-    Pack<T, N> o;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(__fmaf_rn((to_f32(p[j].v[i]) - mean) * rstd, w[i], b[i]));
-    st_pack((T*)a.y + row * a.ldy + c, o);
-  }
+}
+
+// Sum over a CTA, the same in each thread; `tmp`: a word for each warp, which no earlier sum has used.
+__device__ __forceinline__ float cta_sum(float x, float* tmp) {
+  x = warp_sum(x);
+  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0.f;
+  for (int w = 0; w < kMostThreads / 32; ++w) x += tmp[w];
+  return x;
 }
 
 // Rows of any width: read three times, twice of these from the caches.  Where y
@@ -137,13 +263,13 @@ __global__ void __launch_bounds__(kMostThreads) norm_wide_kernel(const __grid_co
   };
   float s = 0.f;
   for (uint64_t c = threadIdx.x; c < a.width; c += kMostThreads) s += value(c);
-  const float mean = __fdiv_rn(row_sum(s, kMostThreads, tmp[0]), (float)a.width);
+  const float mean = __fdiv_rn(cta_sum(s, tmp[0]), (float)a.width);
   s = 0.f;
   for (uint64_t c = threadIdx.x; c < a.width; c += kMostThreads) {
     const float d = value(c) - mean;
     s = __fmaf_rn(d, d, s);
   }
-  const float rstd = inverse(__fdiv_rn(row_sum(s, kMostThreads, tmp[1]), (float)a.width), a.eps);
+  const float rstd = inverse(__fdiv_rn(cta_sum(s, tmp[1]), (float)a.width), a.eps);
   if (a.stats && threadIdx.x == 0) {
     a.stats[2 * row] = mean;
     a.stats[2 * row + 1] = rstd;
@@ -164,15 +290,20 @@ __global__ void __launch_bounds__(kMostThreads) norm_wide_kernel(const __grid_co
 // columns' sums over the rows that pass through it; a second kernel adds the
 // CTAs' sums, in order.
 
-// Sums of two values over a row's threads: the tpr of a group, which has the
-// CTA's barrier 1 + group and two rows of `tmp` that it uses in turn.
+// Sums of two values over a row's threads; `tmp`: a place for each warp, of two rows that are used in turn.
 __device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float2* tmp) {
-  x.x = warp_sum(x.x);
-  x.y = warp_sum(x.y);
+  // the two halves of the warp take one value each
+  const bool upper = threadIdx.x & 16;
+  const float other = __shfl_xor_sync(kAll, upper ? x.x : x.y, 16);
+  float v = (upper ? x.y : x.x) + other;
+#pragma unroll
+  for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  x.x = __shfl_sync(kAll, v, 0);
+  x.y = __shfl_sync(kAll, v, 16);
   if (tpr == 32) return x;
   const int warp = (threadIdx.x >> 5) - group * (tpr >> 5);
   if ((threadIdx.x & 31) == 0) tmp[warp] = x;
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  group_barrier(group, tpr);
   x = make_float2(0.f, 0.f);
   for (int w = 0; w < tpr >> 5; ++w) {
     x.x += tmp[w].x;
@@ -182,12 +313,24 @@ __device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float2
 }
 
 template <typename T, typename W, int N, int NV>
-__global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_constant__ NormArgs a, int tpr) {
+__global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_constant__ NormArgs a,
+                                                                 const __grid_constant__ Ring ring) {
   op_wait();
-  extern __shared__ float sums[];  // [groups][2][width]
+  extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
   __shared__ float2 tmp[2][kMostThreads / 32];
-  const int tid = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  constexpr bool SHIFT = N == 1;
+  Stream<T, SHIFT, NV> in(ring, a.tokens, a.width);
+  in.base[0] = (const char*)a.x;
+  in.ld[0] = a.ldx * sizeof(T);
+  in.base[1] = (const char*)a.grad_y;
+  in.ld[1] = a.ldg * sizeof(T);
+  in.base[2] = (const char*)a.grad_total;
+  in.ld[2] = a.ldgt * sizeof(T);
+  uint64_t row = in.row;
+  const uint64_t step = in.step;
+  const int tid = in.tid, tpr = ring.tpr, group = in.group, groups = ring.groups;
   const uint32_t D = (uint32_t)a.width;
+  in.begin(smem);
   const float per = __frcp_rn((float)D);
   float w[NV][N], dw[NV][N], db[NV][N];
 #pragma unroll
@@ -198,26 +341,20 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
     for (int i = 0; i < N; ++i) dw[j][i] = db[j][i] = 0.f;
   }
   int turn = 0;
-  for (uint64_t row = (uint64_t)blockIdx.x * groups + group; row < a.tokens; row += (uint64_t)gridDim.x * groups) {
-    const T* x = (const T*)a.x + row * a.ldx;
-    const T* dy = (const T*)a.grad_y + row * a.ldg;
-    const T* dt = a.grad_total ? (const T*)a.grad_total + row * a.ldgt : nullptr;
-    Pack<T, N> px[NV], pg[NV], pt[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint32_t c = (uint32_t)(tid + j * tpr) * N;
-      px[j] = ld_in<T, N>(x + c, c < D);
-      pg[j] = ld_in<T, N>(dy + c, c < D);
-      pt[j] = ld_in<T, N>(dt + c, dt && c < D);
-    }
-    const float mean = a.stats[2 * row], rstd = a.stats[2 * row + 1];
+  float2 ahead = row < a.tokens ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
+  for (; row < a.tokens; row += step) {
+    const int at = in.next(smem);
+    const float mean = ahead.x, rstd = ahead.y;
+    if (row + step < a.tokens) ahead = *reinterpret_cast<const float2*>(a.stats + 2 * (row + step));
     float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      const bool on = (uint32_t)(tid + j * tpr) * N < D;
       // beside the row, dy is 0: no sum takes part of it
+      const Pack<T, N> px = in.template get<N>(smem, at, 0, row, j, on), pg = in.template get<N>(smem, at, 1, row, j, on);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float xh = (to_f32(px[j].v[i]) - mean) * rstd, d = to_f32(pg[j].v[i]), g = d * w[j][i];
+        const float xh = (to_f32(px.v[i]) - mean) * rstd, d = to_f32(pg.v[i]), g = d * w[j][i];
         dw[j][i] = __fmaf_rn(d, xh, dw[j][i]);
         db[j][i] += d;
         s.x += g;
@@ -231,17 +368,28 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
     for (int j = 0; j < NV; ++j) {
       const uint32_t c = (uint32_t)(tid + j * tpr) * N;
       if (c >= D) break;
-      Pack<T, N> o;
+      const Pack<T, N> px = in.template get<N>(smem, at, 0, row, j, true), pg = in.template get<N>(smem, at, 1, row, j, true);
+      float v[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float xh = (to_f32(px[j].v[i]) - mean) * rstd, g = to_f32(pg[j].v[i]) * w[j][i];
-        const float v = rstd * (__fmaf_rn(-xh, mx, g - m));
-        o.v[i] = from_f32<T>(dt ? v + to_f32(pt[j].v[i]) : v);
+        const float xh = (to_f32(px.v[i]) - mean) * rstd, g = to_f32(pg.v[i]) * w[j][i];
+        v[i] = rstd * (__fmaf_rn(-xh, mx, g - m));
       }
+      if (a.grad_total) {
+        const Pack<T, N> pt = in.template get<N>(smem, at, 2, row, j, true);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += to_f32(pt.v[i]);
+      }
+      Pack<T, N> o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(v[i]);
       st_pack((T*)a.y + row * a.ldy + c, o);
     }
   }
   if (!a.parts) return;
+  copies_left<0>();
+  __syncthreads();
+  float* sums = (float*)smem;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -329,21 +477,62 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ 
 
 bool even(const void* p, uint64_t ld, uint64_t size) { return !p || (((uintptr_t)p | ld * size) & 15u) == 0; }
 
-int whole_warps(uint64_t threads) { return (int)((threads + 31) / 32 * 32); }
-
-// f(vector's elements, vectors of a thread): the fewest with which 512 threads
-// cover a row of up to kMostWidth elements.
-template <int N, typename F>
-purlin_status with_vectors(uint64_t width, F f) {
-  using std::integral_constant;
-  const uint64_t nv = (width + N - 1) / N;
-  if (nv <= kMostThreads) return f(integral_constant<int, N>(), integral_constant<int, 1>());
-  if (N == 8 || nv <= kMostThreads * 2) return f(integral_constant<int, N>(), integral_constant<int, 2>());
-  if constexpr (N < 8) {
-    if (N == 4 || nv <= kMostThreads * 4) return f(integral_constant<int, N>(), integral_constant<int, 4>());
-    if constexpr (N < 4) return f(integral_constant<int, N>(), integral_constant<int, 16>());
+// How the threads of a CTA share rows: NV vectors of N elements in each, in groups
+// of tpr threads.  The group whose row costs the fewest instructions, by NV vectors
+// of 14 instructions an element and 40 around them in each warp, 30 more where
+// warps wait for each other: a warp for a row of 520 binary32 values takes 5
+// vectors a lane (.. us), 5 warps one each (.. us).
+template <int N, int NV>
+void try_shape(uint64_t width, int* best, int* nv, int* tpr) {
+  const int t = (int)((width + 32 * N * NV - 1) / (32 * N * NV)) * 32;
+  if (t > kMostThreads) return;
+  const int cost = t / 32 * (NV * N * 14 + 40 + (t > 32 ? 30 : 0));
+  if (*best == 0 || cost < *best) {
+    *best = cost;
+    *nv = NV;
+    *tpr = t;
   }
-  return PL_ERR_UNSUPPORTED;
+}
+
+template <int N, typename F>
+purlin_status with_shape(uint64_t width, F f) {
+  using std::integral_constant;
+  int best = 0, nv = 0, tpr = 0;
+  constexpr integral_constant<int, N> n;
+  if constexpr (N == 8) {
+    try_shape<8, 1>(width, &best, &nv, &tpr);
+    try_shape<8, 2>(width, &best, &nv, &tpr);
+    try_shape<8, 3>(width, &best, &nv, &tpr);
+    return nv == 1 ? f(n, integral_constant<int, 1>(), tpr) : nv == 2 ? f(n, integral_constant<int, 2>(), tpr) : f(n, integral_constant<int, 3>(), tpr);
+  } else if constexpr (N == 4) {
+    try_shape<4, 1>(width, &best, &nv, &tpr);
+    try_shape<4, 2>(width, &best, &nv, &tpr);
+    try_shape<4, 4>(width, &best, &nv, &tpr);
+    try_shape<4, 5>(width, &best, &nv, &tpr);
+    return nv == 1 ? f(n, integral_constant<int, 1>(), tpr) : nv == 2 ? f(n, integral_constant<int, 2>(), tpr) :
+           nv == 4 ? f(n, integral_constant<int, 4>(), tpr) : f(n, integral_constant<int, 5>(), tpr);
+  } else {
+    try_shape<1, 4>(width, &best, &nv, &tpr);
+    try_shape<1, 16>(width, &best, &nv, &tpr);
+    return nv == 4 ? f(n, integral_constant<int, 4>(), tpr) : f(n, integral_constant<int, 16>(), tpr);
+  }
+}
+
+constexpr uint32_t kSmem = 200 * 1024;
+
+// The ring of a launch, with as many stages (2 to 4) as fit.
+template <typename T, int N, int NV>
+Ring ring_of(uint64_t width, int tpr, int n) {
+  Ring r = {};
+  r.n = n;
+  r.tpr = tpr;
+  r.groups = kMostThreads / tpr;
+  r.granules = (uint32_t)(width * sizeof(T) + (N == 1 ? 30 : 0)) / 16;
+  for (r.stages = 4; r.stages > 2 && r.smem() > kSmem; --r.stages) {
+  }
+  // rows of 8192 binary32 values of three matrices still fit twice
+  while (r.groups > 1 && r.smem() > kSmem) --r.groups;
+  return r;
 }
 
 template <typename T, typename W>
@@ -353,12 +542,14 @@ purlin_status norm_t(const NormArgs& a, cudaStream_t s) {
   const uint64_t es = sizeof(T);
   const bool vec = a.width % V == 0 && even(a.x, a.ldx, es) && even(a.residual, a.ldr, es) && even(a.y, a.ldy, es) &&
                    even(a.total, a.ldt, es) && even(a.weight, 0, 1) && even(a.bias, 0, 1);
-  auto go = [&](auto n, auto nv) {
+  auto go = [&](auto n, auto nv, int tpr) {
     constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
-    const int tpr = whole_warps((a.width + N * NV - 1) / (N * NV)), per = tpr == 32 ? 4 : 1;
-    return op_launch(norm_kernel<T, W, N, NV>, (a.tokens + per - 1) / per, tpr * per, 0, s, a, tpr);
+    const Ring r = ring_of<T, N, NV>(a.width, tpr, a.residual ? 2 : 1);
+    const uint64_t grid = std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
+    if (purlin_status e = op_smem((const void*)norm_kernel<T, W, N, NV>, r.smem(), kSmem)) return e;
+    return op_launch(norm_kernel<T, W, N, NV>, grid, tpr * r.groups, r.smem(), s, a, r);
   };
-  return vec ? with_vectors<V>(a.width, go) : with_vectors<1>(a.width, go);
+  return vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
 }
 
 template <typename T, typename W>
@@ -370,23 +561,22 @@ purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
   int parts = 0;
   purlin_status st = PL_OK;
   if (a.width > (uint64_t)kMostWidth) {
-    parts = (int)std::min<uint64_t>(kMostParts, a.tokens);
+    parts = (int)std::min<uint64_t>(kSms, a.tokens);
     // the columns first: dx may lie on what they read
     if (sums) st = op_launch(norm_columns_kernel<T>, (a.width + kColumns - 1) / kColumns * parts, kColumns, 0, s, a, parts);
     if (!st) st = op_launch(norm_grad_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a);
   } else if (a.tokens) {
     const bool vec = a.width % V == 0 && even(a.x, a.ldx, es) && even(a.grad_y, a.ldg, es) && even(a.y, a.ldy, es) &&
                      even(a.grad_total, a.ldgt, es) && even(a.weight, 0, 1);
-    auto go = [&](auto n, auto nv) {
+    auto go = [&](auto n, auto nv, int tpr) {
       constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
-      const int tpr = whole_warps((a.width + N * NV - 1) / (N * NV)), groups = kMostThreads / tpr;
-      parts = (int)std::min<uint64_t>(kMostParts, (a.tokens + groups - 1) / groups);
-      const size_t smem = sums ? (size_t)groups * 2 * a.width * sizeof(float) : 0;
-      const void* fn = (const void*)norm_grad_kernel<T, W, N, NV>;
-      if (purlin_status e = op_smem(fn, smem, kMostThreads * N * NV * 2 * (int)sizeof(float))) return e;
-      return op_launch(norm_grad_kernel<T, W, N, NV>, parts, tpr * groups, smem, s, a, tpr);
+      const Ring r = ring_of<T, N, NV>(a.width, tpr, a.grad_total ? 3 : 2);
+      parts = (int)std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
+      const uint32_t of_sums = sums ? (uint32_t)(r.groups * 2 * a.width * sizeof(float)) : 0, smem = std::max(r.smem(), of_sums);
+      if (purlin_status e = op_smem((const void*)norm_grad_kernel<T, W, N, NV>, smem, kSmem)) return e;
+      return op_launch(norm_grad_kernel<T, W, N, NV>, parts, tpr * r.groups, smem, s, a, r);
     };
-    st = vec ? with_vectors<V>(a.width, go) : with_vectors<1>(a.width, go);
+    st = vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
   }
   if (st || !sums) return st;
   return op_launch(norm_join_kernel<W>, (a.width + 31) / 32 * 2, 256, 0, s, a, parts);
@@ -396,7 +586,7 @@ purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
 
 // Sums of a weight's and a bias's gradient for each of the CTAs that leave them.
 size_t norm_grad_bytes(uint64_t tokens, uint64_t width) {
-  return (size_t)(std::min<uint64_t>(kMostParts, tokens) * 2 * width * sizeof(float));
+  return (size_t)(std::min<uint64_t>(kSms, tokens) * 2 * width * sizeof(float));
 }
 
 purlin_status launch_norm(const NormArgs& a, int dtype, int w_dtype, cudaStream_t s) {
