@@ -12,9 +12,9 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 16;           // of a CTA, a token each at a time
 constexpr int kThreads = kWarps * 32;
+constexpr int kMostCtas = 2 * 152;   // that leave sums
 constexpr int kRows = 8;             // warps whose sums have a row of shared memory
 constexpr int kCluster = 8;          // CTAs whose sums are added through shared memory
-constexpr int kMostClusters = 38;    // two CTAs on each of 152 SMs, in the main
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -92,17 +92,24 @@ __device__ __forceinline__ float inverse(float x) {
   return y;
 }
 
+// e^x; results below the smallest normal number are 0.
+__device__ __forceinline__ float exponential(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
 // A token's logits become its scores as shares of one; `slope` is what a
 // score's derivative has beside them, 1 - sigmoid.  A row of nothing but -inf
-// has shares of 0.  No decision hangs on them, so the reciprocals need not be
-// the nearest numbers.
+// has shares of 0.  No decision hangs on them, so neither exponentials nor
+// reciprocals need be the nearest numbers.
 template <typename T, int N>
 __device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, float (&x)[N], float (&slope)[N]) {
   float s = 0.f;
   if (sigmoid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float e = expf(-to_f32(row.v[i]));
+      const float e = exponential(-to_f32(row.v[i]));
       x[i] = inverse(1.f + e);
       slope[i] = e < 1.f ? e * x[i] : 1.f - x[i];  // where s is near 1, the difference would be rounding
       s += x[i];
@@ -116,7 +123,7 @@ __device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, float
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = expf(to_f32(row.v[i]) - m);
+      x[i] = exponential(to_f32(row.v[i]) - m);
       slope[i] = 1.f;
       s += x[i];
     }
@@ -134,23 +141,23 @@ __device__ __forceinline__ float loss_of(const BalanceArgs& a, float picks, floa
   return all > 0.f ? a.scale * (float)a.experts * __fdiv_rn(dot, all) : 0.f;
 }
 
-// The threads of a cluster's CTAs take the experts, at(e) being an expert's picks (as
-// bits) and shares, and `tokens` the tokens: they write the outputs.  tmp: two words
-// for each warp.
+// The threads of this CTA, of a cluster's, take experts first .. first + per, at(e)
+// being an expert's picks (as bits) and shares, and `tokens` the tokens: they
+// write the outputs.  tmp: two words for each warp.
 template <typename A>
-__device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float* tmp, A at) {
+__device__ __forceinline__ void finish(const BalanceArgs& a, float tokens, float* tmp, int first, int per, A at) {
   const uint32_t rank = cluster_rank();
   float picks = 0.f, dot = 0.f;
-  // expert by expert to CTA by CTA, so that few experts too are shared
-  for (int e = (int)rank + kCluster * threadIdx.x; e < a.experts; e += kCluster * kThreads) {
+  const int e = first + threadIdx.x;
+  if ((int)threadIdx.x < per && e < a.experts) {
     const float2 v = at(e);
     const uint32_t c = __float_as_uint(v.x);
     const float p = v.y;
     a.counts[e] = (int32_t)c;
     a.sums[e] = (float)c;
     a.sums[a.experts + e] = p;
-    picks += (float)c;
-    dot = __fmaf_rn((float)c, p, dot);
+    picks = (float)c;
+    dot = (float)c * p;
   }
   if (rank == 0 && threadIdx.x == 0) a.sums[2 * a.experts] = tokens;
   if (!a.loss) return;
@@ -190,9 +197,9 @@ struct Token {
 
 // A warp holds a token, N neighbouring experts in each lane, and adds its
 // shares to the lane's sums; picks are counted in shared memory.  The warps'
-// sums are added in order, then the cluster's CTAs'.
+// sums are added in order, then, of one cluster `alone`, the CTAs'.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int clusters) {
+__global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int alone) {
   op_wait();
   extern __shared__ float dyn[];   // [kRows][experts] shares, whose first row the CTA's become; [experts] picks
   __shared__ uint32_t tokens_of[kWarps];
@@ -244,12 +251,25 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
     for (int w = 1; w < kRows; ++w) s += dyn[w * E + e];
     dyn[e] = s;
   }
+  if (!alone) {  // this CTA's sums are for balance_parts_kernel
+    uint32_t* out = a.parts + (uint64_t)blockIdx.x * (2 * E + 1);
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      out[e] = picks[e];
+      out[E + e] = __float_as_uint(dyn[e]);
+    }
+    if (threadIdx.x == 0) {
+      uint32_t tokens = 0;
+      for (int w = 0; w < kWarps; ++w) tokens += tokens_of[w];
+      out[2 * E] = tokens;
+    }
+    return;
+  }
   cluster_sync();
-  const uint32_t rank = cluster_rank();
   uint32_t tokens = 0;
   for (int i = lane; i < kCluster * kWarps; i += 32) tokens += ld_cluster(tokens_of + i % kWarps, i / kWarps);
   tokens = __reduce_add_sync(kAll, tokens);
-  auto at = [&](int e) {
+  const int per = (E + kCluster - 1) / kCluster;
+  finish(a, (float)tokens, tmp, (int)cluster_rank() * per, per, [&](int e) {
     uint32_t c = 0;
     float s = 0.f;
 #pragma unroll
@@ -258,36 +278,40 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
       s += __uint_as_float(ld_cluster(dyn + e, r));
     }
     return make_float2(__uint_as_float(c), s);
-  };
-  if (clusters == 1) {
-    finish(a, (float)tokens, tmp, at);
-  } else {
-    uint32_t* out = a.parts + (uint64_t)(blockIdx.x / kCluster) * (2 * E + 1);
-    for (int e = (int)rank * kThreads + threadIdx.x; e < E; e += kCluster * kThreads) {
-      const float2 v = at(e);
-      out[e] = __float_as_uint(v.x);
-      out[E + e] = __float_as_uint(v.y);
-    }
-    if (rank == 0 && threadIdx.x == 0) out[2 * E] = tokens;
-  }
+  });
   cluster_sync();
 }
 
-// The clusters' sums, added in order.
-__global__ void __launch_bounds__(kThreads) balance_parts_kernel(const __grid_constant__ BalanceArgs a, int clusters) {
+// The CTAs' sums: a cluster whose CTAs take `per` neighbouring experts each, in
+// up to 32 threads each that share the CTAs' sums and are added in order.
+__global__ void __launch_bounds__(kThreads) balance_parts_kernel(const __grid_constant__ BalanceArgs a, int ctas, int per) {
   op_wait();
   __shared__ float tmp[2 * kWarps];
-  const int E = a.experts, row = 2 * E + 1;
+  __shared__ float sum[kThreads];
+  __shared__ uint32_t picks[kThreads];
+  const int E = a.experts, row = 2 * E + 1, first = (int)cluster_rank() * per;
   uint32_t tokens = 0;
-  for (int p = threadIdx.x & 31; p < clusters; p += 32) tokens += a.parts[(uint64_t)p * row + 2 * E];
-  tokens = __reduce_add_sync(kAll, tokens);
-  finish(a, (float)tokens, tmp, [&](int e) {
-    uint32_t c = 0;
-    float s = 0.f;
-#pragma unroll 10
-    for (int p = 0; p < clusters; ++p) {
+  for (int p = threadIdx.x & 31; p < ctas; p += 32) tokens += a.parts[(uint64_t)p * row + 2 * E];
+  const int columns = min(kThreads / per, 32), e = first + threadIdx.x % per;
+  uint32_t c = 0;
+  float s = 0.f;
+  if (e < E && (int)threadIdx.x < columns * per) {
+#pragma unroll 8
+    for (int p = threadIdx.x / per; p < ctas; p += columns) {
       c += a.parts[(uint64_t)p * row + e];
       s += __uint_as_float(a.parts[(uint64_t)p * row + E + e]);
+    }
+  }
+  picks[threadIdx.x] = c;
+  sum[threadIdx.x] = s;
+  tokens = __reduce_add_sync(kAll, tokens);
+  __syncthreads();
+  finish(a, (float)tokens, tmp, first, per, [&](int e) {
+    uint32_t c = 0;
+    float s = 0.f;
+    for (int q = 0; q < columns; ++q) {
+      c += picks[q * per + e - first];
+      s += sum[q * per + e - first];
     }
     return make_float2(__uint_as_float(c), s);
   });
@@ -396,28 +420,28 @@ bool even(const BalanceArgs& a) {
   return a.experts % N == 0 && bits % need == 0;  // every lane's experts exist or none
 }
 
-int clusters_of(uint64_t tokens) {
-  const uint64_t per = kCluster * kWarps * 4;
-  return (int)std::max<uint64_t>(1, std::min<uint64_t>(kMostClusters, (tokens + per - 1) / per));
-}
+// Few tokens go through one cluster and one launch: 4 for each of its warps.
+bool few(uint64_t tokens) { return tokens <= kCluster * kWarps * 4; }
+int ctas_of(uint64_t tokens) { return few(tokens) ? kCluster : (int)std::min<uint64_t>(kMostCtas, (tokens + kWarps - 1) / kWarps); }
 
 }  // namespace
 
 size_t balance_bytes(uint64_t tokens, int experts) {
-  const int clusters = clusters_of(tokens);
-  return clusters == 1 ? 0 : (size_t)clusters * (2 * (size_t)experts + 1) * sizeof(uint32_t);
+  return few(tokens) ? 0 : (size_t)ctas_of(tokens) * (2 * (size_t)experts + 1) * sizeof(uint32_t);
 }
 
 purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
-  const int clusters = clusters_of(a.tokens);
+  const bool alone = few(a.tokens);
+  const int ctas = ctas_of(a.tokens), per = (a.experts + kCluster - 1) / kCluster;
   const size_t smem = (size_t)(kRows + 1) * a.experts * sizeof(float);
   const purlin_status st = with_lanes(a.experts, [&](auto n) {
     constexpr int N = decltype(n)::value;
-    if (dtype == PL_F32) return op_launch_cluster(kCluster, balance_kernel<float, N>, clusters * kCluster, kThreads, smem, s, a, (int)even<float, N>(a), clusters);
-    return op_launch_cluster(kCluster, balance_kernel<bf16, N>, clusters * kCluster, kThreads, smem, s, a, (int)even<bf16, N>(a), clusters);
+    const int c = alone ? kCluster : 1;
+    if (dtype == PL_F32) return op_launch_cluster(c, balance_kernel<float, N>, ctas, kThreads, smem, s, a, (int)even<float, N>(a), (int)alone);
+    return op_launch_cluster(c, balance_kernel<bf16, N>, ctas, kThreads, smem, s, a, (int)even<bf16, N>(a), (int)alone);
   });
-  if (st || clusters == 1) return st;
-  return op_launch_cluster(kCluster, balance_parts_kernel, kCluster, kThreads, 0, s, a, clusters);
+  if (st || alone) return st;
+  return op_launch_cluster(kCluster, balance_parts_kernel, kCluster, kThreads, 0, s, a, ctas, per);
 }
 
 purlin_status launch_balance_join(const BalanceArgs& a, cudaStream_t s) {

@@ -238,6 +238,70 @@ __device__ __forceinline__ Pack<T, N> zero_pack() {
   return r;
 }
 
+// Two binary32 values that one instruction takes at once, each rounded as alone.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float both(F2 a) {
+  const float2 s = split(a);
+  return s.x + s.y;
+}
+
+// 16 bytes of T as pairs, and back (bf16: rounded two at a time).
+__device__ __forceinline__ F2 pair_of(uint32_t bf16x2) {
+  return f2(__uint_as_float(bf16x2 << 16), __uint_as_float(bf16x2 & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t bf16x2_of(F2 a) {
+  const float2 s = split(a);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(s.y), "f"(s.x));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void pairs_of(uint4 u, F2* p) {
+  if constexpr (sizeof(T) == 2) {
+    p[0] = pair_of(u.x);
+    p[1] = pair_of(u.y);
+    p[2] = pair_of(u.z);
+    p[3] = pair_of(u.w);
+  } else {
+    p[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+    p[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 packed(const F2* p) {
+  if constexpr (sizeof(T) == 2) return make_uint4(bf16x2_of(p[0]), bf16x2_of(p[1]), bf16x2_of(p[2]), bf16x2_of(p[3]));
+  const float2 a = split(p[0]), b = split(p[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+
 __device__ __forceinline__ void op_status(uint32_t* status, uint32_t what) { atomicCAS(status, 0u, what); }
 
 constexpr int kRowThreads = 256;

@@ -11,6 +11,8 @@
 // of the lowest value are rows like others.
 #include <math.h>
 
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace pl {
@@ -34,6 +36,31 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ F2 ex2(F2 x) {
+  const float2 s = split(x);
+  return f2(ex2(s.x), ex2(s.y));
+}
+
+// The largest of m and the elements of F vectors, NaN the lesser of any two.
+template <typename T, int F>
+__device__ __forceinline__ float largest(const uint4 (&x)[F], float m) {
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 top = __bfloat162bfloat162(__ushort_as_bfloat16(0xFF80));  // -inf
+#pragma unroll
+    for (int u = 0; u < F; ++u) {
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __hmax2(top, reinterpret_cast<const __nv_bfloat162&>(w[i]));
+    }
+    return fmaxf(m, fmaxf(__low2float(top), __high2float(top)));
+  } else {
+#pragma unroll
+    for (int u = 0; u < F; ++u)
+      m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(x[u].x)), fmaxf(__uint_as_float(x[u].y), __uint_as_float(x[u].z))), __uint_as_float(x[u].w));
+    return m;
+  }
 }
 
 // A maximum and the sum of 2^(scale (x - maximum)) of the values behind it; a
@@ -105,7 +132,7 @@ __device__ __forceinline__ uint64_t share(uint64_t nv, uint32_t rank, uint32_t s
 template <typename T>
 __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant__ DistilArgs a, int split) {
   op_wait();
-  constexpr int V = V16<T>, F = 4;
+  constexpr int V = V16<T>;
   __shared__ float2 of_warp[kWarps], of_cta[kMostCluster];
   __shared__ float best_of[kWarps];
   __shared__ float sum_of[3][kWarps];
@@ -120,28 +147,30 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
 
   Picks<T> picks;
   if (rank == 0) picks.load(a, token, row);
-  float m = -INFINITY, s = 0.f;
-  for (uint64_t v = v0 + tid; v < v1; v += F * kThreads) {
-    Pack<T, V> x[F];
+  float m = -INFINITY;
+  F2 sum = f2(0.f);
+  auto step = [&](auto number, uint64_t v) {
+    constexpr int F = decltype(number)::value, P = V / 2;
+    uint4 x[F];
 #pragma unroll
-    for (int u = 0; u < F; ++u) x[u] = ld_pack_if<T, V>(body + (v + u * kThreads) * V, v + u * kThreads < v1);
+    for (int u = 0; u < F; ++u) x[u] = ld16_if(body + (v + u * kThreads) * V, true);
 #pragma unroll
-    for (int u = 0; u < F; ++u) pin(x[u]);
-    float top = m;
-#pragma unroll
-    for (int u = 0; u < F; ++u)
-      if (v + u * kThreads < v1)
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, to_f32(x[u].v[i]));
-    const float n = at_least(top);
-    s *= ex2((m - n) * c);
+    for (int u = 0; u < F; ++u) asm volatile("" : "+r"(x[u].x), "+r"(x[u].y), "+r"(x[u].z), "+r"(x[u].w));
+    const float top = largest<T, F>(x, m), n = at_least(top);
+    sum = sum * f2(ex2((m - n) * c));
     m = top;
 #pragma unroll
-    for (int u = 0; u < F; ++u)
-      if (v + u * kThreads < v1)
+    for (int u = 0; u < F; ++u) {
+      F2 p[P];
+      pairs_of<T>(x[u], p);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += ex2((to_f32(x[u].v[i]) - n) * c);
-  }
+      for (int i = 0; i < P; ++i) sum = sum + ex2((p[i] + f2(-n)) * f2(c));
+    }
+  };
+  uint64_t v = v0 + tid;
+  for (; v + 3 * kThreads < v1; v += 4 * kThreads) step(std::integral_constant<int, 4>(), v);
+  for (; v < v1; v += kThreads) step(std::integral_constant<int, 1>(), v);
+  float s = both(sum);
   if (rank == 0 && tid < cut.beside) {
     const float x = to_f32(row[cut.at<V>(tid)]);
     s = __fmaf_rn(s, ex2((m - at_least(fmaxf(m, x))) * c), ex2((x - at_least(fmaxf(m, x))) * c));
@@ -244,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) distil_join_kernel(const __grid_cons
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_constant__ DistilArgs a, int split) {
   op_wait();
-  constexpr int V = V16<T>, F = 4;
+  constexpr int V = V16<T>;
   __shared__ float best_of[kWarps], sum_of[kWarps];
   __shared__ int64_t id_of[PURLIN_MAX_PICKS];
   __shared__ float q_of[PURLIN_MAX_PICKS];
@@ -287,24 +316,33 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
 
   const T* from = row + cut.head;
   T* to = out + cut.head;
-  for (uint64_t v = v0 + tid; v < v1; v += F * kThreads) {
-    Pack<T, V> x[F];
+  auto step = [&](auto number, uint64_t v) {
+    constexpr int F = decltype(number)::value, P = V / 2;
+    uint4 x[F];
 #pragma unroll
     for (int u = 0; u < F; ++u) {
-      const bool on = v + u * kThreads < v1;
       const T* p = from + (v + u * kThreads) * V;
-      if constexpr (SHIFT) x[u] = ld_row_if<T, true>(p, on);
-      else x[u] = ld_pack_if<T, V, Ld::kWritten>(p, on);
+      if constexpr (SHIFT) {
+        const Pack<T, V> r = ld_row_if<T, true>(p, true);
+        memcpy(&x[u], &r, 16);
+      } else {
+        x[u] = ld16_if<Ld::kWritten>(p, true);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < F; ++u) pin(x[u]);
+    for (int u = 0; u < F; ++u) asm volatile("" : "+r"(x[u].x), "+r"(x[u].y), "+r"(x[u].z), "+r"(x[u].w));
 #pragma unroll
     for (int u = 0; u < F; ++u) {
+      F2 p[P];
+      pairs_of<T>(x[u], p);
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[u].v[i] = from_f32<T>(grad(to_f32(x[u].v[i])));
-      if (v + u * kThreads < v1) st_pack(to + (v + u * kThreads) * V, x[u]);
+      for (int i = 0; i < P; ++i) p[i] = none ? f2(0.f) : f2(f) * ex2((p[i] + f2(-m)) * f2(c));
+      *reinterpret_cast<uint4*>(to + (v + u * kThreads) * V) = packed<T>(p);
     }
-  }
+  };
+  uint64_t v = v0 + tid;
+  for (; v + 3 * kThreads < v1; v += 4 * kThreads) step(std::integral_constant<int, 4>(), v);
+  for (; v < v1; v += kThreads) step(std::integral_constant<int, 1>(), v);
   if (rank == 0 && tid < cut.beside) {
     const uint64_t i = cut.at<V>(tid);
     out[i] = from_f32<T>(grad(to_f32(row[i])));

@@ -44,8 +44,10 @@ struct Ring {
   uint32_t smem() const { return (uint32_t)(n * stages * groups) * granules * 16; }
 };
 
-template <typename T, bool SHIFT, int NV>
+template <typename T, int N, int NV>
 struct Stream {
+  static constexpr bool SHIFT = N == 1;
+  static constexpr int P = N * NV / 2;  // pairs of a thread
   const Ring& r;
   const char* base[3];
   uint64_t ld[3];       // bytes
@@ -101,36 +103,80 @@ struct Stream {
     slot_out = at + 1 == r.stages ? 0 : at + 1;
     return at;
   }
-  // The row's vector j of this thread, or its element j; zeros beside the row.
-  template <int N>
-  __device__ __forceinline__ Pack<T, N> get(char* smem, int stage, int m, uint64_t at_row, int j, bool on) const {
-    const char* s = slot(smem, stage, m);
-    Pack<T, N> v = zero_pack<T, N>();
+  // What this thread has of the row, as pairs; zeros beside the row.
+  __device__ __forceinline__ void get(const char* smem, int stage, int m, uint64_t at_row, F2 (&v)[P]) const {
+    const char* s = slot((char*)smem, stage, m);
     if constexpr (!SHIFT) {
-      if (on) v = *reinterpret_cast<const Pack<T, N>*>(s + (tid + j * r.tpr) * 16);
-      return v;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t i = (tid + j * r.tpr) * 16;
+        pairs_of<T>(i < bytes ? *reinterpret_cast<const uint4*>(s + i) : make_uint4(0, 0, 0, 0), v + j * (P / NV));
+      }
+    } else {
+      s += (uint32_t)((uintptr_t)(base[m] + at_row * ld[m]) & 15u);
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) {
+        const uint32_t i = (tid + j * r.tpr) * sizeof(T), k = i + r.tpr * sizeof(T);
+        v[j / 2] = f2(i < bytes ? to_f32(*reinterpret_cast<const T*>(s + i)) : 0.f,
+                      k < bytes ? to_f32(*reinterpret_cast<const T*>(s + k)) : 0.f);
+      }
     }
-    const uint32_t off = (uint32_t)((uintptr_t)(base[m] + at_row * ld[m]) & 15u);
-    if (on) v.v[0] = *reinterpret_cast<const T*>(s + off + (tid + j * r.tpr) * sizeof(T));
-    return v;
+  }
+  // The same into a row of global memory, rounded; `v` becomes what is stored.
+  __device__ __forceinline__ void put(T* to, F2 (&v)[P]) const {
+    if constexpr (!SHIFT) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t i = (tid + j * r.tpr) * 16;
+        if (i < bytes) *reinterpret_cast<uint4*>((char*)to + i) = packed<T>(v + j * (P / NV));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) {
+        const uint32_t i = tid + j * r.tpr, k = i + r.tpr;
+        const float2 x = split(v[j / 2]);
+        if (i * sizeof(T) < bytes) to[i] = from_f32<T>(x.x);
+        if (k * sizeof(T) < bytes) to[k] = from_f32<T>(x.y);
+      }
+    }
+  }
+  // A vector of columns, or `none` where there is no such vector or column.
+  template <typename W>
+  __device__ __forceinline__ void columns(const void* p, float none, F2 (&v)[P]) const {
+    float x[2 * P];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[j * N + i] = none;
+    if (p)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t c = (tid + j * r.tpr) * N;
+        if (c * sizeof(T) >= bytes) break;
+        const W* w = (const W*)p + c;
+        constexpr int M = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
+#pragma unroll
+        for (int q = 0; q < N; q += M) {
+          const Pack<W, M> of = *reinterpret_cast<const Pack<W, M>*>(w + q);
+#pragma unroll
+          for (int i = 0; i < M; ++i) x[j * N + q + i] = to_f32(of.v[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = f2(x[2 * i], x[2 * i + 1]);
+  }
+  // 1 in place of the row's elements, 0 beside them.
+  __device__ __forceinline__ F2 inside(int pair) const {
+    const int j = pair * 2 / N;
+    if constexpr (!SHIFT) return f2((tid + j * r.tpr) * 16 < bytes ? 1.f : 0.f);
+    return f2((tid + j * r.tpr) * sizeof(T) < bytes ? 1.f : 0.f, (tid + (j + 1) * r.tpr) * sizeof(T) < bytes ? 1.f : 0.f);
+  }
+  // The column of a pair's first (0) or second (1) element.
+  __device__ __forceinline__ uint32_t column(int pair, int second) const {
+    const int e = 2 * pair + second;
+    return (tid + e / N * r.tpr) * N + e % N;
   }
 };
-
-// N columns of a weight or bias, or `none` where there is no such vector.
-template <typename W, int N>
-__device__ __forceinline__ void ld_columns(const void* p, uint64_t c, bool on, float none, float (&out)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) out[i] = none;
-  if (!p || !on) return;
-  const W* w = (const W*)p + c;
-  constexpr int M = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
-#pragma unroll
-  for (int q = 0; q < N; q += M) {
-    const Pack<W, M> r = *reinterpret_cast<const Pack<W, M>*>(w + q);
-#pragma unroll
-    for (int i = 0; i < M; ++i) out[q + i] = to_f32(r.v[i]);
-  }
-}
 
 __device__ __forceinline__ float inverse(float variance, float eps) { return __frcp_rn(__fsqrt_rn(variance + eps)); }
 
@@ -144,8 +190,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   op_wait();
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 tmp[2][kMostThreads / 32];
-  constexpr bool SHIFT = N == 1;
-  Stream<T, SHIFT, NV> in(ring, a.tokens, a.width);
+  constexpr int P = N * NV / 2;
+  Stream<T, N, NV> in(ring, a.tokens, a.width);
   in.base[0] = (const char*)a.x;
   in.ld[0] = a.ldx * sizeof(T);
   in.base[1] = (const char*)a.residual;
@@ -157,13 +203,9 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   const int tid = in.tid, tpr = ring.tpr, warps = tpr >> 5, warp = tid >> 5;
   const uint32_t D = (uint32_t)a.width;
   in.begin(smem);
-  float w[NV][N], b[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint32_t c = (uint32_t)(tid + j * tpr) * N;
-    ld_columns<W, N>(a.weight, c, c < D, 1.f, w[j]);
-    ld_columns<W, N>(a.bias, c, c < D, 0.f, b[j]);
-  }
+  F2 w[P], b[P];
+  in.template columns<W>(a.weight, 1.f, w);
+  in.template columns<W>(a.bias, 0.f, b);
   // elements of this warp, and of any warp: those of vectors 32 warp + j tpr .. + 32
   auto part = [&](int of) {
     uint32_t n = 0;
@@ -181,34 +223,27 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   int turn = 0;
   for (; row < a.tokens; row += step) {
     const int at = in.next(smem);
-    float v[NV][N], s = 0.f;
+    F2 v[P], sum = f2(0.f);
+    in.get(smem, at, 0, row, v);
+    if (a.residual) {
+      F2 q[P];
+      in.get(smem, at, 1, row, q);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool on = (uint32_t)(tid + j * tpr) * N < D;
-      const Pack<T, N> p = in.template get<N>(smem, at, 0, row, j, on);
-      if (a.residual) {
-        const Pack<T, N> q = in.template get<N>(smem, at, 1, row, j, on);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j][i] = to_f32(from_f32<T>(to_f32(p.v[i]) + to_f32(q.v[i])));
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[j][i] = to_f32(p.v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) s += v[j][i];
-    }
-    s = warp_sum(s);
-    float mean = s * per_mine, squares = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool on = (uint32_t)(tid + j * tpr) * N < D;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float d = v[j][i] - mean;
-        if (on) squares = __fmaf_rn(d, d, squares);
+      for (int i = 0; i < P; ++i) {
+        v[i] = v[i] + q[i];
+        if constexpr (sizeof(T) == 2) v[i] = pair_of(bf16x2_of(v[i]));  // the norm is of what is stored
       }
     }
-    squares = warp_sum(squares);
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum = sum + v[i];
+    float s = warp_sum(both(sum)), mean = s * per_mine;
+    sum = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const F2 d = fma2(in.inside(i), f2(-mean), v[i]);  // 0 beside the row
+      sum = fma2(d, d, sum);
+    }
+    float squares = warp_sum(both(sum));
     if (warps > 1) {
       float2* t = tmp[turn] + in.group * warps;
       turn ^= 1;
@@ -221,20 +256,10 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     }
     const float rstd = inverse(squares * per, a.eps);
     if (a.stats && tid == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+    if (a.total) in.put((T*)a.total + row * a.ldt, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint32_t c = (uint32_t)(tid + j * tpr) * N;
-      if (c >= D) break;
-      Pack<T, N> o;
-      if (a.total) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(v[j][i]);
-        st_pack((T*)a.total + row * a.ldt + c, o);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(__fmaf_rn((v[j][i] - mean) * rstd, w[j][i], b[j][i]));
-      st_pack((T*)a.y + row * a.ldy + c, o);
-    }
+    for (int i = 0; i < P; ++i) v[i] = fma2((v[i] + f2(-mean)) * f2(rstd), w[i], b[i]);
+    in.put((T*)a.y + row * a.ldy, v);
   }
 }
 
@@ -318,8 +343,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   op_wait();
   extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
   __shared__ float2 tmp[2][kMostThreads / 32];
-  constexpr bool SHIFT = N == 1;
-  Stream<T, SHIFT, NV> in(ring, a.tokens, a.width);
+  constexpr int P = N * NV / 2;
+  Stream<T, N, NV> in(ring, a.tokens, a.width);
   in.base[0] = (const char*)a.x;
   in.ld[0] = a.ldx * sizeof(T);
   in.base[1] = (const char*)a.grad_y;
@@ -332,74 +357,68 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   const uint32_t D = (uint32_t)a.width;
   in.begin(smem);
   const float per = __frcp_rn((float)D);
-  float w[NV][N], dw[NV][N], db[NV][N];
+  F2 w[P], dw[P], db[P];
+  in.template columns<W>(a.weight, 1.f, w);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint32_t c = (uint32_t)(tid + j * tpr) * N;
-    ld_columns<W, N>(a.weight, c, c < D, 1.f, w[j]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) dw[j][i] = db[j][i] = 0.f;
-  }
+  for (int i = 0; i < P; ++i) dw[i] = db[i] = f2(0.f);
   int turn = 0;
   float2 ahead = row < a.tokens ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
   for (; row < a.tokens; row += step) {
     const int at = in.next(smem);
     const float mean = ahead.x, rstd = ahead.y;
     if (row + step < a.tokens) ahead = *reinterpret_cast<const float2*>(a.stats + 2 * (row + step));
-    float2 s = make_float2(0.f, 0.f);
+    F2 x[P], g[P], sum = f2(0.f), sum_xh = f2(0.f);
+    in.get(smem, at, 0, row, x);
+    in.get(smem, at, 1, row, g);
+    // beside the row, dy is 0: no sum takes part of it
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool on = (uint32_t)(tid + j * tpr) * N < D;
-      // beside the row, dy is 0: no sum takes part of it
-      const Pack<T, N> px = in.template get<N>(smem, at, 0, row, j, on), pg = in.template get<N>(smem, at, 1, row, j, on);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float xh = (to_f32(px.v[i]) - mean) * rstd, d = to_f32(pg.v[i]), g = d * w[j][i];
-        dw[j][i] = __fmaf_rn(d, xh, dw[j][i]);
-        db[j][i] += d;
-        s.x += g;
-        s.y = __fmaf_rn(g, xh, s.y);
-      }
+    for (int i = 0; i < P; ++i) {
+      x[i] = (x[i] + f2(-mean)) * f2(rstd);
+      dw[i] = fma2(g[i], x[i], dw[i]);
+      db[i] = db[i] + g[i];
+      g[i] = g[i] * w[i];
+      sum = sum + g[i];
+      sum_xh = fma2(g[i], x[i], sum_xh);
     }
+    float2 s = make_float2(both(sum), both(sum_xh));
     s = group_sum(s, tpr, group, tmp[turn] + group * (tpr >> 5));
     turn ^= 1;
-    const float m = s.x * per, mx = s.y * per;
+    const F2 m = f2(-s.x * per), mx = f2(-s.y * per);
+    if constexpr (P > 8) {  // too many registers to hold them while the warps wait
+      in.get(smem, at, 0, row, x);
+      in.get(smem, at, 1, row, g);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint32_t c = (uint32_t)(tid + j * tpr) * N;
-      if (c >= D) break;
-      const Pack<T, N> px = in.template get<N>(smem, at, 0, row, j, true), pg = in.template get<N>(smem, at, 1, row, j, true);
-      float v[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float xh = (to_f32(px.v[i]) - mean) * rstd, g = to_f32(pg.v[i]) * w[j][i];
-        v[i] = rstd * (__fmaf_rn(-xh, mx, g - m));
+      for (int i = 0; i < P; ++i) {
+        x[i] = (x[i] + f2(-mean)) * f2(rstd);
+        g[i] = g[i] * w[i];
       }
-      if (a.grad_total) {
-        const Pack<T, N> pt = in.template get<N>(smem, at, 2, row, j, true);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += to_f32(pt.v[i]);
-      }
-      Pack<T, N> o;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(v[i]);
-      st_pack((T*)a.y + row * a.ldy + c, o);
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = f2(rstd) * fma2(x[i], mx, g[i] + m);
+    if (a.grad_total) {
+      in.get(smem, at, 2, row, g);
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[i] = x[i] + g[i];
+    }
+    in.put((T*)a.y + row * a.ldy, x);
   }
   if (!a.parts) return;
   copies_left<0>();
   __syncthreads();
   float* sums = (float*)smem;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t c = (uint32_t)(tid + j * tpr) * N + i;
-      if (c < D) {
-        sums[(2 * group) * D + c] = dw[j][i];
-        sums[(2 * group + 1) * D + c] = db[j][i];
-      }
+  for (int i = 0; i < P; ++i) {
+    const float2 of_w = split(dw[i]), of_b = split(db[i]);
+    const uint32_t c = in.column(i, 0), e = in.column(i, 1);
+    if (c < D) {
+      sums[2 * group * D + c] = of_w.x;
+      sums[(2 * group + 1) * D + c] = of_b.x;
     }
+    if (e < D) {
+      sums[2 * group * D + e] = of_w.y;
+      sums[(2 * group + 1) * D + e] = of_b.y;
+    }
+  }
   __syncthreads();
   for (uint32_t c = threadIdx.x; c < 2 * D; c += blockDim.x) {
     float v = 0.f;
