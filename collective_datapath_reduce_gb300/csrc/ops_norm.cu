@@ -31,6 +31,23 @@ template <int N>
 __device__ __forceinline__ void copies_left() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  return u;
+}
+template <typename T>
+__device__ __forceinline__ float ld_shared1(uint32_t at) {
+  if constexpr (sizeof(T) == 4) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+  } else {
+    unsigned short x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+    return __uint_as_float((uint32_t)x << 16);
+  }
+}
 
 // Rows on their way into shared memory.  A CTA is `groups` groups of tpr
 // threads, a row each at a time; a group has `stages` slots, a row of each of n
@@ -44,137 +61,139 @@ struct Ring {
   uint32_t smem() const { return (uint32_t)(n * stages * groups) * granules * 16; }
 };
 
-template <typename T, int N, int NV>
+// A thread's view of a row: NV vectors of N elements, tpr vectors apart, as P
+// pairs.  Beside the row it reads the row's first vector (element) in place of
+// what is not there: `inside` is 0 for those, and they are not written.
+template <typename T, int N, int NV, int M>
 struct Stream {
   static constexpr bool SHIFT = N == 1;
-  static constexpr int P = N * NV / 2;  // pairs of a thread
-  const Ring& r;
-  const char* base[3];
-  uint64_t ld[3];       // bytes
-  uint64_t tokens, row, step;  // the next row to fetch, and the distance to the one behind it
-  uint32_t bytes;       // of a row
-  int tid, group, slot_in, slot_out, done;
+  static constexpr int P = N * NV / 2, S = N * (int)sizeof(T);  // S: bytes of a vector
+  const char* from[M];   // the next row to fetch, of each matrix
+  uint64_t step[M];      // bytes to the one behind it
+  uint64_t left;         // rows to fetch
+  uint32_t bytes, matrix, stage, slots, in, out, first;  // of shared memory
+  int tid, group, tpr, stages;
 
-  __device__ __forceinline__ Stream(const Ring& ring, uint64_t tokens, uint64_t width)
-      : r(ring), tokens(tokens), bytes((uint32_t)(width * sizeof(T))), slot_in(0), slot_out(0), done(0) {
-    tid = threadIdx.x % r.tpr;
-    group = threadIdx.x / r.tpr;
-    row = (uint64_t)blockIdx.x * r.groups + group;
-    step = (uint64_t)gridDim.x * r.groups;
+  __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t tokens, uint64_t width) {
+    tpr = r.tpr;
+    stages = r.stages;
+    tid = threadIdx.x % tpr;
+    group = threadIdx.x / tpr;
+    bytes = (uint32_t)(width * sizeof(T));
+    matrix = (uint32_t)r.groups * r.granules * 16;
+    stage = matrix * r.n;
+    slots = stage * stages;
+    in = out = 0;
+    first = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)group * r.granules * 16;
+    const uint64_t row = (uint64_t)blockIdx.x * r.groups + group, rows = (uint64_t)gridDim.x * r.groups;
+    left = row < tokens ? (tokens - row - 1) / rows + 1 : 0;
   }
-  __device__ __forceinline__ char* slot(char* smem, int stage, int m) const {
-    return smem + (uint64_t)((stage * r.n + m) * r.groups + group) * r.granules * 16;
+  __device__ __forceinline__ void open(int m, const void* p, uint64_t ld, uint64_t row, uint64_t rows) {
+    from[m] = (const char*)p + row * ld * sizeof(T);
+    step[m] = rows * ld * sizeof(T);
   }
+  // Bytes from the row's start to vector j, and whether it is there.
+  __device__ __forceinline__ uint32_t offset(int j) const { return (uint32_t)(tid + j * tpr) * S; }
+  __device__ __forceinline__ bool there(int j) const { return offset(j) < bytes; }
+
   // One more row, or an empty step behind the last.
-  __device__ __forceinline__ void fetch(char* smem) {
-    if (row < tokens) {
+  __device__ __forceinline__ void fetch() {
+    if (left) {
+      --left;
 #pragma unroll
-      for (int m = 0; m < 3; ++m) {
-        if (m >= r.n) break;
-        const char* p = base[m] + row * ld[m];
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(smem, slot_in, m));
+      for (int m = 0; m < M; ++m) {
+        if (!from[m]) break;
+        const uint32_t to = first + in + m * matrix;
         if constexpr (SHIFT) {
-          const uint32_t off = (uint32_t)((uintptr_t)p & 15u), g = (off + bytes + 15) / 16;
-          for (uint32_t i = tid; i < g; i += r.tpr) copy16(to + i * 16, p - off + (uint64_t)i * 16);
+          const uint32_t off = (uint32_t)((uintptr_t)from[m] & 15u), end = off + bytes;
+          for (uint32_t i = tid * 16; i < end; i += tpr * 16) copy16(to + i, from[m] - off + i);
         } else {
 #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const uint32_t i = tid + j * r.tpr;
-            if (i * 16 < bytes) copy16(to + i * 16, p + (uint64_t)i * 16);
-          }
+          for (int j = 0; j < NV; ++j)
+            if (there(j)) copy16(to + offset(j), from[m] + offset(j));
         }
+        from[m] += step[m];
       }
-      row += step;
     }
     copies_close();
-    slot_in = slot_in + 1 == r.stages ? 0 : slot_in + 1;
+    in += stage;
+    if (in == slots) in = 0;
   }
-  __device__ __forceinline__ void begin(char* smem) {
-    for (int i = 1; i < r.stages; ++i) fetch(smem);
+  __device__ __forceinline__ void begin() {
+    for (int i = 1; i < stages; ++i) fetch();
   }
-  // Waits for the oldest row, then fetches one into the slot that the row before it left.
-  __device__ __forceinline__ int next(char* smem) {
-    if (r.stages == 2) copies_left<0>();
-    else if (r.stages == 3) copies_left<1>();
+  // Waits for the oldest row, then fetches one into the slot that the row before
+  // it left; where the oldest is.
+  __device__ __forceinline__ uint32_t next() {
+    if (stages == 2) copies_left<0>();
+    else if (stages == 3) copies_left<1>();
     else copies_left<2>();
-    if (SHIFT) group_barrier(group, r.tpr);
-    const int at = slot_out;
-    fetch(smem);
-    slot_out = at + 1 == r.stages ? 0 : at + 1;
+    if (SHIFT) group_barrier(group, tpr);
+    const uint32_t at = first + out;
+    out += stage;
+    if (out == slots) out = 0;
+    fetch();
     return at;
   }
-  // What this thread has of the row, as pairs; zeros beside the row.
-  __device__ __forceinline__ void get(const char* smem, int stage, int m, uint64_t at_row, F2 (&v)[P]) const {
-    const char* s = slot((char*)smem, stage, m);
+  // What this thread has of matrix m's row, which starts at address `row`.
+  __device__ __forceinline__ void get(uint32_t at, int m, const void* row, F2 (&v)[P]) const {
+    at += m * matrix;
     if constexpr (!SHIFT) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t i = (tid + j * r.tpr) * 16;
-        pairs_of<T>(i < bytes ? *reinterpret_cast<const uint4*>(s + i) : make_uint4(0, 0, 0, 0), v + j * (P / NV));
-      }
+      for (int j = 0; j < NV; ++j) pairs_of<T>(ld_shared16(at + (there(j) ? offset(j) : 0)), v + j * (P / NV));
     } else {
-      s += (uint32_t)((uintptr_t)(base[m] + at_row * ld[m]) & 15u);
+      at += (uint32_t)((uintptr_t)row & 15u);
 #pragma unroll
-      for (int j = 0; j < NV; j += 2) {
-        const uint32_t i = (tid + j * r.tpr) * sizeof(T), k = i + r.tpr * sizeof(T);
-        v[j / 2] = f2(i < bytes ? to_f32(*reinterpret_cast<const T*>(s + i)) : 0.f,
-                      k < bytes ? to_f32(*reinterpret_cast<const T*>(s + k)) : 0.f);
-      }
+      for (int j = 0; j < NV; j += 2)
+        v[j / 2] = f2(ld_shared1<T>(at + (there(j) ? offset(j) : 0)), ld_shared1<T>(at + (there(j + 1) ? offset(j + 1) : 0)));
     }
   }
-  // The same into a row of global memory, rounded; `v` becomes what is stored.
-  __device__ __forceinline__ void put(T* to, F2 (&v)[P]) const {
+  // The same into a row of global memory, rounded.
+  __device__ __forceinline__ void put(T* to, const F2 (&v)[P]) const {
     if constexpr (!SHIFT) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t i = (tid + j * r.tpr) * 16;
-        if (i < bytes) *reinterpret_cast<uint4*>((char*)to + i) = packed<T>(v + j * (P / NV));
-      }
+      for (int j = 0; j < NV; ++j)
+        if (there(j)) *reinterpret_cast<uint4*>((char*)to + offset(j)) = packed<T>(v + j * (P / NV));
     } else {
 #pragma unroll
       for (int j = 0; j < NV; j += 2) {
-        const uint32_t i = tid + j * r.tpr, k = i + r.tpr;
         const float2 x = split(v[j / 2]);
-        if (i * sizeof(T) < bytes) to[i] = from_f32<T>(x.x);
-        if (k * sizeof(T) < bytes) to[k] = from_f32<T>(x.y);
+        if (there(j)) to[tid + j * tpr] = from_f32<T>(x.x);
+        if (there(j + 1)) to[tid + (j + 1) * tpr] = from_f32<T>(x.y);
       }
     }
   }
-  // A vector of columns, or `none` where there is no such vector or column.
+  // A vector of columns, `none` where there is no such vector, 0 beside the row.
   template <typename W>
   __device__ __forceinline__ void columns(const void* p, float none, F2 (&v)[P]) const {
     float x[2 * P];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[j * N + i] = none;
-    if (p)
+      for (int i = 0; i < N; ++i) x[j * N + i] = there(j) ? none : 0.f;
+      if (!p || !there(j)) continue;
+      const W* w = (const W*)p + (tid + j * tpr) * N;
+      constexpr int K = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t c = (tid + j * r.tpr) * N;
-        if (c * sizeof(T) >= bytes) break;
-        const W* w = (const W*)p + c;
-        constexpr int M = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
+      for (int q = 0; q < N; q += K) {
+        const Pack<W, K> of = *reinterpret_cast<const Pack<W, K>*>(w + q);
 #pragma unroll
-        for (int q = 0; q < N; q += M) {
-          const Pack<W, M> of = *reinterpret_cast<const Pack<W, M>*>(w + q);
-#pragma unroll
-          for (int i = 0; i < M; ++i) x[j * N + q + i] = to_f32(of.v[i]);
-        }
+        for (int i = 0; i < K; ++i) x[j * N + q + i] = to_f32(of.v[i]);
       }
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = f2(x[2 * i], x[2 * i + 1]);
   }
-  // 1 in place of the row's elements, 0 beside them.
+  // 1 for the row's elements, 0 beside them.
   __device__ __forceinline__ F2 inside(int pair) const {
     const int j = pair * 2 / N;
-    if constexpr (!SHIFT) return f2((tid + j * r.tpr) * 16 < bytes ? 1.f : 0.f);
-    return f2((tid + j * r.tpr) * sizeof(T) < bytes ? 1.f : 0.f, (tid + (j + 1) * r.tpr) * sizeof(T) < bytes ? 1.f : 0.f);
+    if constexpr (!SHIFT) return f2(there(j) ? 1.f : 0.f);
+    return f2(there(j) ? 1.f : 0.f, there(j + 1) ? 1.f : 0.f);
   }
   // The column of a pair's first (0) or second (1) element.
   __device__ __forceinline__ uint32_t column(int pair, int second) const {
     const int e = 2 * pair + second;
-    return (tid + e / N * r.tpr) * N + e % N;
+    return (uint32_t)(tid + e / N * tpr) * N + e % N;
   }
 };
 
@@ -191,18 +210,16 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 tmp[2][kMostThreads / 32];
   constexpr int P = N * NV / 2;
-  Stream<T, N, NV> in(ring, a.tokens, a.width);
-  in.base[0] = (const char*)a.x;
-  in.ld[0] = a.ldx * sizeof(T);
-  in.base[1] = (const char*)a.residual;
-  in.ld[1] = a.ldr * sizeof(T);
-  in.base[2] = nullptr;
-  in.ld[2] = 0;
-  uint64_t row = in.row;
-  const uint64_t step = in.step;
-  const int tid = in.tid, tpr = ring.tpr, warps = tpr >> 5, warp = tid >> 5;
+  Stream<T, N, NV, 2> in(ring, smem, a.tokens, a.width);
+  const int tid = in.tid, tpr = in.tpr, warps = tpr >> 5, warp = tid >> 5;
+  const uint64_t rows = (uint64_t)gridDim.x * ring.groups;
+  uint64_t row = (uint64_t)blockIdx.x * ring.groups + in.group;
+  in.open(0, a.x, a.ldx, row, rows);
+  if (a.residual) in.open(1, a.residual, a.ldr, row, rows);
+  else in.from[1] = nullptr;
+  const bool second = a.residual != nullptr;
   const uint32_t D = (uint32_t)a.width;
-  in.begin(smem);
+  in.begin();
   F2 w[P], b[P];
   in.template columns<W>(a.weight, 1.f, w);
   in.template columns<W>(a.bias, 0.f, b);
@@ -221,13 +238,13 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   const int lane = tid & 31;
   const float of_lane = lane < warps ? (float)part(lane) : 0.f, per_lane = of_lane > 0.f ? __frcp_rn(of_lane) : 0.f;
   int turn = 0;
-  for (; row < a.tokens; row += step) {
-    const int at = in.next(smem);
+  for (; row < a.tokens; row += rows) {
+    const uint32_t at = in.next();
     F2 v[P], sum = f2(0.f);
-    in.get(smem, at, 0, row, v);
-    if (a.residual) {
+    in.get(at, 0, (const T*)a.x + row * a.ldx, v);
+    if (second) {
       F2 q[P];
-      in.get(smem, at, 1, row, q);
+      in.get(at, 1, (const T*)a.residual + row * a.ldr, q);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         v[i] = v[i] + q[i];
@@ -235,12 +252,12 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
       }
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum = sum + v[i];
+    for (int i = 0; i < P; ++i) sum = fma2(in.inside(i), v[i], sum);
     float s = warp_sum(both(sum)), mean = s * per_mine;
     sum = f2(0.f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const F2 d = fma2(in.inside(i), f2(-mean), v[i]);  // 0 beside the row
+      const F2 d = in.inside(i) * (v[i] + f2(-mean));
       sum = fma2(d, d, sum);
     }
     float squares = warp_sum(both(sum));
@@ -344,18 +361,17 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
   __shared__ float2 tmp[2][kMostThreads / 32];
   constexpr int P = N * NV / 2;
-  Stream<T, N, NV> in(ring, a.tokens, a.width);
-  in.base[0] = (const char*)a.x;
-  in.ld[0] = a.ldx * sizeof(T);
-  in.base[1] = (const char*)a.grad_y;
-  in.ld[1] = a.ldg * sizeof(T);
-  in.base[2] = (const char*)a.grad_total;
-  in.ld[2] = a.ldgt * sizeof(T);
-  uint64_t row = in.row;
-  const uint64_t step = in.step;
-  const int tid = in.tid, tpr = ring.tpr, group = in.group, groups = ring.groups;
+  Stream<T, N, NV, 3> in(ring, smem, a.tokens, a.width);
+  const int tpr = in.tpr, group = in.group, groups = ring.groups;
+  const uint64_t rows = (uint64_t)gridDim.x * groups;
+  uint64_t row = (uint64_t)blockIdx.x * groups + group;
+  in.open(0, a.x, a.ldx, row, rows);
+  in.open(1, a.grad_y, a.ldg, row, rows);
+  if (a.grad_total) in.open(2, a.grad_total, a.ldgt, row, rows);
+  else in.from[2] = nullptr;
+  const bool third = a.grad_total != nullptr;
   const uint32_t D = (uint32_t)a.width;
-  in.begin(smem);
+  in.begin();
   const float per = __frcp_rn((float)D);
   F2 w[P], dw[P], db[P];
   in.template columns<W>(a.weight, 1.f, w);
@@ -363,14 +379,15 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   for (int i = 0; i < P; ++i) dw[i] = db[i] = f2(0.f);
   int turn = 0;
   float2 ahead = row < a.tokens ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
-  for (; row < a.tokens; row += step) {
-    const int at = in.next(smem);
+  for (; row < a.tokens; row += rows) {
+    const uint32_t at = in.next();
     const float mean = ahead.x, rstd = ahead.y;
-    if (row + step < a.tokens) ahead = *reinterpret_cast<const float2*>(a.stats + 2 * (row + step));
+    if (row + rows < a.tokens) ahead = *reinterpret_cast<const float2*>(a.stats + 2 * (row + rows));
+    const T *of_x = (const T*)a.x + row * a.ldx, *of_g = (const T*)a.grad_y + row * a.ldg;
     F2 x[P], g[P], sum = f2(0.f), sum_xh = f2(0.f);
-    in.get(smem, at, 0, row, x);
-    in.get(smem, at, 1, row, g);
-    // beside the row, dy is 0: no sum takes part of it
+    in.get(at, 0, of_x, x);
+    in.get(at, 1, of_g, g);
+    // beside the row the weights are 0, and sums of columns that nobody writes
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       x[i] = (x[i] + f2(-mean)) * f2(rstd);
@@ -385,8 +402,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
     turn ^= 1;
     const F2 m = f2(-s.x * per), mx = f2(-s.y * per);
     if constexpr (P > 8) {  // too many registers to hold them while the warps wait
-      in.get(smem, at, 0, row, x);
-      in.get(smem, at, 1, row, g);
+      in.get(at, 0, of_x, x);
+      in.get(at, 1, of_g, g);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         x[i] = (x[i] + f2(-mean)) * f2(rstd);
@@ -395,8 +412,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) x[i] = f2(rstd) * fma2(x[i], mx, g[i] + m);
-    if (a.grad_total) {
-      in.get(smem, at, 2, row, g);
+    if (third) {
+      in.get(at, 2, (const T*)a.grad_total + row * a.ldgt, g);
 #pragma unroll
       for (int i = 0; i < P; ++i) x[i] = x[i] + g[i];
     }
