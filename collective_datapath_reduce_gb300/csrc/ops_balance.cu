@@ -21,10 +21,11 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
   return x;
 }
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
-  return x;
+// Largest value of the warp, NaN the lesser of any two.
+__device__ __forceinline__ float redux_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -43,7 +44,7 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
   return v;
 }
 
-// N neighbouring values in each lane; those past `width` are `none`.
+// N (an even number) neighbouring values in each lane; those past `width` are `none`.
 template <typename T, int N>
 struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Lane {
   T v[N];
@@ -64,75 +65,96 @@ struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Lane {
       for (int i = 0; i < N; ++i) v[i] = e0 + i < width ? p[e0 + i] : from_f32<T>(none);
     }
   }
+  __device__ __forceinline__ void pairs(F2 (&p)[N / 2]) const {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) p[i] = f2(to_f32(v[2 * i]), to_f32(v[2 * i + 1]));
+  }
 };
 template <typename T, int N>
-__device__ __forceinline__ void st_lane(T* p, int width, bool vec, const float (&x)[N]) {
+__device__ __forceinline__ void st_lane(T* p, int width, bool vec, const F2 (&x)[N / 2]) {
   const int e0 = (threadIdx.x & 31) * N;
   constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
+  T v[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 of = split(x[i]);
+    v[2 * i] = from_f32<T>(of.x);
+    v[2 * i + 1] = from_f32<T>(of.y);
+  }
   if (vec) {
     if (e0 >= width) return;
 #pragma unroll
     for (int q = 0; q < N; q += M) {
       Pack<T, M> r;
 #pragma unroll
-      for (int i = 0; i < M; ++i) r.v[i] = from_f32<T>(x[q + i]);
+      for (int i = 0; i < M; ++i) r.v[i] = v[q + i];
       st_pack(p + e0 + q, r);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (e0 + i < width) p[e0 + i] = from_f32<T>(x[i]);
+      if (e0 + i < width) p[e0 + i] = v[i];
   }
 }
 
+// 2^x; results below the smallest normal number are 0.
+__device__ __forceinline__ F2 ex2(F2 x) {
+  float2 s = split(x);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
+  return f2(s.x, s.y);
+}
 // 1 / x, within 1 ulp; of a number past 2^126, 0.
-__device__ __forceinline__ float inverse(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+__device__ __forceinline__ F2 inverse(F2 x) {
+  float2 s = split(x);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
+  return f2(s.x, s.y);
 }
 
-// e^x; results below the smallest normal number are 0.
-__device__ __forceinline__ float exponential(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-
-// A token's logits become its scores as shares of one; `slope` is what a
-// score's derivative has beside them, 1 - sigmoid.  A row of nothing but -inf
-// has shares of 0.  No decision hangs on them, so neither exponentials nor
-// reciprocals need be the nearest numbers.
+// A token's logits become its scores as shares of one, x; `slope` is what a
+// score's derivative has beside them, 1 - sigmoid = exp(-logit) x sigmoid.  A row
+// of nothing but -inf has shares of 0.  No decision hangs on them, so neither
+// exponentials nor reciprocals need be the nearest numbers.
+constexpr float kLog2e = 1.4426950408889634f;
 template <typename T, int N>
-__device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, float (&x)[N], float (&slope)[N]) {
-  float s = 0.f;
+__device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, F2 (&x)[N / 2], F2 (&slope)[N / 2]) {
+  constexpr int P = N / 2;
+  F2 sum = f2(0.f);
+  float s;
+  row.pairs(x);
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float e = exponential(-to_f32(row.v[i]));
-      x[i] = inverse(1.f + e);
-      slope[i] = e < 1.f ? e * x[i] : 1.f - x[i];  // where s is near 1, the difference would be rounding
-      s += x[i];
+    for (int i = 0; i < P; ++i) {
+      // exp(-x) at most 2^127: a sigmoid below 2^-126 is 0, and the slope a number
+      const float2 a = split(x[i] * f2(-kLog2e));
+      const F2 e = ex2(f2(fminf(a.x, 127.f), fminf(a.y, 127.f)));
+      x[i] = inverse(f2(1.f) + e);
+      slope[i] = e * x[i];
+      sum = sum + x[i];
     }
-    s = warp_sum(s) + 1e-20f;
+    s = warp_sum(both(sum)) + 1e-20f;
   } else {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, to_f32(row.v[i]));
-    m = warp_max(m);
+    for (int i = 0; i < P; ++i) {
+      const float2 a = split(x[i]);
+      m = fmaxf(m, fmaxf(a.x, a.y));
+    }
+    m = redux_max(m);
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = exponential(to_f32(row.v[i]) - m);
-      slope[i] = 1.f;
-      s += x[i];
+    for (int i = 0; i < P; ++i) {
+      x[i] = ex2((x[i] + f2(-m)) * f2(kLog2e));
+      slope[i] = f2(1.f);
+      sum = sum + x[i];
     }
-    s = warp_sum(s);
+    s = warp_sum(both(sum));
     if (s == 0.f) s = 1.f;
   }
   s = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] *= s;
+  for (int i = 0; i < P; ++i) x[i] = x[i] * f2(s);
 }
 
 // The loss of picks C, shares P and N tokens: scale x E x sum C P / (sum C x N).
@@ -214,9 +236,10 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
   if (AHEAD && t < a.tokens) next.load(a, t, vec);
   for (int e = threadIdx.x; e < E; e += kThreads) picks[e] = 0;
   __syncthreads();
-  float sum[N];
+  constexpr int P = N / 2;
+  F2 sum[P];
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum[i] = 0.f;
+  for (int i = 0; i < P; ++i) sum[i] = f2(0.f);
   uint32_t counted = 0;
   for (; t < a.tokens; t += step) {
     if constexpr (AHEAD) {
@@ -228,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
     const bool on = now.id >= 0 && now.id < E;
     if (!__any_sync(kAll, on)) continue;  // padding: its logits may be anything
     if (on) atomicAdd(picks + now.id, 1u);
-    float x[N], slope[N];
+    F2 x[P], slope[P];
     shares<T, N>(now.row, a.sigmoid, x, slope);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] += x[i];
+    for (int i = 0; i < P; ++i) sum[i] = sum[i] + x[i];
     ++counted;
   }
   if (lane == 0) tokens_of[warp] = counted;
@@ -241,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int e = lane * N + i;
-        if (e < E) dyn[warp % kRows * E + e] = sum[i] + (first ? dyn[warp % kRows * E + e] : 0.f);
+        const float2 of = split(sum[i / 2]);
+        if (e < E) dyn[warp % kRows * E + e] = (i % 2 ? of.y : of.x) + (first ? dyn[warp % kRows * E + e] : 0.f);
       }
     __syncthreads();
   }
@@ -364,9 +388,13 @@ __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(c
   }
   const float all = all_picks(a.sums, E, tmp) * a.sums[2 * E];
   const float f = all > 0.f ? __fdiv_rn((a.grad_loss ? *a.grad_loss : 1.f) * a.scale * (float)E, all) : 0.f;
-  float c[N];
+  constexpr int P = N / 2;
+  F2 c[P];
 #pragma unroll
-  for (int i = 0; i < N; ++i) c[i] = lane * N + i < E ? f * a.sums[lane * N + i] : 0.f;
+  for (int i = 0; i < P; ++i) {
+    const int e = lane * N + 2 * i;
+    c[i] = f2(f) * f2(e < E ? a.sums[e] : 0.f, e + 1 < E ? a.sums[e + 1] : 0.f);
+  }
   for (; t < a.tokens; t += step) {
     if constexpr (AHEAD) {
       now = next;
@@ -378,32 +406,32 @@ __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(c
     } else {
       now.load(a, t, vec);
     }
-    float x[N], slope[N];
+    F2 x[P], slope[P];
     if (__any_sync(kAll, now.id >= 0 && now.id < E)) {
       shares<T, N>(now.row, a.sigmoid, x, slope);
-      float dot = 0.f;
+      F2 sum = f2(0.f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) dot = __fmaf_rn(x[i], c[i], dot);
-      dot = warp_sum(dot);
+      for (int i = 0; i < P; ++i) sum = fma2(x[i], c[i], sum);
+      const float dot = warp_sum(both(sum));
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = x[i] * (c[i] - dot) * slope[i];
+      for (int i = 0; i < P; ++i) x[i] = x[i] * (c[i] + f2(-dot)) * slope[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = 0.f;
+      for (int i = 0; i < P; ++i) x[i] = f2(0.f);
     }
     if (a.base) {
       if (!AHEAD) base.load((const T*)a.base + t * a.ldb, E, vec, 0.f);
+      base.pairs(slope);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] += to_f32(base.v[i]);
+      for (int i = 0; i < P; ++i) x[i] = x[i] + slope[i];
     }
     st_lane<T, N>((T*)a.grad_logits + t * a.ldg, E, vec, x);
   }
 }
 
-// Experts of a lane: the smallest power of two that covers them with 32 lanes.
+// Experts of a lane: the smallest power of two, 2 at least, that covers them with 32 lanes.
 template <typename F>
 purlin_status with_lanes(int experts, F f) {
-  if (experts <= 32) return f(std::integral_constant<int, 1>());
   if (experts <= 64) return f(std::integral_constant<int, 2>());
   if (experts <= 128) return f(std::integral_constant<int, 4>());
   if (experts <= 256) return f(std::integral_constant<int, 8>());

@@ -19,9 +19,7 @@ namespace pl {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMostCluster = 8;    // CTAs of a token
-constexpr int kHeld = PURLIN_MAX_PICKS / kThreads;  // picks of a thread
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -88,38 +86,45 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// A thread's picks of a token: where each stands in the range (-1: elsewhere, -2: no
-// pick), the teacher's logit and the student's.
-template <typename T>
+// A thread's picks of a token, HELD of them, THREADS apart: the teacher's logits, and
+// where each stands in the range (kElsewhere, or kNone for no pick).
+constexpr int64_t kElsewhere = -1, kNone = -2;
+template <int THREADS, int HELD>
 struct Picks {
-  int64_t at[kHeld];
-  float t[kHeld], z[kHeld];
+  int64_t at[HELD];
+  float t[HELD];
 
-  __device__ __forceinline__ void load(const DistilArgs& a, uint64_t token, const T* row) {
+  __device__ __forceinline__ void load(const DistilArgs& a, uint64_t token) {
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const int k = threadIdx.x + j * kThreads;
-      at[j] = -2;
+    for (int j = 0; j < HELD; ++j) {
+      const int k = threadIdx.x + j * THREADS;
+      at[j] = -1;
       t[j] = -INFINITY;
-      z[j] = 0.f;
       if (k >= a.picks) continue;
       const uint64_t i = token * a.picks + k;
-      const int64_t id = a.wide_ids ? ((const int64_t*)a.ids)[i] : ((const int32_t*)a.ids)[i];
-      if (id < 0 || id >= a.vocabulary) continue;
+      at[j] = a.wide_ids ? ((const int64_t*)a.ids)[i] : ((const int32_t*)a.ids)[i];
       t[j] = a.teacher_bf16 ? to_f32(((const bf16*)a.teacher)[i]) : ((const float*)a.teacher)[i];
-      at[j] = id >= a.first && (uint64_t)(id - a.first) < a.width ? id - a.first : -1;
-      if (at[j] >= 0) z[j] = to_f32(row[at[j]]);
+    }
+  }
+  // Ids become places.  Apart from the loads, so that these are under way meanwhile.
+  __device__ __forceinline__ void place(const DistilArgs& a) {
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const int64_t id = at[j];
+      const bool pick = id >= 0 && id < a.vocabulary;
+      if (!pick) t[j] = -INFINITY;
+      at[j] = !pick ? kNone : id >= a.first && (uint64_t)(id - a.first) < a.width ? id - a.first : kElsewhere;
     }
   }
   __device__ __forceinline__ float best() const {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) m = fmaxf(m, t[j]);
+    for (int j = 0; j < HELD; ++j) m = fmaxf(m, t[j]);
     return m;
   }
   // exp of the teacher's logit against the best one, over the temperature
   __device__ __forceinline__ float weight(int j, float best, float tau) const {
-    return at[j] == -2 ? 0.f : expf(__fdiv_rn(t[j] - at_least(best), tau));
+    return at[j] == kNone ? 0.f : expf(__fdiv_rn(t[j] - at_least(best), tau));
   }
 };
 
@@ -129,13 +134,13 @@ struct Picks {
 __device__ __forceinline__ uint64_t share(uint64_t nv, uint32_t rank, uint32_t split) { return nv * rank / split; }
 
 // One token, by a cluster of CTAs that share its row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant__ DistilArgs a, int split) {
+template <typename T, int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS) distil_kernel(const __grid_constant__ DistilArgs a, int split) {
   op_wait();
-  constexpr int V = V16<T>;
-  __shared__ float2 of_warp[kWarps], of_cta[kMostCluster];
-  __shared__ float best_of[kWarps];
-  __shared__ float sum_of[3][kWarps];
+  constexpr int V = V16<T>, WARPS = THREADS / 32;
+  __shared__ float2 of_warp[WARPS], of_cta[kMostCluster];
+  __shared__ float best_of[WARPS];
+  __shared__ float sum_of[3][WARPS];
   const uint64_t token = blockIdx.x / split;
   const uint32_t rank = blockIdx.x % split, tid = threadIdx.x;
   if (split > 1) cluster_arrive();  // that this CTA runs: others may write to its memory
@@ -145,15 +150,15 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
   const uint64_t v0 = share(cut.nv, rank, split), v1 = share(cut.nv, rank + 1, split);
   const T* body = row + cut.head;
 
-  Picks<T> picks;
-  if (rank == 0) picks.load(a, token, row);
+  Picks<THREADS, HELD> picks;
+  if (rank == 0) picks.load(a, token);
   float m = -INFINITY;
   F2 sum = f2(0.f);
   auto step = [&](auto number, uint64_t v) {
     constexpr int F = decltype(number)::value, P = V / 2;
     uint4 x[F];
 #pragma unroll
-    for (int u = 0; u < F; ++u) x[u] = ld16_if(body + (v + u * kThreads) * V, true);
+    for (int u = 0; u < F; ++u) x[u] = ld16_if(body + (v + u * THREADS) * V, true);
 #pragma unroll
     for (int u = 0; u < F; ++u) asm volatile("" : "+r"(x[u].x), "+r"(x[u].y), "+r"(x[u].z), "+r"(x[u].w));
     const float top = largest<T, F>(x, m), n = at_least(top);
@@ -168,13 +173,19 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
     }
   };
   uint64_t v = v0 + tid;
-  for (; v + 3 * kThreads < v1; v += 4 * kThreads) step(std::integral_constant<int, 4>(), v);
-  for (; v < v1; v += kThreads) step(std::integral_constant<int, 1>(), v);
+  for (; v + 3 * THREADS < v1; v += 4 * THREADS) step(std::integral_constant<int, 4>(), v);
+  for (; v < v1; v += THREADS) step(std::integral_constant<int, 1>(), v);
   float s = both(sum);
   if (rank == 0 && tid < cut.beside) {
     const float x = to_f32(row[cut.at<V>(tid)]);
     s = __fmaf_rn(s, ex2((m - at_least(fmaxf(m, x))) * c), ex2((x - at_least(fmaxf(m, x))) * c));
     m = fmaxf(m, x);
+  }
+  float z[HELD];
+  if (rank == 0) {
+    picks.place(a);
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) z[j] = picks.at[j] >= 0 ? to_f32(row[picks.at[j]]) : 0.f;
   }
   float2 ms = warp_all(make_float2(m, s), [c](float2 p, float2 q) { return joined(p, q, c); });
   float best = rank == 0 ? warp_max(picks.best()) : 0.f;
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
   __syncthreads();
   ms = of_warp[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) ms = joined(ms, of_warp[w], c);
+  for (int w = 1; w < WARPS; ++w) ms = joined(ms, of_warp[w], c);
   if (split > 1) {
     cluster_wait();
     if (tid == 0) st_cluster(of_cta + rank, 0, ms);
@@ -199,17 +210,17 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
   }
   best = best_of[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) best = fmaxf(best, best_of[w]);
+  for (int w = 1; w < WARPS; ++w) best = fmaxf(best, best_of[w]);
 
   // the sums over the picks: e, and of those in the range e (log-ratio) and e
   float all = 0.f, term = 0.f, mass = 0.f;
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
+  for (int j = 0; j < HELD; ++j) {
     const float e = picks.weight(j, best, a.temperature);
     all += e;
     if (picks.at[j] < 0 || e == 0.f) continue;
     const float of_t = __fdiv_rn(picks.t[j] - at_least(best), a.temperature);
-    const float of_z = __fdiv_rn(picks.z[j] - at_least(ms.x), a.temperature);
+    const float of_z = __fdiv_rn(z[j] - at_least(ms.x), a.temperature);
     term = __fmaf_rn(e, of_t - of_z, term);
     mass += e;
   }
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
   if (tid) return;
   all = term = mass = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     all += sum_of[0][w];
     term += sum_of[1][w];
     mass += sum_of[2][w];
@@ -245,9 +256,10 @@ __global__ void __launch_bounds__(kThreads) distil_kernel(const __grid_constant_
 }
 
 // The parts of all ranges of a token, one thread for a token.
-__global__ void __launch_bounds__(kThreads) distil_join_kernel(const __grid_constant__ DistilArgs a) {
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) distil_join_kernel(const __grid_constant__ DistilArgs a) {
   op_wait();
-  const uint64_t token = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  const uint64_t token = (uint64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   if (token >= a.tokens) return;
   const float c = a.log2e_per_temperature;
   float2 ms = make_float2(-INFINITY, 0.f);
@@ -270,13 +282,13 @@ __global__ void __launch_bounds__(kThreads) distil_join_kernel(const __grid_cons
 // dz_j = G (Q p_j - the sum of q_k over the picks k of j), G = dL scale / temperature.
 // The row is written without the picks first, then the picks' places again, by
 // the CTA that wrote them, each by the first pick of its word.
-template <typename T, bool SHIFT>
-__global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_constant__ DistilArgs a, int split) {
+template <typename T, bool SHIFT, int THREADS, int HELD>
+__global__ void __launch_bounds__(THREADS) distil_grad_kernel(const __grid_constant__ DistilArgs a, int split) {
   op_wait();
-  constexpr int V = V16<T>;
-  __shared__ float best_of[kWarps], sum_of[kWarps];
-  __shared__ int64_t id_of[PURLIN_MAX_PICKS];
-  __shared__ float q_of[PURLIN_MAX_PICKS];
+  constexpr int V = V16<T>, WARPS = THREADS / 32;
+  __shared__ float best_of[WARPS], sum_of[WARPS];
+  __shared__ int64_t id_of[THREADS * HELD];
+  __shared__ float q_of[THREADS * HELD];
   const uint64_t token = blockIdx.x / split;
   const uint32_t rank = blockIdx.x % split, tid = threadIdx.x;
   const T* row = (const T*)a.logits + token * a.ld;
@@ -285,21 +297,26 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
   const Cut cut = cut_of<T, true>(out, a.width);
   const uint64_t v0 = share(cut.nv, rank, split), v1 = share(cut.nv, rank + 1, split);
 
-  Picks<T> picks;
-  picks.load(a, token, row);
+  Picks<THREADS, HELD> picks;
+  picks.load(a, token);
+  const float of_max = a.stats[2 * token], total = a.stats[2 * token + 1], of_loss = a.grad_loss[token];
+  picks.place(a);
+  float z[HELD];
+#pragma unroll
+  for (int j = 0; j < HELD; ++j) z[j] = picks.at[j] >= 0 ? to_f32(row[picks.at[j]]) : 0.f;
   float best = warp_max(picks.best());
   if ((tid & 31) == 0) best_of[tid >> 5] = best;
   __syncthreads();
   best = best_of[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) best = fmaxf(best, best_of[w]);
-  float e[kHeld], all = 0.f;
+  for (int w = 1; w < WARPS; ++w) best = fmaxf(best, best_of[w]);
+  float e[HELD], all = 0.f;
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
+  for (int j = 0; j < HELD; ++j) {
     all += e[j] = picks.weight(j, best, a.temperature);
-    if (tid + j * kThreads < a.picks) {
-      id_of[tid + j * kThreads] = picks.at[j];
-      q_of[tid + j * kThreads] = e[j];
+    if (tid + j * THREADS < a.picks) {
+      id_of[tid + j * THREADS] = picks.at[j];
+      q_of[tid + j * THREADS] = e[j];
     }
   }
   all = warp_sum(all);
@@ -307,10 +324,10 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
   __syncthreads();  // the picks' logits are read before any gradient is written in their place
   all = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += sum_of[w];
-  const float m = at_least(a.stats[2 * token]), total = a.stats[2 * token + 1];
+  for (int w = 0; w < WARPS; ++w) all += sum_of[w];
+  const float m = at_least(of_max);
   const bool none = all == 0.f || total == 0.f;  // no picks, or nothing to take them from
-  const float G = none ? 0.f : __fdiv_rn(a.grad_loss[token] * a.scale, a.temperature);
+  const float G = none ? 0.f : __fdiv_rn(of_loss * a.scale, a.temperature);
   const float f = none ? 0.f : __fdiv_rn(G, total) * __fdiv_rn(all, all);  // Q is 1, or NaN
   auto grad = [&](float z) { return none ? 0.f : f * ex2((z - m) * c); };
 
@@ -321,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
     uint4 x[F];
 #pragma unroll
     for (int u = 0; u < F; ++u) {
-      const T* p = from + (v + u * kThreads) * V;
+      const T* p = from + (v + u * THREADS) * V;
       if constexpr (SHIFT) {
         const Pack<T, V> r = ld_row_if<T, true>(p, true);
         memcpy(&x[u], &r, 16);
@@ -337,20 +354,20 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
       pairs_of<T>(x[u], p);
 #pragma unroll
       for (int i = 0; i < P; ++i) p[i] = none ? f2(0.f) : f2(f) * ex2((p[i] + f2(-m)) * f2(c));
-      *reinterpret_cast<uint4*>(to + (v + u * kThreads) * V) = packed<T>(p);
+      *reinterpret_cast<uint4*>(to + (v + u * THREADS) * V) = packed<T>(p);
     }
   };
   uint64_t v = v0 + tid;
-  for (; v + 3 * kThreads < v1; v += 4 * kThreads) step(std::integral_constant<int, 4>(), v);
-  for (; v < v1; v += kThreads) step(std::integral_constant<int, 1>(), v);
+  for (; v + 3 * THREADS < v1; v += 4 * THREADS) step(std::integral_constant<int, 4>(), v);
+  for (; v < v1; v += THREADS) step(std::integral_constant<int, 1>(), v);
   if (rank == 0 && tid < cut.beside) {
     const uint64_t i = cut.at<V>(tid);
     out[i] = from_f32<T>(grad(to_f32(row[i])));
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int k = tid + j * kThreads;
+  for (int j = 0; j < HELD; ++j) {
+    const int k = tid + j * THREADS;
     if (k >= a.picks || picks.at[j] < 0 || none) continue;
     const uint64_t i = (uint64_t)picks.at[j];
     const bool beside = i < cut.head || i >= cut.head + cut.nv * V;
@@ -363,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) distil_grad_kernel(const __grid_cons
         first = first && o > k;
         q += q_of[o];
       }
-    if (first) out[i] = from_f32<T>(__fmaf_rn(-G, __fdiv_rn(q, all), grad(picks.z[j])));
+    if (first) out[i] = from_f32<T>(__fmaf_rn(-G, __fdiv_rn(q, all), grad(z[j])));
   }
 }
 
@@ -374,16 +391,36 @@ int split_of(uint64_t tokens, uint64_t width, uint64_t want) {
   return n;
 }
 
+// f(threads of a CTA, picks of a thread).  Fewer threads for a row mean that more
+// rows are under way, of which each spends some time on its picks and sums: 8191 rows
+// of 1000 / 8192 / 32768 bf16 words take 30 / 37 / 86 us with 256 threads each, 16 / 26 / 81 with
+// 128, 12 / 24 / 82 with 64 (4096 x 131072: 156, 150, 154); the gradient 35 / 61 / 161, 17 / 45 / 162,
+// 16 / 48 / 171 (2047 x 65537 binary32: 172, 187, 184, and 164 with 512).
+struct RowSizes {
+  uint64_t of64, of128;  // bytes of a row, at most
+};
+constexpr RowSizes kForward = {32 * 1024, UINT64_MAX}, kBackward = {8 * 1024, 64 * 1024};
+template <typename F>
+purlin_status with_threads(RowSizes most, uint64_t bytes, int picks, F f) {
+  using std::integral_constant;
+  if (bytes <= most.of64 && picks <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+  if (bytes <= most.of128 && picks <= 128) return f(integral_constant<int, 128>(), integral_constant<int, 1>());
+  return f(integral_constant<int, 512>(), integral_constant<int, PURLIN_MAX_PICKS / 512>());
+}
+
 }  // namespace
 
 purlin_status launch_distil(const DistilArgs& a, int dtype, cudaStream_t s) {
   const int split = split_of(a.tokens, a.width, 4 * 152);
-  if (dtype == PL_F32) return op_launch_cluster(split, distil_kernel<float>, a.tokens * split, kThreads, 0, s, a, split);
-  return op_launch_cluster(split, distil_kernel<bf16>, a.tokens * split, kThreads, 0, s, a, split);
+  return with_threads(kForward, a.width * (dtype == PL_F32 ? 4 : 2), a.picks, [&](auto threads, auto held) {
+    constexpr int N = decltype(threads)::value, H = decltype(held)::value;
+    if (dtype == PL_F32) return op_launch_cluster(split, distil_kernel<float, N, H>, a.tokens * split, N, 0, s, a, split);
+    return op_launch_cluster(split, distil_kernel<bf16, N, H>, a.tokens * split, N, 0, s, a, split);
+  });
 }
 
 purlin_status launch_distil_join(const DistilArgs& a, cudaStream_t s) {
-  return op_launch(distil_join_kernel, (a.tokens + kThreads - 1) / kThreads, kThreads, 0, s, a);
+  return op_launch(distil_join_kernel, (a.tokens + kJoinThreads - 1) / kJoinThreads, kJoinThreads, 0, s, a);
 }
 
 purlin_status launch_distil_grad(const DistilArgs& a, int dtype, cudaStream_t s) {
@@ -391,9 +428,12 @@ purlin_status launch_distil_grad(const DistilArgs& a, int dtype, cudaStream_t s)
   const uint64_t es = dtype == PL_F32 ? 4 : 2;
   // rows of both matrices at the same distance from a 16-byte boundary, all of them
   const bool even = (((uintptr_t)a.logits ^ (uintptr_t)a.grad_logits) & 15) == 0 && ((a.ld - a.ldg) * es & 15) == 0;
-  auto go = [&](auto fn) { return op_launch(fn, a.tokens * split, kThreads, 0, s, a, split); };
-  if (dtype == PL_F32) return even ? go(distil_grad_kernel<float, false>) : go(distil_grad_kernel<float, true>);
-  return even ? go(distil_grad_kernel<bf16, false>) : go(distil_grad_kernel<bf16, true>);
+  return with_threads(kBackward, a.width * es, a.picks, [&](auto threads, auto held) {
+    constexpr int N = decltype(threads)::value, H = decltype(held)::value;
+    auto go = [&](auto fn) { return op_launch(fn, a.tokens * split, N, 0, s, a, split); };
+    if (dtype == PL_F32) return even ? go(distil_grad_kernel<float, false, N, H>) : go(distil_grad_kernel<float, true, N, H>);
+    return even ? go(distil_grad_kernel<bf16, false, N, H>) : go(distil_grad_kernel<bf16, true, N, H>);
+  });
 }
 
 }  // namespace pl

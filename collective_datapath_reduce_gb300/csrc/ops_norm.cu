@@ -68,13 +68,13 @@ template <typename T, int N, int NV, int M>
 struct Stream {
   static constexpr bool SHIFT = N == 1;
   static constexpr int P = N * NV / 2, S = N * (int)sizeof(T);  // S: bytes of a vector
-  const char* from[M];   // the next row to fetch, of each matrix
+  const char* from[M];   // the next row to fetch, of each matrix; aligned: this thread's first vector
   uint64_t step[M];      // bytes to the one behind it
   uint64_t left;         // rows to fetch
   uint32_t bytes, matrix, stage, slots, in, out, first;  // of shared memory
   int tid, group, tpr, stages;
 
-  __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t tokens, uint64_t width) {
+  __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t width) {
     tpr = r.tpr;
     stages = r.stages;
     tid = threadIdx.x % tpr;
@@ -85,11 +85,14 @@ struct Stream {
     slots = stage * stages;
     in = out = 0;
     first = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)group * r.granules * 16;
-    const uint64_t row = (uint64_t)blockIdx.x * r.groups + group, rows = (uint64_t)gridDim.x * r.groups;
+    left = 0;
+  }
+  // Rows `row`, row + rows, .. of `tokens`.
+  __device__ __forceinline__ void take(uint64_t row, uint64_t rows, uint64_t tokens) {
     left = row < tokens ? (tokens - row - 1) / rows + 1 : 0;
   }
   __device__ __forceinline__ void open(int m, const void* p, uint64_t ld, uint64_t row, uint64_t rows) {
-    from[m] = (const char*)p + row * ld * sizeof(T);
+    from[m] = (const char*)p + row * ld * sizeof(T) + (SHIFT ? 0 : tid * 16);
     step[m] = rows * ld * sizeof(T);
   }
   // Bytes from the row's start to vector j, and whether it is there.
@@ -110,7 +113,7 @@ struct Stream {
         } else {
 #pragma unroll
           for (int j = 0; j < NV; ++j)
-            if (there(j)) copy16(to + offset(j), from[m] + offset(j));
+            if (there(j)) copy16(to + offset(j), from[m] + j * tpr * 16);
         }
         from[m] += step[m];
       }
@@ -127,7 +130,8 @@ struct Stream {
   __device__ __forceinline__ uint32_t next() {
     if (stages == 2) copies_left<0>();
     else if (stages == 3) copies_left<1>();
-    else copies_left<2>();
+    else if (stages == 4) copies_left<2>();
+    else copies_left<3>();
     if (SHIFT) group_barrier(group, tpr);
     const uint32_t at = first + out;
     out += stage;
@@ -148,18 +152,18 @@ struct Stream {
         v[j / 2] = f2(ld_shared1<T>(at + (there(j) ? offset(j) : 0)), ld_shared1<T>(at + (there(j + 1) ? offset(j + 1) : 0)));
     }
   }
-  // The same into a row of global memory, rounded.
+  // The same into global memory, rounded; `to`: this thread's first vector.
   __device__ __forceinline__ void put(T* to, const F2 (&v)[P]) const {
     if constexpr (!SHIFT) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (there(j)) *reinterpret_cast<uint4*>((char*)to + offset(j)) = packed<T>(v + j * (P / NV));
+        if (there(j)) *reinterpret_cast<uint4*>((char*)to + j * tpr * 16) = packed<T>(v + j * (P / NV));
     } else {
 #pragma unroll
       for (int j = 0; j < NV; j += 2) {
         const float2 x = split(v[j / 2]);
-        if (there(j)) to[tid + j * tpr] = from_f32<T>(x.x);
-        if (there(j + 1)) to[tid + (j + 1) * tpr] = from_f32<T>(x.y);
+        if (there(j)) to[j * tpr] = from_f32<T>(x.x);
+        if (there(j + 1)) to[(j + 1) * tpr] = from_f32<T>(x.y);
       }
     }
   }
@@ -210,10 +214,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 tmp[2][kMostThreads / 32];
   constexpr int P = N * NV / 2;
-  Stream<T, N, NV, 2> in(ring, smem, a.tokens, a.width);
+  Stream<T, N, NV, 2> in(ring, smem, a.width);
   const int tid = in.tid, tpr = in.tpr, warps = tpr >> 5, warp = tid >> 5;
   const uint64_t rows = (uint64_t)gridDim.x * ring.groups;
   uint64_t row = (uint64_t)blockIdx.x * ring.groups + in.group;
+  in.take(row, rows, a.tokens);
   in.open(0, a.x, a.ldx, row, rows);
   if (a.residual) in.open(1, a.residual, a.ldr, row, rows);
   else in.from[1] = nullptr;
@@ -238,6 +243,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   const int lane = tid & 31;
   const float of_lane = lane < warps ? (float)part(lane) : 0.f, per_lane = of_lane > 0.f ? __frcp_rn(of_lane) : 0.f;
   int turn = 0;
+  T* y = (T*)a.y + row * a.ldy + tid * N;
+  T* total = a.total ? (T*)a.total + row * a.ldt + tid * N : nullptr;
   for (; row < a.tokens; row += rows) {
     const uint32_t at = in.next();
     F2 v[P], sum = f2(0.f);
@@ -273,10 +280,14 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
     }
     const float rstd = inverse(squares * per, a.eps);
     if (a.stats && tid == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
-    if (a.total) in.put((T*)a.total + row * a.ldt, v);
+    if (total) {
+      in.put(total, v);
+      total += rows * a.ldt;
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = fma2((v[i] + f2(-mean)) * f2(rstd), w[i], b[i]);
-    in.put((T*)a.y + row * a.ldy, v);
+    in.put(y, v);
+    y += rows * a.ldy;
   }
 }
 
@@ -332,26 +343,23 @@ __global__ void __launch_bounds__(kMostThreads) norm_wide_kernel(const __grid_co
 // columns' sums over the rows that pass through it; a second kernel adds the
 // CTAs' sums, in order.
 
-// Sums of two values over a row's threads; `tmp`: a place for each warp, of two rows that are used in turn.
-__device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float2* tmp) {
-  // the two halves of the warp take one value each
-  const bool upper = threadIdx.x & 16;
-  const float other = __shfl_xor_sync(kAll, upper ? x.x : x.y, 16);
-  float v = (upper ? x.y : x.x) + other;
+// Sums of two values over a row's threads; `tmp`: two words for each warp, of two
+// rows that are used in turn.  The halves of a warp take one value each.
+__device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
   for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-  x.x = __shfl_sync(kAll, v, 0);
-  x.y = __shfl_sync(kAll, v, 16);
-  if (tpr == 32) return x;
-  const int warp = (threadIdx.x >> 5) - group * (tpr >> 5);
-  if ((threadIdx.x & 31) == 0) tmp[warp] = x;
-  group_barrier(group, tpr);
-  x = make_float2(0.f, 0.f);
-  for (int w = 0; w < tpr >> 5; ++w) {
-    x.x += tmp[w].x;
-    x.y += tmp[w].y;
+  return v;
+}
+__device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float* tmp) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, warps = tpr >> 5;
+  const float other = __shfl_xor_sync(kAll, half ? x.x : x.y, 16);
+  float v = half_sum((half ? x.y : x.x) + other);
+  if (warps > 1) {
+    if ((lane & 15) == 0) tmp[2 * ((threadIdx.x >> 5) - group * warps) + half] = v;
+    group_barrier(group, tpr);
+    v = half_sum((lane & 15) < warps ? tmp[2 * (lane & 15) + half] : 0.f);
   }
-  return x;
+  return make_float2(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 16));
 }
 
 template <typename T, typename W, int N, int NV>
@@ -359,12 +367,16 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
                                                                  const __grid_constant__ Ring ring) {
   op_wait();
   extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
-  __shared__ float2 tmp[2][kMostThreads / 32];
+  __shared__ float tmp[2][kMostThreads / 16];
   constexpr int P = N * NV / 2;
-  Stream<T, N, NV, 3> in(ring, smem, a.tokens, a.width);
+  Stream<T, N, NV, 3> in(ring, smem, a.width);
   const int tpr = in.tpr, group = in.group, groups = ring.groups;
   const uint64_t rows = (uint64_t)gridDim.x * groups;
-  uint64_t row = (uint64_t)blockIdx.x * groups + group;
+  // groups of one number take neighbouring rows, so that the last rows, fewer than
+  // groups, fall on all CTAs (20011 x 520 binary32: 25.5 us, 26.0 with neighbours to a
+  // CTA; in the forward pass that is the better way, 102 us and 105)
+  uint64_t row = (uint64_t)group * gridDim.x + blockIdx.x;
+  in.take(row, rows, a.tokens);
   in.open(0, a.x, a.ldx, row, rows);
   in.open(1, a.grad_y, a.ldg, row, rows);
   if (a.grad_total) in.open(2, a.grad_total, a.ldgt, row, rows);
@@ -378,6 +390,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < P; ++i) dw[i] = db[i] = f2(0.f);
   int turn = 0;
+  T* dx = (T*)a.y + row * a.ldy + in.tid * N;
   float2 ahead = row < a.tokens ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
   for (; row < a.tokens; row += rows) {
     const uint32_t at = in.next();
@@ -398,7 +411,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
       sum_xh = fma2(g[i], x[i], sum_xh);
     }
     float2 s = make_float2(both(sum), both(sum_xh));
-    s = group_sum(s, tpr, group, tmp[turn] + group * (tpr >> 5));
+    s = group_sum(s, tpr, group, tmp[turn] + group * (tpr >> 4));
     turn ^= 1;
     const F2 m = f2(-s.x * per), mx = f2(-s.y * per);
     if constexpr (P > 8) {  // too many registers to hold them while the warps wait
@@ -417,7 +430,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
 #pragma unroll
       for (int i = 0; i < P; ++i) x[i] = x[i] + g[i];
     }
-    in.put((T*)a.y + row * a.ldy, x);
+    in.put(dx, x);
+    dx += rows * a.ldy;
   }
   if (!a.parts) return;
   copies_left<0>();
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
 template <typename T, typename W>
 __global__ void __launch_bounds__(kMostThreads) norm_grad_wide_kernel(const __grid_constant__ NormArgs a) {
   op_wait();
-  __shared__ float2 tmp[kMostThreads / 32];
+  __shared__ float tmp[kMostThreads / 16];
   const uint64_t row = blockIdx.x;
   const T* x = (const T*)a.x + row * a.ldx;
   const T* dy = (const T*)a.grad_y + row * a.ldg;
@@ -488,26 +502,32 @@ __global__ void __launch_bounds__(kColumns) norm_columns_kernel(const __grid_con
   a.parts[(part * 2 + 1) * a.width + c] = db;
 }
 
-// The CTAs' sums of 32 columns, added in order by eight warps that share the CTAs.
+// The CTAs' sums of 32 columns, added in order by eight warps that share the CTAs,
+// a warp's loads all at once.
+constexpr int kJoinWarps = 8, kJoinLoads = (kSms + kJoinWarps - 1) / kJoinWarps;
 template <typename W>
-__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormArgs a, int parts) {
+__global__ void __launch_bounds__(kJoinWarps * 32) norm_join_kernel(const __grid_constant__ NormArgs a, int parts) {
   op_wait();
-  __shared__ float tmp[8][32];
+  __shared__ float tmp[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int which = blockIdx.x & 1;
+  const int which = blockIdx.x & 1;  // the weight's or the bias's
   const uint64_t c = (uint64_t)(blockIdx.x >> 1) * 32 + lane;
   W* out = (W*)(which ? a.grad_bias : a.grad_weight);
   if (!out) return;
-  float v = 0.f;
-  if (c < a.width)
-#pragma unroll 4
-    for (int p = warp; p < parts; p += 8) v += a.parts[((uint64_t)p * 2 + which) * a.width + c];
+  float x[kJoinLoads], v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinLoads; ++i) {
+    const int p = warp + i * kJoinWarps;
+    x[i] = ld1_if(a.parts + ((uint64_t)p * 2 + which) * a.width + c, p < parts && c < a.width);
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinLoads; ++i) v += x[i];
   tmp[warp][lane] = v;
   __syncthreads();
   if (warp || c >= a.width) return;
   v = tmp[0][lane];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) v += tmp[w][lane];
+  for (int w = 1; w < kJoinWarps; ++w) v += tmp[w][lane];
   out[c] = from_f32<W>(v);
 }
 
@@ -556,7 +576,7 @@ purlin_status with_shape(uint64_t width, F f) {
 
 constexpr uint32_t kSmem = 200 * 1024;
 
-// The ring of a launch, with as many stages (2 to 4) as fit.
+// The ring of a launch.
 template <typename T, int N, int NV>
 Ring ring_of(uint64_t width, int tpr, int n) {
   Ring r = {};
@@ -564,7 +584,11 @@ Ring ring_of(uint64_t width, int tpr, int n) {
   r.tpr = tpr;
   r.groups = kMostThreads / tpr;
   r.granules = (uint32_t)(width * sizeof(T) + (N == 1 ? 30 : 0)) / 16;
-  for (r.stages = 4; r.stages > 2 && r.smem() > kSmem; --r.stages) {
+  // as many rows under way as make 64 KiB, four at most (of 40 KiB, 16384 x 5120: 104 us
+  // with one, 102 with two; of 65 KiB, 20011 x 520 binary32: 24.3 us with one, 25.5 with two)
+  r.stages = 1;
+  const uint32_t row = r.smem();
+  for (r.stages = 2; r.stages < 5 && (uint32_t)(r.stages - 1) * row < 64 * 1024; ++r.stages) {
   }
   // rows of 8192 binary32 values of three matrices still fit twice
   while (r.groups > 1 && r.smem() > kSmem) --r.groups;
@@ -615,7 +639,7 @@ purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
     st = vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
   }
   if (st || !sums) return st;
-  return op_launch(norm_join_kernel<W>, (a.width + 31) / 32 * 2, 256, 0, s, a, parts);
+  return op_launch(norm_join_kernel<W>, (a.width + 31) / 32 * 2, kJoinWarps * 32, 0, s, a, parts);
 }
 
 }  // namespace
