@@ -93,8 +93,13 @@ class ExpertStep:
 
     def forward(self, tokens):
         """(outputs of every rank, what the backward pass needs)."""
-        s, h, local = self.shape, self.handle, self.shape.experts // self.shape.world
         everyone, x = self._embed(tokens)
+        y, saved = self._layer(x)
+        return y, dict(saved, everyone=everyone)
+
+    def _layer(self, x):
+        """The expert layer on every rank's rows: (outputs, what its backward pass needs)."""
+        s, h, local = self.shape, self.handle, self.shape.experts // self.shape.world
         ids, weights, places, logits, offsets, rows = [], [], [], [], [], []
         for r in range(s.world):
             logits.append((x[r].float() @ self.router.float().t()).contiguous())
@@ -123,10 +128,10 @@ class ExpertStep:
             back.append(torch.empty_like(out))
             purlin.combine_rows(out, groups[d], None, back[d], h)
         returned = self._exchange(back, [list(c) for c in zip(*counts)])
-        y = [self._new(s.tokens, s.width) for _ in tokens]
+        y = [self._new(s.tokens, s.width) for _ in x]
         for r in range(s.world):
             purlin.combine_rows(returned[r], places[r], weights[r], y[r], h)
-        return y, dict(everyone=everyone, x=x, logits=logits, ids=ids, weights=weights, places=places, counts=counts,
+        return y, dict(x=x, logits=logits, ids=ids, weights=weights, places=places, counts=counts,
                        per_expert=per_expert, groups=groups, regrouped=regrouped, returned=returned)
 
     def _experts(self, d, rows, sizes):
@@ -147,6 +152,11 @@ class ExpertStep:
 
     def backward(self, grad_y, f):
         """Gradients in the order of parameters(), given the outputs' and forward's second result."""
+        grad_x, *rest = self._layer_grad(grad_y, f)
+        return [*self._embed_grad(grad_x, f["everyone"]), *rest]
+
+    def _layer_grad(self, grad_y, f):
+        """The expert layer's backward pass: gradients of every rank's rows, then those of its parameters."""
         s, h, local = self.shape, self.handle, self.shape.experts // self.shape.world
         W = range(s.world)
         grad_rows = [torch.empty_like(f["returned"][r]) for r in W]
@@ -170,18 +180,29 @@ class ExpertStep:
         for r in W:
             grad_x.append(self._new(s.tokens, s.width))
             purlin.combine_rows(returned[r], f["places"][r], None, grad_x[r], h)
-            grad_logits = torch.empty_like(f["logits"][r])
-            purlin.route_experts_grad(f["logits"][r], f["ids"][r], grad_weights[r], grad_logits, h)
+            grad_logits = self._route_grad(f, r, grad_weights[r])
             grad_x[r] += (grad_logits @ self.router.float()).to(self.dtype)
             grad_router.append((grad_logits.t() @ f["x"][r].float()).to(self.dtype).contiguous())
         purlin.all_reduce(grad_router, grad_router, h)
-        everyone = [self._new(s.world * s.tokens, s.width) for _ in W]
+        return grad_x, grad_router[0], *grad_up, *grad_down
+
+    def _route_grad(self, f, r, grad_weights):
+        """Gradient of rank r's router logits."""
+        grad = torch.empty_like(f["logits"][r])
+        purlin.route_experts_grad(f["logits"][r], f["ids"][r], grad_weights, grad, self.handle)
+        return grad
+
+    def _embed_grad(self, grad_x, tokens, bases=None):
+        """Gradients of every rank's range of the table, added to `bases`, given those of its
+        rows and everyone's tokens."""
+        s, h = self.shape, self.handle
+        everyone = [self._new(s.world * s.tokens, s.width) for _ in grad_x]
         purlin.all_gather(grad_x, everyone, h)
-        grad_tables = [torch.empty_like(t) for t in self.tables]
-        for r in W:
-            purlin.embed_grad(everyone[r], f["everyone"][r], grad_tables[r], h, first=r * self.tables[r].shape[0],
-                              scale=s.scale)
-        return [*grad_tables, grad_router[0], *grad_up, *grad_down]
+        grads = [torch.empty_like(t) for t in self.tables] if bases is None else bases
+        for r, grad in enumerate(grads):
+            purlin.embed_grad(everyone[r], tokens[r], grad, h, first=r * self.tables[r].shape[0], scale=s.scale,
+                              base=None if bases is None else grad)
+        return grads
 
     def step(self, tokens, targets):
         """One step on half the mean squared distance to the targets: (loss, gradients' norm)."""
