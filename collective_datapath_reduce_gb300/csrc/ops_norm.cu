@@ -279,7 +279,10 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
       squares = warp_sum(__fmaf_rn(of_lane * d, d, of.y));
     }
     const float rstd = inverse(squares * per, a.eps);
-    if (a.stats && tid == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+    if (a.stats && tid == 0) {
+      a.stats[2 * row] = mean;
+      a.stats[2 * row + 1] = rstd;
+    }
     if (total) {
       in.put(total, v);
       total += rows * a.ldt;
@@ -391,11 +394,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   for (int i = 0; i < P; ++i) dw[i] = db[i] = f2(0.f);
   int turn = 0;
   T* dx = (T*)a.y + row * a.ldy + in.tid * N;
-  float2 ahead = row < a.tokens ? *reinterpret_cast<const float2*>(a.stats + 2 * row) : make_float2(0.f, 0.f);
+  float2 ahead = row < a.tokens ? make_float2(a.stats[2 * row], a.stats[2 * row + 1]) : make_float2(0.f, 0.f);
   for (; row < a.tokens; row += rows) {
     const uint32_t at = in.next();
     const float mean = ahead.x, rstd = ahead.y;
-    if (row + rows < a.tokens) ahead = *reinterpret_cast<const float2*>(a.stats + 2 * (row + rows));
+    if (row + rows < a.tokens) ahead = make_float2(a.stats[2 * (row + rows)], a.stats[2 * (row + rows) + 1]);
     const T *of_x = (const T*)a.x + row * a.ldx, *of_g = (const T*)a.grad_y + row * a.ldg;
     F2 x[P], g[P], sum = f2(0.f), sum_xh = f2(0.f);
     in.get(at, 0, of_x, x);

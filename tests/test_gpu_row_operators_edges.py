@@ -1,0 +1,168 @@
+"""Layer norm, balance and distillation at odd addresses of every buffer, in host memory, past 32-bit offsets, by threads."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators as O
+from collective_datapath_reduce_gb300 import torch_api as purlin
+from test_gpu_operators import DEV, E24, Guarded, h  # noqa: F401 (h: a fixture)
+from test_gpu_row_operators import BF16, F32, everything, status
+
+pytestmark = pytest.mark.gpu
+
+
+def at(t, off):
+    """A copy of t that starts `off` elements past a 256-byte boundary."""
+    flat = torch.empty(t.numel() + off, dtype=t.dtype, device=t.device)
+    out = flat[off:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_buffer_at_the_alignment_of_its_elements(h, dtype, off):  # noqa: F811
+    """Results are those of aligned buffers: exactly where the arithmetic does not go by vectors."""
+    g = torch.Generator(device=DEV).manual_seed(off)
+    T, D, E, k, V, K = 37, 264, 40, 4, 1032, 12
+    r = lambda *s, t=dtype: torch.randn(s, generator=g, device=DEV).to(t)  # noqa: E731
+    x, dy, dt, w, b = r(T, D), r(T, D), r(T, D), r(D), r(D)
+    logits, z, teacher, dl = r(T, E), r(T, V), r(T, K, t=F32), r(T, t=F32)
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, 1).indices.to(torch.int32)
+    words = torch.rand(T, V, generator=g, device=DEV).topk(K, 1).indices.to(torch.int32)
+
+    def run(a):
+        n = lambda *s, t=dtype: a(torch.zeros(s, dtype=t, device=DEV))  # noqa: E731
+        o = dict(y=n(T, D), total=n(T, D), stats=n(T, 2, t=F32), dx=n(T, D), dw=n(D), db=n(D), counts=n(E, t=torch.int32),
+                 sums=n(2 * E + 1, t=F32), loss=n(1, t=F32), dlogits=n(T, E), kl=n(T, t=F32), ks=n(T, 2, t=F32), dz=n(T, V))
+        purlin.layer_norm(a(x), a(w), a(b), o["y"], h, residual=a(dt), total=o["total"], stats=o["stats"])
+        purlin.layer_norm_grad(a(dy), o["total"], o["stats"], a(w), o["dx"], o["dw"], o["db"], h, grad_total=a(dt))
+        purlin.balance_loss(a(logits), a(ids), o["counts"], o["sums"], o["loss"], h)
+        purlin.balance_loss_grad(a(logits), a(ids), o["sums"], o["loss"], o["dlogits"], h, base=a(logits))
+        purlin.distil_loss(a(z), a(words), a(teacher), o["kl"], o["ks"], h)
+        purlin.distil_loss_grad(a(z), a(words), a(teacher), o["ks"], a(dl), o["dz"], h)
+        return o
+    want, got = run(lambda t: t), run(lambda t: at(t, off))
+    for name in want:
+        a, b_ = want[name].double(), got[name].double()
+        # other orders of sums of 1032 terms at most, and the output's rounding
+        step = 2.0 ** -7 if want[name].dtype is BF16 else 0.0
+        bound = step * a.abs() + 2 * 1032 * E24 * a.abs().mean() * 16
+        assert ((a - b_).abs() <= bound).all(), name
+    assert torch.equal(want["counts"], got["counts"])
+
+
+def test_rows_in_pinned_host_memory(h):  # noqa: F811
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for D in (96, 101):
+        x = torch.randn(9, D, generator=g, device=DEV)
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        w, stats, dw = torch.randn(D, generator=g, device=DEV), torch.empty(9, 2, device=DEV), torch.empty(D, device=DEV)
+        hx, hy, hdx = x.cpu().pin_memory(), torch.empty(9, D).pin_memory(), torch.empty(9, D).pin_memory()
+        purlin.layer_norm(x, w, None, y, h, stats=stats)
+        purlin.layer_norm(hx, w, None, hy, h)
+        purlin.layer_norm_grad(y, x, stats, w, dx, dw, None, h)
+        purlin.layer_norm_grad(y, hx, stats, w, hdx, dw, None, h)
+        z = torch.randn(4, 5 * D, generator=g, device=DEV)
+        ids, t = torch.arange(8, device=DEV).view(4, 2), torch.zeros(4, 2, device=DEV)
+        loss, other, s = torch.empty(4, device=DEV), torch.empty(4, device=DEV), torch.empty(4, 2, device=DEV)
+        purlin.distil_loss(z, ids, t, loss, s, h)
+        purlin.distil_loss(z.cpu().pin_memory(), ids, t, other, s, h)
+        counts, sums, sums2 = torch.empty(D, dtype=torch.int32, device=DEV), torch.empty(2 * D + 1, device=DEV), torch.empty(2 * D + 1, device=DEV)
+        picks = torch.zeros(9, 1, dtype=torch.int32, device=DEV)
+        purlin.balance_loss(x, picks, counts, sums, None, h)
+        purlin.balance_loss(hx, picks, counts, sums2, None, h)
+        torch.cuda.synchronize()
+        assert torch.equal(hy, y.cpu()) and torch.equal(hdx, dx.cpu()) and torch.equal(loss, other) and torch.equal(sums, sums2)
+
+
+def test_rows_past_32_bit_offsets(h):  # noqa: F811
+    """2.3 Gi elements: the last rows as the first."""
+    T, D = 70001, 33000
+    x = torch.empty(T, D, dtype=BF16, device=DEV)
+    row = torch.randn(3, D, device=DEV).to(BF16)
+    for part in x.split(9999):
+        part.copy_(row[0])
+    x[-2:] = row[1:]
+    small = torch.cat([row[:1], row[1:]])
+    ids, t = torch.tensor([[5, D - 1]], device=DEV), torch.tensor([[1.0, 0.5]], device=DEV)
+    loss, stats = torch.empty(T, device=DEV), torch.empty(T, 2, device=DEV)
+    want, s = torch.empty(3, device=DEV), torch.empty(3, 2, device=DEV)
+    purlin.distil_loss(x, ids.expand(T, 2).contiguous(), t.expand(T, 2).contiguous(), loss, stats, h)
+    purlin.distil_loss(small, ids.expand(3, 2).contiguous(), t.expand(3, 2).contiguous(), want, s, h)
+    # the few rows are cut into CTAs, whose sums join in another order
+    assert ((loss[-2:] - want[1:]).abs() <= 600 * E24 * want[1:].abs()).all() and (loss[:-2] == loss[0]).all()
+    grad = torch.ones(T, device=DEV)
+    purlin.distil_loss_grad(x, ids.expand(T, 2).contiguous(), t.expand(T, 2).contiguous(), stats, grad, x, h)
+    out = torch.empty_like(small)
+    purlin.distil_loss_grad(small, ids.expand(3, 2).contiguous(), t.expand(3, 2).contiguous(), stats[-3:].contiguous(), grad[:3], out, h)
+    assert torch.equal(x[-3:], out) and torch.equal(x[0], x[-3])
+    del x
+    T, D = 300001, 8192
+    x = torch.empty(T, D, dtype=BF16, device=DEV)
+    for part in x.split(9999):
+        part.copy_(row[0, :D])
+    x[-2:] = row[1:, :D]
+    stats, dw = torch.empty(T, 2, device=DEV), torch.empty(D, device=DEV)
+    purlin.layer_norm(x, None, None, x, h, stats=stats)
+    y, s3 = torch.empty(3, D, dtype=BF16, device=DEV), torch.empty(3, 2, device=DEV)
+    purlin.layer_norm(small[:, :D], None, None, y, h, stats=s3)
+    assert torch.equal(x[-2:], y[1:]) and torch.equal(stats[-2:], s3[1:]) and torch.equal(x[0], y[0]) and torch.equal(x[T // 2], y[0])
+    purlin.layer_norm_grad(x, x, stats, None, x, None, dw, h)
+    want = (T - 2) * y[0].double() + y[1].double() + y[2].double()
+    size = (T - 2) * y[0].double().abs() + y[1].double().abs() + y[2].double().abs()
+    assert ((dw.double() - want).abs() <= size * (T // 152 + 16 + 152 // 8 + 8 + 1) * E24).all()
+    assert torch.equal(x[0], x[T // 2])
+
+
+def test_threads_and_graphs_on_one_handle(h):  # noqa: F811
+    call, want = everything(h)
+    call()
+    torch.cuda.synchronize()
+    jobs, failures = [everything(h) for _ in range(4)], []
+    start = threading.Barrier(len(jobs))
+
+    def work(call):
+        try:
+            start.wait()
+            for _ in range(5):
+                call()
+        except Exception as e:  # told to the main thread
+            failures.append(e)
+    threads = [threading.Thread(target=work, args=(c,)) for c, _ in jobs]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    assert not failures
+    # two graphs, replayed at once on two streams, beside the handle's own blocks
+    sides, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    more = [everything(h) for _ in sides]
+    torch.cuda.synchronize()
+    for (call, _), side in zip(more, sides):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            call()
+            call()
+    for _ in range(3):
+        for graph, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                graph.replay()
+        jobs[0][0]()
+    torch.cuda.synchronize()
+    for _, got in jobs + more:
+        for name in want:
+            assert torch.equal(got[name], want[name]), name
+    assert status(h) == (0, 0)
+
+
+def test_rows_behind_the_last_stay_as_they_were(h):  # noqa: F811
+    """Outputs with room for more rows than there are tokens: a slice is written, nothing behind it."""
+    x = torch.randn(64, 80, device=DEV)
+    y, stats = Guarded(64, 80, F32), Guarded(64, 2, F32)
+    purlin.layer_norm(x[:5], None, None, y.view[:5], h, stats=stats.view[:5])
+    assert (y.view[5:] == -77).all() and (stats.view[5:] == -77).all() and y.intact() and stats.intact()
+    want = O.layer_norm(x[:5].double().cpu().numpy())[0]
+    assert np.abs(y.view[:5].double().cpu().numpy() - want).max() < 200 * E24 * 4
