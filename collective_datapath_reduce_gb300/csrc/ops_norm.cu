@@ -457,7 +457,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   for (uint32_t c = threadIdx.x; c < 2 * D; c += blockDim.x) {
     float v = 0.f;
     for (int g = 0; g < groups; ++g) v += sums[2 * g * D + c];
-    a.parts[(uint64_t)blockIdx.x * 2 * D + c] = v;
+    if (gridDim.x > 1) {
+      a.parts[(uint64_t)blockIdx.x * 2 * D + c] = v;
+    } else if (W* out = (W*)(c < D ? a.grad_weight : a.grad_bias)) {  // all there is
+      out[c < D ? c : c - D] = from_f32<W>(v);
+    }
   }
 }
 
@@ -641,7 +645,7 @@ purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
     };
     st = vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
   }
-  if (st || !sums) return st;
+  if (st || !sums || (parts == 1 && a.width <= (uint64_t)kMostWidth)) return st;
   return op_launch(norm_join_kernel<W>, (a.width + 31) / 32 * 2, kJoinWarps * 32, 0, s, a, parts);
 }
 

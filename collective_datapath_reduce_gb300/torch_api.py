@@ -494,10 +494,11 @@ def layer_norm_grad(grad_y, x, stats, weight, grad_x, grad_weight, grad_bias, ha
     _packed(stats, (T, 2), torch.float32, what, "stats")
     ldt = _matrix(grad_total, T, D, grad_y.dtype, what, "grad_total") if grad_total is not None else 0
     ldo = _matrix(grad_x, T, D, grad_y.dtype, what, "grad_x")
-    of = next((t for t in (weight, grad_weight, grad_bias) if t is not None), None)
-    dw = P.PL_F32 if of is None else _values(of, what)
-    for t, name in ((weight, "weight"), (grad_weight, "grad_weight"), (grad_bias, "grad_bias")):
-        _vector(t, D, of.dtype if of is not None else None, what, name)
+    of = weight if weight is not None else grad_weight if grad_weight is not None else grad_bias
+    dw, dtype = (P.PL_F32, None) if of is None else (_values(of, what), of.dtype)
+    _vector(weight, D, dtype, what, "weight")
+    _vector(grad_weight, D, dtype, what, "grad_weight")
+    _vector(grad_bias, D, dtype, what, "grad_bias")
     nbytes = P.purlin_layer_norm_grad_bytes(T, D) if grad_weight is not None or grad_bias is not None else 0
     _call_in_workspace(P.purlin_layer_norm_grad, what, handle, stream, nbytes, grad_y, ldg, x, ldx, stats, T, D, dt, weight,
                        dw, grad_total, ldt, grad_x, ldo, grad_weight, grad_bias)
