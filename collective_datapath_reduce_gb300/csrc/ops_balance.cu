@@ -44,58 +44,63 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
   return v;
 }
 
-// N (an even number) neighbouring values in each lane; those past `width` are `none`.
+// A row's values in a warp's lanes, N (an even number) in each: vectors of M
+// neighbours, 32 vectors apart, or single values where the row is not made of such.
 template <typename T, int N>
 struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Lane {
+  static constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
   T v[N];
+  // Which value the lane's i-th is.
+  static __device__ __forceinline__ int at(int i, bool vec) {
+    const int lane = threadIdx.x & 31;
+    return vec ? (lane + i / M * 32) * M + i % M : lane + i * 32;
+  }
+  // The row at p; values past its width are `none`.
   __device__ __forceinline__ void load(const T* p, int width, bool vec, float none) {
-    const int e0 = (threadIdx.x & 31) * N;
-    constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
     if (vec) {
-      if (e0 < width) {
 #pragma unroll
-        for (int q = 0; q < N; q += M)
-          *reinterpret_cast<Pack<T, M>*>(v + q) = *reinterpret_cast<const Pack<T, M>*>(p + e0 + q);
-        return;
+      for (int q = 0; q < N; q += M) {
+        Pack<T, M> r;
+        if (at(q, true) < width) r = *reinterpret_cast<const Pack<T, M>*>(p + at(q, true));
+        else
+#pragma unroll
+          for (int i = 0; i < M; ++i) r.v[i] = from_f32<T>(none);
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[q + i] = r.v[i];
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = from_f32<T>(none);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = e0 + i < width ? p[e0 + i] : from_f32<T>(none);
+      for (int i = 0; i < N; ++i) v[i] = at(i, false) < width ? p[at(i, false)] : from_f32<T>(none);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int width, bool vec) const {
+    if (vec) {
+#pragma unroll
+      for (int q = 0; q < N; q += M) {
+        Pack<T, M> r;
+#pragma unroll
+        for (int i = 0; i < M; ++i) r.v[i] = v[q + i];
+        if (at(q, true) < width) st_pack(p + at(q, true), r);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (at(i, false) < width) p[at(i, false)] = v[i];
     }
   }
   __device__ __forceinline__ void pairs(F2 (&p)[N / 2]) const {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) p[i] = f2(to_f32(v[2 * i]), to_f32(v[2 * i + 1]));
   }
-};
-template <typename T, int N>
-__device__ __forceinline__ void st_lane(T* p, int width, bool vec, const F2 (&x)[N / 2]) {
-  const int e0 = (threadIdx.x & 31) * N;
-  constexpr int M = N * sizeof(T) > 16 ? 16 / sizeof(T) : N;
-  T v[N];
+  __device__ __forceinline__ void round(const F2 (&p)[N / 2]) {
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const float2 of = split(x[i]);
-    v[2 * i] = from_f32<T>(of.x);
-    v[2 * i + 1] = from_f32<T>(of.y);
-  }
-  if (vec) {
-    if (e0 >= width) return;
-#pragma unroll
-    for (int q = 0; q < N; q += M) {
-      Pack<T, M> r;
-#pragma unroll
-      for (int i = 0; i < M; ++i) r.v[i] = v[q + i];
-      st_pack(p + e0 + q, r);
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 of = split(p[i]);
+      v[2 * i] = from_f32<T>(of.x);
+      v[2 * i + 1] = from_f32<T>(of.y);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (e0 + i < width) p[e0 + i] = v[i];
   }
-}
+};
 
 // 2^x; results below the smallest normal number are 0.
 __device__ __forceinline__ F2 ex2(F2 x) {
@@ -217,7 +222,7 @@ struct Token {
   }
 };
 
-// A warp holds a token, N neighbouring experts in each lane, and adds its
+// A warp holds a token, N experts in each lane, and adds its
 // shares to the lane's sums; picks are counted in shared memory.  The warps'
 // sums are added in order, then, of one cluster `alone`, the CTAs'.
 template <typename T, int N>
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
     if (warp / kRows == first / kRows)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int e = lane * N + i;
+        const int e = Lane<T, N>::at(i, vec);
         const float2 of = split(sum[i / 2]);
         if (e < E) dyn[warp % kRows * E + e] = (i % 2 ? of.y : of.x) + (first ? dyn[warp % kRows * E + e] : 0.f);
       }
@@ -376,7 +381,7 @@ template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(const __grid_constant__ BalanceArgs a, int vec) {
   op_wait();
   __shared__ float tmp[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.experts;
+  const int warp = threadIdx.x >> 5, E = a.experts;
   const uint64_t step = (uint64_t)gridDim.x * kWarps;
   uint64_t t = (uint64_t)blockIdx.x * kWarps + warp;
   Token<T, N> now, next;
@@ -392,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(c
   F2 c[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = lane * N + 2 * i;
-    c[i] = f2(f) * f2(e < E ? a.sums[e] : 0.f, e + 1 < E ? a.sums[e + 1] : 0.f);
+    const int e = Lane<T, N>::at(2 * i, vec), o = Lane<T, N>::at(2 * i + 1, vec);
+    c[i] = f2(f) * f2(e < E ? a.sums[e] : 0.f, o < E ? a.sums[o] : 0.f);
   }
   for (; t < a.tokens; t += step) {
     if constexpr (AHEAD) {
@@ -425,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(c
 #pragma unroll
       for (int i = 0; i < P; ++i) x[i] = x[i] + slope[i];
     }
-    st_lane<T, N>((T*)a.grad_logits + t * a.ldg, E, vec, x);
+    now.row.round(x);
+    now.row.store((T*)a.grad_logits + t * a.ldg, E, vec);
   }
 }
 
@@ -441,11 +447,11 @@ purlin_status with_lanes(int experts, F f) {
 
 template <typename T, int N>
 bool even(const BalanceArgs& a) {
-  const uint64_t need = std::min<uint64_t>(16, N * sizeof(T));
+  constexpr uint64_t need = Lane<T, N>::M * sizeof(T);
   uint64_t bits = (uint64_t)(uintptr_t)a.logits | a.ld * sizeof(T);
   if (a.grad_logits) bits |= (uint64_t)(uintptr_t)a.grad_logits | a.ldg * sizeof(T);
   if (a.base) bits |= (uint64_t)(uintptr_t)a.base | a.ldb * sizeof(T);
-  return a.experts % N == 0 && bits % need == 0;  // every lane's experts exist or none
+  return a.experts % Lane<T, N>::M == 0 && bits % need == 0;  // a vector's experts exist or none
 }
 
 // Few tokens go through one cluster and one launch: 4 for each of its warps.

@@ -9,7 +9,6 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kMostThreads = 512;
 constexpr int kSms = 152;
-constexpr int kMostWidth = 8192;  // that 512 threads hold in their registers
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -18,7 +17,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 __device__ __forceinline__ void group_barrier(int group, int tpr) {
-  if (tpr == 32) __syncwarp();
+  if (tpr <= 32) __syncwarp();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
 }
 
@@ -49,12 +48,16 @@ __device__ __forceinline__ float ld_shared1(uint32_t at) {
   }
 }
 
+// How rows lie.  On 16-byte boundaries, and the threads' vectors fill them (kWhole)
+// or reach past their ends, whole vectors (kPart); or any other way, element by
+// element (kSingle).
+enum class Lie { kWhole, kPart, kSingle };
+
 // Rows on their way into shared memory.  A CTA is `groups` groups of tpr
 // threads, a row each at a time; a group has `stages` slots, a row of each of n
 // matrices in every one, so that stages - 1 rows are under way while one is
-// worked on.  Aligned rows: a thread copies the vectors that it uses, and waits
-// for nobody else.  Others (SHIFT): the aligned granules that hold the row's
-// bytes, which the threads then share.
+// worked on.  A thread copies the vectors that it uses, and waits for nobody
+// else; kSingle's threads share the aligned granules that hold the row's bytes.
 struct Ring {
   int n, stages, tpr, groups;
   uint32_t granules;  // of a row's slot
@@ -62,42 +65,52 @@ struct Ring {
 };
 
 // A thread's view of a row: NV vectors of N elements, tpr vectors apart, as P
-// pairs.  Beside the row it reads the row's first vector (element) in place of
-// what is not there: `inside` is 0 for those, and they are not written.
-template <typename T, int N, int NV, int M>
+// pairs.  For a vector beside the row it reads the row's first and counts it 0 times.
+template <typename T, Lie LIE, int NV, int M>
 struct Stream {
-  static constexpr bool SHIFT = N == 1;
-  static constexpr int P = N * NV / 2, S = N * (int)sizeof(T);  // S: bytes of a vector
-  const char* from[M];   // the next row to fetch, of each matrix; aligned: this thread's first vector
+  static constexpr bool SINGLE = LIE == Lie::kSingle;
+  static constexpr int N = SINGLE ? 1 : V16<T>, P = N * NV / 2, S = N * (int)sizeof(T);  // S: bytes of a vector
+  const char* from[M];   // the next row to fetch, of each matrix; but for kSingle: this thread's first vector
   uint64_t step[M];      // bytes to the one behind it
   uint64_t left;         // rows to fetch
-  uint32_t bytes, matrix, stage, slots, in, out, first;  // of shared memory
-  int tid, group, tpr, stages;
+  uint32_t bytes;        // of a row
+  uint32_t matrix, stage, slots, in, out, first;  // of shared memory, in bytes
+  int tid, group, tpr, stages, width;
 
-  __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t width) {
+  __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t columns) {
     tpr = r.tpr;
     stages = r.stages;
     tid = threadIdx.x % tpr;
     group = threadIdx.x / tpr;
-    bytes = (uint32_t)(width * sizeof(T));
+    width = (int)columns;
+    bytes = (uint32_t)width * sizeof(T);
     matrix = (uint32_t)r.groups * r.granules * 16;
     stage = matrix * r.n;
     slots = stage * stages;
     in = out = 0;
     first = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)group * r.granules * 16;
-    left = 0;
   }
   // Rows `row`, row + rows, .. of `tokens`.
   __device__ __forceinline__ void take(uint64_t row, uint64_t rows, uint64_t tokens) {
     left = row < tokens ? (tokens - row - 1) / rows + 1 : 0;
   }
   __device__ __forceinline__ void open(int m, const void* p, uint64_t ld, uint64_t row, uint64_t rows) {
-    from[m] = (const char*)p + row * ld * sizeof(T) + (SHIFT ? 0 : tid * 16);
+    from[m] = (const char*)p + row * ld * sizeof(T) + (SINGLE ? 0 : tid * 16);
     step[m] = rows * ld * sizeof(T);
   }
-  // Bytes from the row's start to vector j, and whether it is there.
+  // This thread's first vector of a row of a matrix that is written.
+  __device__ __forceinline__ T* place(void* p, uint64_t ld, uint64_t row) const {
+    return (T*)p + row * ld + tid * N;
+  }
+  // Bytes from the row's start to vector j, its column, and whether it is there.
   __device__ __forceinline__ uint32_t offset(int j) const { return (uint32_t)(tid + j * tpr) * S; }
-  __device__ __forceinline__ bool there(int j) const { return offset(j) < bytes; }
+  __device__ __forceinline__ int column(int j) const { return (tid + j * tpr) * N; }
+  __device__ __forceinline__ bool there(int j) const { return LIE == Lie::kWhole || offset(j) < bytes; }
+  // How often a pair counts.
+  __device__ __forceinline__ F2 times(int pair) const {
+    if constexpr (SINGLE) return f2(there(2 * pair) ? 1.f : 0.f, there(2 * pair + 1) ? 1.f : 0.f);
+    return f2(there(pair * 2 / N) ? 1.f : 0.f);
+  }
 
   // One more row, or an empty step behind the last.
   __device__ __forceinline__ void fetch() {
@@ -105,11 +118,11 @@ struct Stream {
       --left;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        if (!from[m]) break;
+        if (!step[m]) break;
         const uint32_t to = first + in + m * matrix;
-        if constexpr (SHIFT) {
-          const uint32_t off = (uint32_t)((uintptr_t)from[m] & 15u), end = off + bytes;
-          for (uint32_t i = tid * 16; i < end; i += tpr * 16) copy16(to + i, from[m] - off + i);
+        if constexpr (SINGLE) {
+          const uint32_t off = (uint32_t)((uintptr_t)from[m] & 15u), last = off + bytes;
+          for (uint32_t i = tid * 16; i < last; i += tpr * 16) copy16(to + i, from[m] - off + i);
         } else {
 #pragma unroll
           for (int j = 0; j < NV; ++j)
@@ -132,7 +145,7 @@ struct Stream {
     else if (stages == 3) copies_left<1>();
     else if (stages == 4) copies_left<2>();
     else copies_left<3>();
-    if (SHIFT) group_barrier(group, tpr);
+    if (SINGLE) group_barrier(group, tpr);
     const uint32_t at = first + out;
     out += stage;
     if (out == slots) out = 0;
@@ -142,9 +155,9 @@ struct Stream {
   // What this thread has of matrix m's row, which starts at address `row`.
   __device__ __forceinline__ void get(uint32_t at, int m, const void* row, F2 (&v)[P]) const {
     at += m * matrix;
-    if constexpr (!SHIFT) {
+    if constexpr (!SINGLE) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) pairs_of<T>(ld_shared16(at + (there(j) ? offset(j) : 0)), v + j * (P / NV));
+      for (int j = 0; j < NV; ++j) pairs_of<T>(ld_shared16(at + (there(j) ? offset(j) : 0)), v + j * (N / 2));
     } else {
       at += (uint32_t)((uintptr_t)row & 15u);
 #pragma unroll
@@ -154,10 +167,10 @@ struct Stream {
   }
   // The same into global memory, rounded; `to`: this thread's first vector.
   __device__ __forceinline__ void put(T* to, const F2 (&v)[P]) const {
-    if constexpr (!SHIFT) {
+    if constexpr (!SINGLE) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (there(j)) *reinterpret_cast<uint4*>((char*)to + j * tpr * 16) = packed<T>(v + j * (P / NV));
+        if (there(j)) *reinterpret_cast<uint4*>((char*)to + j * tpr * 16) = packed<T>(v + j * (N / 2));
     } else {
 #pragma unroll
       for (int j = 0; j < NV; j += 2) {
@@ -171,81 +184,85 @@ struct Stream {
   template <typename W>
   __device__ __forceinline__ void columns(const void* p, float none, F2 (&v)[P]) const {
     float x[2 * P];
+    const bool vec = !SINGLE && ((uintptr_t)p & 15u) == 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      const W* w = (const W*)p + column(j);
 #pragma unroll
       for (int i = 0; i < N; ++i) x[j * N + i] = there(j) ? none : 0.f;
       if (!p || !there(j)) continue;
-      const W* w = (const W*)p + (tid + j * tpr) * N;
-      constexpr int K = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
+      if (vec) {
+        constexpr int K = N * sizeof(W) > 16 ? 16 / sizeof(W) : N;
 #pragma unroll
-      for (int q = 0; q < N; q += K) {
-        const Pack<W, K> of = *reinterpret_cast<const Pack<W, K>*>(w + q);
+        for (int q = 0; q < N; q += K) {
+          const Pack<W, K> of = *reinterpret_cast<const Pack<W, K>*>(w + q);
 #pragma unroll
-        for (int i = 0; i < K; ++i) x[j * N + q + i] = to_f32(of.v[i]);
+          for (int i = 0; i < K; ++i) x[j * N + q + i] = to_f32(of.v[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[j * N + i] = to_f32(w[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = f2(x[2 * i], x[2 * i + 1]);
   }
-  // 1 for the row's elements, 0 beside them.
-  __device__ __forceinline__ F2 inside(int pair) const {
-    const int j = pair * 2 / N;
-    if constexpr (!SHIFT) return f2(there(j) ? 1.f : 0.f);
-    return f2(there(j) ? 1.f : 0.f, there(j + 1) ? 1.f : 0.f);
-  }
-  // The column of a pair's first (0) or second (1) element.
-  __device__ __forceinline__ uint32_t column(int pair, int second) const {
-    const int e = 2 * pair + second;
-    return (uint32_t)(tid + e / N * tpr) * N + e % N;
-  }
 };
+
+// Sum over the lanes of a row: all, or the tpr (8 or 16) that have it.
+__device__ __forceinline__ float lanes_sum(float x, int tpr) {
+  if (tpr >= 32) x += __shfl_xor_sync(kAll, x, 16);
+  if (tpr >= 16) x += __shfl_xor_sync(kAll, x, 8);
+#pragma unroll
+  for (int d = 4; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
 
 __device__ __forceinline__ float inverse(float variance, float eps) { return __frcp_rn(__fsqrt_rn(variance + eps)); }
 
-// Rows pass through a CTA's registers, NV vectors of N elements in each of a row's
-// threads, and its weights stay there.  A warp takes the mean of its part and
-// the squares of the distances from that; the warps' means and squares join to
-// the row's, (sum of squares) + n (mean of the part - mean)^2 each, behind one
-// barrier.
-template <typename T, typename W, int N, int NV>
+// Rows pass through a CTA's registers, NV vectors in each of a row's threads, and
+// its weights stay there.  A warp takes the mean of its part and the squares of the
+// distances from that; the warps' means and squares join to the row's, (sum of
+// squares) + n (mean of the part - mean)^2 each, behind one barrier.
+template <typename T, typename W, Lie LIE, int NV>
 __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Ring ring) {
   op_wait();
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 tmp[2][kMostThreads / 32];
-  constexpr int P = N * NV / 2;
-  Stream<T, N, NV, 2> in(ring, smem, a.width);
-  const int tid = in.tid, tpr = in.tpr, warps = tpr >> 5, warp = tid >> 5;
+  using Rows = Stream<T, LIE, NV, 2>;
+  constexpr int P = Rows::P, N = Rows::N;
+  Rows in(ring, smem, a.width);
+  const int tid = in.tid, tpr = in.tpr, warps = tpr >> 5, warp = tid >> 5, lane = threadIdx.x & 31;
   const uint64_t rows = (uint64_t)gridDim.x * ring.groups;
   uint64_t row = (uint64_t)blockIdx.x * ring.groups + in.group;
   in.take(row, rows, a.tokens);
-  in.open(0, a.x, a.ldx, row, rows);
-  if (a.residual) in.open(1, a.residual, a.ldr, row, rows);
-  else in.from[1] = nullptr;
   const bool second = a.residual != nullptr;
-  const uint32_t D = (uint32_t)a.width;
+  in.open(0, a.x, a.ldx, row, rows);
+  in.step[1] = 0;
+  if (second) in.open(1, a.residual, a.ldr, row, rows);
   in.begin();
   F2 w[P], b[P];
   in.template columns<W>(a.weight, 1.f, w);
   in.template columns<W>(a.bias, 0.f, b);
-  // elements of this warp, and of any warp: those of vectors 32 warp + j tpr .. + 32
+  // elements of a warp (of a row of a few lanes: all)
   auto part = [&](int of) {
-    uint32_t n = 0;
+    if (warps < 2) return in.width;
+    int n = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t first = (uint32_t)(of * 32 + j * tpr) * N;
-      n += first < D ? min(D - first, 32u * N) : 0u;
+      const int c = (of * 32 + j * tpr) * N;
+      n += max(0, min(in.width - c, 32 * N));
     }
     return n;
   };
-  const float mine = (float)part(warp), per_mine = mine > 0.f ? __frcp_rn(mine) : 0.f, per = __frcp_rn((float)D);
+  const float mine = (float)part(warp), per_mine = mine > 0.f ? __frcp_rn(mine) : 0.f, per = __frcp_rn((float)in.width);
   // lane i joins warp i's
-  const int lane = tid & 31;
   const float of_lane = lane < warps ? (float)part(lane) : 0.f, per_lane = of_lane > 0.f ? __frcp_rn(of_lane) : 0.f;
   int turn = 0;
-  T* y = (T*)a.y + row * a.ldy + tid * N;
-  T* total = a.total ? (T*)a.total + row * a.ldt + tid * N : nullptr;
-  for (; row < a.tokens; row += rows) {
+  T* y = in.place(a.y, a.ldy, row);
+  T* total = a.total ? in.place(a.total, a.ldt, row) : nullptr;
+  // the rows of a warp's lanes need not end together
+  for (; __any_sync(kAll, row < a.tokens); row += rows) {
     const uint32_t at = in.next();
     F2 v[P], sum = f2(0.f);
     in.get(at, 0, (const T*)a.x + row * a.ldx, v);
@@ -259,15 +276,15 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
       }
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum = fma2(in.inside(i), v[i], sum);
-    float s = warp_sum(both(sum)), mean = s * per_mine;
+    for (int i = 0; i < P; ++i) sum = LIE != Lie::kWhole ? fma2(in.times(i), v[i], sum) : sum + v[i];
+    float s = lanes_sum(both(sum), tpr), mean = s * per_mine;
     sum = f2(0.f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const F2 d = in.inside(i) * (v[i] + f2(-mean));
-      sum = fma2(d, d, sum);
+      const F2 d = v[i] + f2(-mean);
+      sum = fma2(LIE != Lie::kWhole ? in.times(i) * d : d, d, sum);
     }
-    float squares = warp_sum(both(sum));
+    float squares = lanes_sum(both(sum), tpr);
     if (warps > 1) {
       float2* t = tmp[turn] + in.group * warps;
       turn ^= 1;
@@ -275,10 +292,11 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
       group_barrier(in.group, tpr);
       const float2 of = lane < warps ? t[lane] : make_float2(0.f, 0.f);
       mean = warp_sum(of.x) * per;
-      const float d = __fmaf_rn(of.x, per_lane, -mean);
-      squares = warp_sum(__fmaf_rn(of_lane * d, d, of.y));
+      const float off = __fmaf_rn(of.x, per_lane, -mean);
+      squares = warp_sum(__fmaf_rn(of_lane * off, off, of.y));
     }
     const float rstd = inverse(squares * per, a.eps);
+    if (row >= a.tokens) continue;
     if (a.stats && tid == 0) {
       a.stats[2 * row] = mean;
       a.stats[2 * row + 1] = rstd;
@@ -354,6 +372,7 @@ __device__ __forceinline__ float half_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float* tmp) {
+  if (tpr < 32) return make_float2(lanes_sum(x.x, tpr), lanes_sum(x.y, tpr));
   const int lane = threadIdx.x & 31, half = lane >> 4, warps = tpr >> 5;
   const float other = __shfl_xor_sync(kAll, half ? x.x : x.y, 16);
   float v = half_sum((half ? x.y : x.x) + other);
@@ -365,27 +384,27 @@ __device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float*
   return make_float2(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 16));
 }
 
-template <typename T, typename W, int N, int NV>
+template <typename T, typename W, Lie LIE, int NV>
 __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_constant__ NormArgs a,
                                                                  const __grid_constant__ Ring ring) {
   op_wait();
   extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
   __shared__ float tmp[2][kMostThreads / 16];
-  constexpr int P = N * NV / 2;
-  Stream<T, N, NV, 3> in(ring, smem, a.width);
-  const int tpr = in.tpr, group = in.group, groups = ring.groups;
+  using Rows = Stream<T, LIE, NV, 3>;
+  constexpr int P = Rows::P, N = Rows::N;
+  Rows in(ring, smem, a.width);
+  const int tpr = in.tpr, group = in.group, groups = ring.groups, D = in.width;
   const uint64_t rows = (uint64_t)gridDim.x * groups;
   // groups of one number take neighbouring rows, so that the last rows, fewer than
   // groups, fall on all CTAs (20011 x 520 binary32: 25.5 us, 26.0 with neighbours to a
   // CTA; in the forward pass that is the better way, 102 us and 105)
   uint64_t row = (uint64_t)group * gridDim.x + blockIdx.x;
   in.take(row, rows, a.tokens);
+  const bool third = a.grad_total != nullptr;
   in.open(0, a.x, a.ldx, row, rows);
   in.open(1, a.grad_y, a.ldg, row, rows);
-  if (a.grad_total) in.open(2, a.grad_total, a.ldgt, row, rows);
-  else in.from[2] = nullptr;
-  const bool third = a.grad_total != nullptr;
-  const uint32_t D = (uint32_t)a.width;
+  in.step[2] = 0;
+  if (third) in.open(2, a.grad_total, a.ldgt, row, rows);
   in.begin();
   const float per = __frcp_rn((float)D);
   F2 w[P], dw[P], db[P];
@@ -393,29 +412,34 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < P; ++i) dw[i] = db[i] = f2(0.f);
   int turn = 0;
-  T* dx = (T*)a.y + row * a.ldy + in.tid * N;
+  T* dx = in.place(a.y, a.ldy, row);
   float2 ahead = row < a.tokens ? make_float2(a.stats[2 * row], a.stats[2 * row + 1]) : make_float2(0.f, 0.f);
-  for (; row < a.tokens; row += rows) {
+  // the rows of a warp's lanes need not end together
+  for (; __any_sync(kAll, row < a.tokens); row += rows) {
     const uint32_t at = in.next();
+    const bool live = row < a.tokens;
     const float mean = ahead.x, rstd = ahead.y;
     if (row + rows < a.tokens) ahead = make_float2(a.stats[2 * (row + rows)], a.stats[2 * (row + rows) + 1]);
     const T *of_x = (const T*)a.x + row * a.ldx, *of_g = (const T*)a.grad_y + row * a.ldg;
     F2 x[P], g[P], sum = f2(0.f), sum_xh = f2(0.f);
-    in.get(at, 0, of_x, x);
-    in.get(at, 1, of_g, g);
-    // beside the row the weights are 0, and sums of columns that nobody writes
+    if (live) {
+      in.get(at, 0, of_x, x);
+      in.get(at, 1, of_g, g);
+      // beside the row the weights are 0, and the columns' sums nobody's
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      x[i] = (x[i] + f2(-mean)) * f2(rstd);
-      dw[i] = fma2(g[i], x[i], dw[i]);
-      db[i] = db[i] + g[i];
-      g[i] = g[i] * w[i];
-      sum = sum + g[i];
-      sum_xh = fma2(g[i], x[i], sum_xh);
+      for (int i = 0; i < P; ++i) {
+        x[i] = (x[i] + f2(-mean)) * f2(rstd);
+        dw[i] = fma2(g[i], x[i], dw[i]);
+        db[i] = db[i] + g[i];
+        g[i] = g[i] * w[i];
+        sum = sum + g[i];
+        sum_xh = fma2(g[i], x[i], sum_xh);
+      }
     }
     float2 s = make_float2(both(sum), both(sum_xh));
     s = group_sum(s, tpr, group, tmp[turn] + group * (tpr >> 4));
     turn ^= 1;
+    if (!live) continue;
     const F2 m = f2(-s.x * per), mx = f2(-s.y * per);
     if constexpr (P > 8) {  // too many registers to hold them while the warps wait
       in.get(at, 0, of_x, x);
@@ -439,22 +463,17 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   if (!a.parts) return;
   copies_left<0>();
   __syncthreads();
-  float* sums = (float*)smem;
+  float *of_w = (float*)smem + 2 * group * D, *of_b = of_w + D;
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const float2 of_w = split(dw[i]), of_b = split(db[i]);
-    const uint32_t c = in.column(i, 0), e = in.column(i, 1);
-    if (c < D) {
-      sums[2 * group * D + c] = of_w.x;
-      sums[(2 * group + 1) * D + c] = of_b.x;
-    }
-    if (e < D) {
-      sums[2 * group * D + e] = of_w.y;
-      sums[(2 * group + 1) * D + e] = of_b.y;
-    }
+  for (int i = 0; i < 2 * P; ++i) {
+    const float2 vw = split(dw[i / 2]), vb = split(db[i / 2]);
+    if (!in.there(i / N)) continue;
+    of_w[in.column(i / N) + i % N] = i % 2 ? vw.y : vw.x;
+    of_b[in.column(i / N) + i % N] = i % 2 ? vb.y : vb.x;
   }
   __syncthreads();
-  for (uint32_t c = threadIdx.x; c < 2 * D; c += blockDim.x) {
+  const float* sums = (const float*)smem;
+  for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
     float v = 0.f;
     for (int g = 0; g < groups; ++g) v += sums[2 * g * D + c];
     if (gridDim.x > 1) {
@@ -540,112 +559,131 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_join_kernel(const __grid
 
 bool even(const void* p, uint64_t ld, uint64_t size) { return !p || (((uintptr_t)p | ld * size) & 15u) == 0; }
 
-// How the threads of a CTA share rows: NV vectors of N elements in each, in groups
-// of tpr threads.  The group whose row costs the fewest instructions, by NV vectors
-// of 14 instructions an element and 40 around them in each warp, 30 more where
-// warps wait for each other: a warp for a row of 520 binary32 values takes 5
-// vectors a lane (.. us), 5 warps one each (.. us).
-template <int N, int NV>
-void try_shape(uint64_t width, int* best, int* nv, int* tpr) {
-  const int t = (int)((width + 32 * N * NV - 1) / (32 * N * NV)) * 32;
-  if (t > kMostThreads) return;
-  const int cost = t / 32 * (NV * N * 14 + 40 + (t > 32 ? 30 : 0));
-  if (*best == 0 || cost < *best) {
-    *best = cost;
-    *nv = NV;
-    *tpr = t;
-  }
-}
-
-template <int N, typename F>
-purlin_status with_shape(uint64_t width, F f) {
-  using std::integral_constant;
-  int best = 0, nv = 0, tpr = 0;
-  constexpr integral_constant<int, N> n;
-  if constexpr (N == 8) {
-    try_shape<8, 1>(width, &best, &nv, &tpr);
-    try_shape<8, 2>(width, &best, &nv, &tpr);
-    try_shape<8, 3>(width, &best, &nv, &tpr);
-    return nv == 1 ? f(n, integral_constant<int, 1>(), tpr) : nv == 2 ? f(n, integral_constant<int, 2>(), tpr) : f(n, integral_constant<int, 3>(), tpr);
-  } else if constexpr (N == 4) {
-    try_shape<4, 1>(width, &best, &nv, &tpr);
-    try_shape<4, 2>(width, &best, &nv, &tpr);
-    try_shape<4, 4>(width, &best, &nv, &tpr);
-    try_shape<4, 5>(width, &best, &nv, &tpr);
-    return nv == 1 ? f(n, integral_constant<int, 1>(), tpr) : nv == 2 ? f(n, integral_constant<int, 2>(), tpr) :
-           nv == 4 ? f(n, integral_constant<int, 4>(), tpr) : f(n, integral_constant<int, 5>(), tpr);
-  } else {
-    try_shape<1, 4>(width, &best, &nv, &tpr);
-    try_shape<1, 16>(width, &best, &nv, &tpr);
-    return nv == 4 ? f(n, integral_constant<int, 4>(), tpr) : f(n, integral_constant<int, 16>(), tpr);
-  }
-}
-
 constexpr uint32_t kSmem = 200 * 1024;
+constexpr uint64_t kMostRow = 32 * 1024;  // bytes: of three matrices two fit
+
+// How the threads of a CTA share rows: NV vectors in each, in groups of tpr threads.
+// The group whose row costs the fewest instructions, by 14 instructions an element
+// and 40 around them in each warp, 30 more where warps wait for each other (without
+// these, 5120 bf16 values go to 20 warps, not 7: 134 us for 16384 rows, not 102; 20011 rows of 520
+// binary32 to 5 warps, not one: 38 us for the gradient, not 24).
+struct Shape {
+  int cost = 0, nv = 0, tpr = 0;
+  bool whole = false;
+  void consider(int n, int vectors, uint64_t width) {
+    const uint64_t per = (uint64_t)n * vectors;
+    int t = (int)std::min<uint64_t>((width + per - 1) / per, 2 * kMostThreads);
+    t = t <= 8 ? 8 : t <= 16 ? 16 : (t + 31) / 32 * 32;
+    if (t > kMostThreads) return;
+    const int c = t * (vectors * n * 14 + 40 + (t > 32 ? 30 : 0));
+    if (cost && c >= cost) return;
+    cost = c;
+    nv = vectors;
+    tpr = t;
+    whole = per * t == width;
+  }
+};
+
+// f(how rows lie, vectors of a thread, threads of a row), or wide() for rows that
+// no CTA holds.
+template <typename T, typename F, typename G>
+purlin_status with_shape(bool aligned, uint64_t width, F f, G wide) {
+  using std::integral_constant;
+  constexpr integral_constant<Lie, Lie::kWhole> whole{};
+  constexpr integral_constant<Lie, Lie::kPart> part{};
+  constexpr integral_constant<Lie, Lie::kSingle> single{};
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 2> two{};
+  constexpr integral_constant<int, 3> three{};
+  constexpr integral_constant<int, 4> four{};
+  constexpr integral_constant<int, 5> five{};
+  constexpr int V = V16<T>;
+  Shape s;
+  if (aligned && width * sizeof(T) <= kMostRow) {
+    if constexpr (V == 8) {
+      for (int nv : {1, 2, 3}) s.consider(V, nv, width);
+      if (s.nv == 3) return f(part, three, s.tpr);
+    } else {
+      for (int nv : {1, 2, 4}) s.consider(V, nv, width);
+      if (width <= 32 * 5 * V) s.consider(V, 5, width);  // registers: only where it saves the barrier
+      if (s.nv == 5) return f(part, five, s.tpr);
+      if (s.nv == 4) return s.whole ? f(whole, four, s.tpr) : f(part, four, s.tpr);
+    }
+    if (s.nv == 2) return s.whole ? f(whole, two, s.tpr) : f(part, two, s.tpr);
+    if (s.nv == 1) return s.whole ? f(whole, one, s.tpr) : f(part, one, s.tpr);
+  }
+  for (int nv : {4, 8, 16}) s.consider(1, nv, width);
+  if (s.nv == 4) return f(single, four, s.tpr);
+  if (s.nv == 8) return f(single, integral_constant<int, 8>(), s.tpr);
+  if (s.nv == 16) return f(single, integral_constant<int, 16>(), s.tpr);
+  return wide();
+}
 
 // The ring of a launch.
-template <typename T, int N, int NV>
-Ring ring_of(uint64_t width, int tpr, int n) {
+template <typename T>
+Ring ring_of(Lie lie, uint64_t width, int tpr, int n) {
   Ring r = {};
   r.n = n;
   r.tpr = tpr;
   r.groups = kMostThreads / tpr;
-  r.granules = (uint32_t)(width * sizeof(T) + (N == 1 ? 30 : 0)) / 16;
+  const uint64_t bytes = width * sizeof(T);
+  r.granules = (uint32_t)((bytes + (lie == Lie::kSingle ? 30 : 0)) / 16);
   // as many rows under way as make 64 KiB, four at most (of 40 KiB, 16384 x 5120: 104 us
   // with one, 102 with two; of 65 KiB, 20011 x 520 binary32: 24.3 us with one, 25.5 with two)
   r.stages = 1;
   const uint32_t row = r.smem();
   for (r.stages = 2; r.stages < 5 && (uint32_t)(r.stages - 1) * row < 64 * 1024; ++r.stages) {
   }
-  // rows of 8192 binary32 values of three matrices still fit twice
   while (r.groups > 1 && r.smem() > kSmem) --r.groups;
   return r;
 }
 
 template <typename T, typename W>
 purlin_status norm_t(const NormArgs& a, cudaStream_t s) {
-  if (a.width > (uint64_t)kMostWidth) return op_launch(norm_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a);
-  constexpr int V = V16<T>;
-  const uint64_t es = sizeof(T);
-  const bool vec = a.width % V == 0 && even(a.x, a.ldx, es) && even(a.residual, a.ldr, es) && even(a.y, a.ldy, es) &&
-                   even(a.total, a.ldt, es) && even(a.weight, 0, 1) && even(a.bias, 0, 1);
-  auto go = [&](auto n, auto nv, int tpr) {
-    constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
-    const Ring r = ring_of<T, N, NV>(a.width, tpr, a.residual ? 2 : 1);
+  constexpr uint64_t es = sizeof(T);
+  const bool aligned = a.width % V16<T> == 0 && even(a.x, a.ldx, es) && even(a.residual, a.ldr, es) && even(a.y, a.ldy, es) &&
+                       even(a.total, a.ldt, es);
+  auto go = [&](auto lie, auto nv, int tpr) {
+    constexpr Lie L = decltype(lie)::value;
+    constexpr int NV = decltype(nv)::value;
+    const Ring r = ring_of<T>(L, a.width, tpr, a.residual ? 2 : 1);
     const uint64_t grid = std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
-    if (purlin_status e = op_smem((const void*)norm_kernel<T, W, N, NV>, r.smem(), kSmem)) return e;
-    return op_launch(norm_kernel<T, W, N, NV>, grid, tpr * r.groups, r.smem(), s, a, r);
+    if (purlin_status e = op_smem((const void*)norm_kernel<T, W, L, NV>, r.smem(), kSmem)) return e;
+    return op_launch(norm_kernel<T, W, L, NV>, grid, tpr * r.groups, r.smem(), s, a, r);
   };
-  return vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
+  return with_shape<T>(aligned, a.width, go, [&] { return op_launch(norm_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a); });
 }
 
 template <typename T, typename W>
 purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
-  constexpr int V = V16<T>;
-  const uint64_t es = sizeof(T);
+  constexpr uint64_t es = sizeof(T);
   const bool sums = a.grad_weight || a.grad_bias;
   if (!sums) a.parts = nullptr;
   int parts = 0;
-  purlin_status st = PL_OK;
-  if (a.width > (uint64_t)kMostWidth) {
+  bool done = !sums;  // nothing is left to be joined
+  const bool aligned = a.width % V16<T> == 0 && even(a.x, a.ldx, es) && even(a.grad_y, a.ldg, es) && even(a.y, a.ldy, es) &&
+                       even(a.grad_total, a.ldgt, es);
+  auto go = [&](auto lie, auto nv, int tpr) {
+    constexpr Lie L = decltype(lie)::value;
+    constexpr int NV = decltype(nv)::value;
+    const Ring r = ring_of<T>(L, a.width, tpr, a.grad_total ? 3 : 2);
+    parts = (int)std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
+    done = done || parts == 1;
+    const uint32_t of_sums = sums ? (uint32_t)(r.groups * 2 * a.width * sizeof(float)) : 0, smem = std::max(r.smem(), of_sums);
+    if (purlin_status e = op_smem((const void*)norm_grad_kernel<T, W, L, NV>, smem, kSmem)) return e;
+    return op_launch(norm_grad_kernel<T, W, L, NV>, parts, tpr * r.groups, smem, s, a, r);
+  };
+  auto wide = [&] {
     parts = (int)std::min<uint64_t>(kSms, a.tokens);
     // the columns first: dx may lie on what they read
-    if (sums) st = op_launch(norm_columns_kernel<T>, (a.width + kColumns - 1) / kColumns * parts, kColumns, 0, s, a, parts);
-    if (!st) st = op_launch(norm_grad_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a);
-  } else if (a.tokens) {
-    const bool vec = a.width % V == 0 && even(a.x, a.ldx, es) && even(a.grad_y, a.ldg, es) && even(a.y, a.ldy, es) &&
-                     even(a.grad_total, a.ldgt, es) && even(a.weight, 0, 1);
-    auto go = [&](auto n, auto nv, int tpr) {
-      constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
-      const Ring r = ring_of<T, N, NV>(a.width, tpr, a.grad_total ? 3 : 2);
-      parts = (int)std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
-      const uint32_t of_sums = sums ? (uint32_t)(r.groups * 2 * a.width * sizeof(float)) : 0, smem = std::max(r.smem(), of_sums);
-      if (purlin_status e = op_smem((const void*)norm_grad_kernel<T, W, N, NV>, smem, kSmem)) return e;
-      return op_launch(norm_grad_kernel<T, W, N, NV>, parts, tpr * r.groups, smem, s, a, r);
-    };
-    st = vec ? with_shape<V>(a.width, go) : with_shape<1>(a.width, go);
-  }
-  if (st || !sums || (parts == 1 && a.width <= (uint64_t)kMostWidth)) return st;
+    if (sums) {
+      const uint64_t grid = (a.width + kColumns - 1) / kColumns * parts;
+      if (purlin_status e = op_launch(norm_columns_kernel<T>, grid, kColumns, 0, s, a, parts)) return e;
+    }
+    return op_launch(norm_grad_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a);
+  };
+  const purlin_status st = a.tokens ? with_shape<T>(aligned, a.width, go, wide) : PL_OK;
+  if (st || done) return st;
   return op_launch(norm_join_kernel<W>, (a.width + 31) / 32 * 2, kJoinWarps * 32, 0, s, a, parts);
 }
 

@@ -166,3 +166,62 @@ def test_rows_behind_the_last_stay_as_they_were(h):  # noqa: F811
     assert (y.view[5:] == -77).all() and (stats.view[5:] == -77).all() and y.intact() and stats.intact()
     want = O.layer_norm(x[:5].double().cpu().numpy())[0]
     assert np.abs(y.view[:5].double().cpu().numpy() - want).max() < 200 * E24 * 4
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,D", [(20003, 16), (20003, 9), (9729, 128), (2433, 65), (305, 1280), (153, 4096), (3, 5120), (5000, 24)])
+def test_rows_that_share_a_warp_or_do_not_fill_the_last_round(h, T, D, dtype):  # noqa: F811
+    """Against torch in 64 bits on the GPU: the lanes of a warp run out of rows at different times."""
+    g = torch.Generator(device=DEV).manual_seed(D)
+    x, dy, dt = (torch.randn(T, D, generator=g, device=DEV).to(dtype) for _ in range(3))
+    w = 1 + 0.1 * torch.randn(D, generator=g, device=DEV)
+    y, dx = Guarded(T, D, dtype), Guarded(T, D, dtype)
+    stats, dw, db = Guarded(T, 2, F32), Guarded(1, D, F32), Guarded(1, D, F32)
+    purlin.layer_norm(x, w, w, y.view, h, stats=stats.view)
+    purlin.layer_norm_grad(dy, x, stats.view, w, dx.view, dw.view[0], db.view[0], h, grad_total=dt)
+    x64, dy64, w64 = x.double(), dy.double(), w.double()
+    mean = x64.mean(1, keepdim=True)
+    rstd = ((x64 - mean).square().mean(1, keepdim=True) + 1e-5).rsqrt()
+    want = (x64 - mean) * rstd * w64 + w64
+    u, n = (2.0 ** -8 if dtype is BF16 else E24), 64 + D // 512
+    # distances from the mean of values below 6, and their deviation (where it is not small): a few sums of n additions
+    tol = u * want.abs() + 8 * n * E24 * (1 + rstd) * (1 + want.abs())
+    assert ((y.view.double() - want).abs() <= tol).all()
+    mean, rstd = stats.view[:, :1].double(), stats.view[:, 1:].double()
+    hat, gw = (x64 - mean) * rstd, dy64 * w64
+    want = rstd * (gw - gw.mean(1, keepdim=True) - hat * (gw * hat).mean(1, keepdim=True)) + dt.double()
+    size = rstd * (gw.abs() + gw.abs().mean(1, keepdim=True) + hat.abs() * (gw * hat).abs().mean(1, keepdim=True)) + dt.double().abs()
+    assert ((dx.view.double() - want).abs() <= u * want.abs() + 2 * n * E24 * size).all()
+    n = T // 152 + 64 + 152
+    assert ((dw.view[0].double() - (dy64 * hat).sum(0)).abs() <= (n + 4) * E24 * (dy64 * hat).abs().sum(0)).all()
+    assert ((db.view[0].double() - dy64.sum(0)).abs() <= n * E24 * dy64.abs().sum(0)).all()
+    assert all(t.intact() for t in (y, dx, stats, dw, db))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", [(3000, 96), (3000, 97), (700, 500), (40000, 8), (513, 1000), (512, 1024)])
+def test_balance_of_every_lie_of_the_logits(h, T, E, dtype):  # noqa: F811
+    """Against torch in 64 bits: experts in vectors and one by one, tokens for one launch and for two."""
+    g = torch.Generator(device=DEV).manual_seed(E)
+    x = torch.randn(T, E, generator=g, device=DEV).to(dtype)
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(4, 1).indices.to(torch.int32)
+    ids[::7] = -1
+    counts, sums, loss = torch.empty(E, dtype=torch.int32, device=DEV), torch.empty(2 * E + 1, device=DEV), torch.empty(1, device=DEV)
+    grad = Guarded(T, E, dtype)
+    purlin.balance_loss(x, ids, counts, sums, loss, h)
+    purlin.balance_loss_grad(x, ids, sums, None, grad.view, h)
+    live = (ids >= 0).any(1)
+    p = torch.softmax(x.double(), 1) * live[:, None]
+    want_c = torch.bincount(ids[ids >= 0].long(), minlength=E)
+    assert torch.equal(counts.long(), want_c) and sums[2 * E].item() == live.sum().item()
+    # a difference of 12 at most, ex2, E in lanes and warps, the reciprocal; then the tokens of a warp, warps and CTAs
+    rel = (3 * 12 + 4 + E // 32 + 6 + 3 + T // 2432 + 64) * E24
+    assert ((sums[E:2 * E].double() - p.sum(0)).abs() <= rel * p.sum(0)).all()
+    of = want_c.double() / want_c.sum()
+    want = E * (of * p.sum(0) / live.sum()).sum()
+    assert abs(loss.item() - want.item()) <= (rel + 64 * E24) * want.item()
+    c = E * of / live.sum()
+    dx = p * (c - (p * c).sum(1, keepdim=True))
+    u = 2.0 ** -8 if dtype is BF16 else E24
+    size = p * (c + (p * c).sum(1, keepdim=True))
+    assert ((grad.view.double() - dx).abs() <= u * dx.abs() + (2 * rel + 40 * E24) * size).all() and grad.intact()
