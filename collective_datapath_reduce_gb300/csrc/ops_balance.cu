@@ -225,6 +225,14 @@ struct Token {
 // A warp holds a token, N experts in each lane, and adds its
 // shares to the lane's sums; picks are counted in shared memory.  The warps'
 // sums are added in order, then, of one cluster `alone`, the CTAs'.
+//
+// Bound by the chain of a token (its loads, exponentials, two reductions across
+// the warp), of which an SM has 32 at once: 65536 x 256 binary32, sigmoid, 8 picks take 17.7
+// us, 61% of the issue slots and 3.9 TB/s (the logits alone: 9.9 us).  60 us with 16
+// warps an SM that load a token when they need it, 30 with 32 and a token fetched
+// ahead, 16 to 18 with two values an instruction and no clusters, which left SMs
+// without CTAs.  Fetching two tokens ahead (20.4 against 19.0 us with the second
+// kernel), CTAs of 32 warps (25.8) and three CTAs an SM (23) were slower.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const __grid_constant__ BalanceArgs a, int vec, int alone) {
   op_wait();
@@ -311,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, N > 16 ? 1 : 2) balance_kernel(const
   cluster_sync();
 }
 
-// The CTAs' sums: a cluster whose CTAs take `per` neighbouring experts each, in
+// The CTAs' sums (304 of them behind a large batch, 620 KB: about 4 us, two round trips
+// to the L2 and two cluster barriers): a cluster whose CTAs take `per` neighbouring experts each, in
 // up to 32 threads each that share the CTAs' sums and are added in order.
 __global__ void __launch_bounds__(kThreads) balance_parts_kernel(const __grid_constant__ BalanceArgs a, int ctas, int per) {
   op_wait();
@@ -377,6 +386,10 @@ __global__ void __launch_bounds__(kThreads) balance_join_kernel(const __grid_con
 
 // With p the shares and c_e = dL x scale x E x C_e / (sum C x N):  dx_j = p_j (c_j -
 // sum p c), for sigmoids times 1 - s_j.  A token without picks has none.
+//
+// 65536 x 256 binary32 run at 5.7 TB/s (23.9 us); small batches wait for the CTAs' first round
+// trips, the sums' and the tokens' (16383 x 160 bf16 on a base: 7.9 us, of which 2.4 are
+// the bytes').
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, N > 8 ? 1 : 2) balance_grad_kernel(const __grid_constant__ BalanceArgs a, int vec) {
   op_wait();
@@ -454,19 +467,25 @@ bool even(const BalanceArgs& a) {
   return a.experts % Lane<T, N>::M == 0 && bits % need == 0;  // a vector's experts exist or none
 }
 
-// Few tokens go through one cluster and one launch: 4 for each of its warps.
-bool few(uint64_t tokens) { return tokens <= kCluster * kWarps * 4; }
-int ctas_of(uint64_t tokens) { return few(tokens) ? kCluster : (int)std::min<uint64_t>(kMostCtas, (tokens + kWarps - 1) / kWarps); }
+// Few tokens go through one cluster and one launch, 16 for each of its warps at
+// most: the second launch costs the host 3 us (calls of 1000 x 256 / 2000 x 256 / 2000 x 500: 10.5 / 11.0 /
+// 15.3 us in one launch, 13.5 / 13.4 / 13.6 in two; on the device 7.7 / 11.0 / 15.3 and 7.1 / 8.7 / 10.8).
+bool few(uint64_t tokens, int experts) {
+  return tokens <= kCluster * kWarps * 16 && tokens * (uint64_t)experts <= kCluster * kWarps * 16 * 256;
+}
+int ctas_of(uint64_t tokens, int experts) {
+  return few(tokens, experts) ? kCluster : (int)std::min<uint64_t>(kMostCtas, (tokens + kWarps - 1) / kWarps);
+}
 
 }  // namespace
 
 size_t balance_bytes(uint64_t tokens, int experts) {
-  return few(tokens) ? 0 : (size_t)ctas_of(tokens) * (2 * (size_t)experts + 1) * sizeof(uint32_t);
+  return few(tokens, experts) ? 0 : (size_t)ctas_of(tokens, experts) * (2 * (size_t)experts + 1) * sizeof(uint32_t);
 }
 
 purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
-  const bool alone = few(a.tokens);
-  const int ctas = ctas_of(a.tokens), per = (a.experts + kCluster - 1) / kCluster;
+  const bool alone = few(a.tokens, a.experts);
+  const int ctas = ctas_of(a.tokens, a.experts), per = (a.experts + kCluster - 1) / kCluster;
   const size_t smem = (size_t)(kRows + 1) * a.experts * sizeof(float);
   const purlin_status st = with_lanes(a.experts, [&](auto n) {
     constexpr int N = decltype(n)::value;

@@ -224,6 +224,14 @@ __device__ __forceinline__ float inverse(float variance, float eps) { return __f
 // its weights stay there.  A warp takes the mean of its part and the squares of the
 // distances from that; the warps' means and squares join to the row's, (sum of
 // squares) + n (mean of the part - mean)^2 each, behind one barrier.
+//
+// 16384 x 5120 bf16 with a residual: 99 us, 6.8 TB/s, the copy bandwidth.  A CTA for each
+// row, weights read anew and two barriers, took 150 us; rows by the ring and weights
+// kept 136; two values an instruction 107, and fewer instructions for addresses the
+// rest.  1024 threads with 8 elements each: 136 us.  Rows of odd width go element by element: 1.8
+// to 2.4 times the time that their bytes take (3001 x 1537 binary32: 10.6 us, 16000 x 4095 bf16: 94),
+// bound by the instructions of an element.  Vectors cut at the rows' ends instead made the
+// warps with the ends the slowest (115 us) and all others wait.
 template <typename T, typename W, Lie LIE, int NV>
 __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Ring ring) {
   op_wait();
@@ -362,7 +370,27 @@ __global__ void __launch_bounds__(kMostThreads) norm_wide_kernel(const __grid_co
 // xh)) / deviation (+ the gradient that reaches x beside the norm), and the
 // columns' sums of dy xh and dy.  A CTA holds whole rows, its threads the
 // columns' sums over the rows that pass through it; a second kernel adds the
-// CTAs' sums, in order.
+// CTAs' sums, in order, or, of few rows, the CTAs of one cluster do.
+//
+// 8192 x 4096 bf16 with the residual's gradient: 50 us, 46 of them before the join; 5.4 TB/s, 80%
+// of the copy bandwidth (39.5 us).  What is left is latency: 16 warps an SM at 120
+// registers, a barrier for each row, 53% of the issue slots.  Loads when a row needs
+// them: 112 us; by the ring 60; two values an instruction 54; sums across a warp by its
+// halves and one round of loads in the join 50.  Launching the join early cost 2 us (its CTAs
+// take the places of this kernel's last ones), CTAs of 1024 threads with 8 elements each
+// 39.
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of the shared memory of the cluster's CTA `rank`, where p is in this one's.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
 
 // Sums of two values over a row's threads; `tmp`: two words for each warp, of two
 // rows that are used in turn.  The halves of a warp take one value each.
@@ -386,7 +414,7 @@ __device__ __forceinline__ float2 group_sum(float2 x, int tpr, int group, float*
 
 template <typename T, typename W, Lie LIE, int NV>
 __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_constant__ NormArgs a,
-                                                                 const __grid_constant__ Ring ring) {
+                                                                 const __grid_constant__ Ring ring, int alone) {
   op_wait();
   extern __shared__ __align__(16) char smem[];  // the ring, then [groups][2][width] sums
   __shared__ float tmp[2][kMostThreads / 16];
@@ -472,16 +500,24 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
     of_b[in.column(i / N) + i % N] = i % 2 ? vb.y : vb.x;
   }
   __syncthreads();
-  const float* sums = (const float*)smem;
+  float* sums = (float*)smem;
   for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
     float v = 0.f;
     for (int g = 0; g < groups; ++g) v += sums[2 * g * D + c];
-    if (gridDim.x > 1) {
-      a.parts[(uint64_t)blockIdx.x * 2 * D + c] = v;
-    } else if (W* out = (W*)(c < D ? a.grad_weight : a.grad_bias)) {  // all there is
-      out[c < D ? c : c - D] = from_f32<W>(v);
-    }
+    if (alone) sums[c] = v;
+    else a.parts[(uint64_t)blockIdx.x * 2 * D + c] = v;
   }
+  if (!alone) return;
+  // the CTAs are one cluster, and take the columns in turn
+  cluster_sync();
+  for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < 2 * D; c += gridDim.x * blockDim.x) {
+    W* out = (W*)(c < D ? a.grad_weight : a.grad_bias);
+    if (!out) continue;
+    float v = 0.f;
+    for (uint32_t r = 0; r < gridDim.x; ++r) v += ld_cluster(sums + c, r);
+    out[c < D ? c : c - D] = from_f32<W>(v);
+  }
+  cluster_sync();  // before a CTA ends whose memory is read
 }
 
 // The same for rows of any width, in two kernels: rows, and sums of columns.
@@ -654,6 +690,11 @@ purlin_status norm_t(const NormArgs& a, cudaStream_t s) {
   return with_shape<T>(aligned, a.width, go, [&] { return op_launch(norm_wide_kernel<T, W>, a.tokens, kMostThreads, 0, s, a); });
 }
 
+// Few rows go through one cluster and one launch, kFewRows for each of its groups:
+// the second launch costs the host 2 to 3 us (calls of 30 / 60 / 120 x 4096 bf16: 13.1 / 13.4 / 17.3 us in
+// one, 15.8 / 15.5 / 15.8 in two; on the device 10.4 / 12.8 / 17.3 and 8.7 / 8.9 / 8.9).
+constexpr int kCluster = 8, kFewRows = 4;
+
 template <typename T, typename W>
 purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
   constexpr uint64_t es = sizeof(T);
@@ -667,11 +708,15 @@ purlin_status norm_grad_t(NormArgs a, cudaStream_t s) {
     constexpr Lie L = decltype(lie)::value;
     constexpr int NV = decltype(nv)::value;
     const Ring r = ring_of<T>(L, a.width, tpr, a.grad_total ? 3 : 2);
-    parts = (int)std::min<uint64_t>(kSms, (a.tokens + r.groups - 1) / r.groups);
-    done = done || parts == 1;
+    const uint64_t rounds = (a.tokens + r.groups - 1) / r.groups;  // of one CTA
+    const bool alone = rounds <= kCluster * kFewRows;
+    parts = (int)std::min<uint64_t>(alone ? kCluster : kSms, rounds);
+    if (alone)
+      while (parts & (parts - 1)) ++parts;  // a power of two
+    done = done || alone;
     const uint32_t of_sums = sums ? (uint32_t)(r.groups * 2 * a.width * sizeof(float)) : 0, smem = std::max(r.smem(), of_sums);
     if (purlin_status e = op_smem((const void*)norm_grad_kernel<T, W, L, NV>, smem, kSmem)) return e;
-    return op_launch(norm_grad_kernel<T, W, L, NV>, parts, tpr * r.groups, smem, s, a, r);
+    return op_launch_cluster(alone ? parts : 1, norm_grad_kernel<T, W, L, NV>, parts, tpr * r.groups, smem, s, a, r, (int)alone);
   };
   auto wide = [&] {
     parts = (int)std::min<uint64_t>(kSms, a.tokens);
