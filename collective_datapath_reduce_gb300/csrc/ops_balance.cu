@@ -479,8 +479,11 @@ int ctas_of(uint64_t tokens, int experts) {
 
 }  // namespace
 
+// The sums of the CTAs of two launches, asked for past 512 tokens whichever way a call
+// then goes.
 size_t balance_bytes(uint64_t tokens, int experts) {
-  return few(tokens, experts) ? 0 : (size_t)ctas_of(tokens, experts) * (2 * (size_t)experts + 1) * sizeof(uint32_t);
+  const uint64_t ctas = std::min<uint64_t>(kMostCtas, (tokens + kWarps - 1) / kWarps);
+  return tokens <= kCluster * kWarps * 4 ? 0 : (size_t)ctas * (2 * (size_t)experts + 1) * sizeof(uint32_t);
 }
 
 purlin_status launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
