@@ -75,17 +75,18 @@ struct Stream {
   uint64_t left;         // rows to fetch
   uint32_t bytes;        // of a row
   uint32_t matrix, stage, slots, in, out, first;  // of shared memory, in bytes
-  int tid, group, tpr, stages, width;
+  int tid, group, tpr, stages, width, n;  // n: matrices
 
   __device__ __forceinline__ Stream(const Ring& r, const void* smem, uint64_t columns) {
     tpr = r.tpr;
     stages = r.stages;
+    n = r.n;
     tid = threadIdx.x % tpr;
     group = threadIdx.x / tpr;
     width = (int)columns;
     bytes = (uint32_t)width * sizeof(T);
     matrix = (uint32_t)r.groups * r.granules * 16;
-    stage = matrix * r.n;
+    stage = matrix * n;
     slots = stage * stages;
     in = out = 0;
     first = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)group * r.granules * 16;
@@ -118,7 +119,7 @@ struct Stream {
       --left;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        if (!step[m]) break;
+        if (m >= n) break;
         const uint32_t to = first + in + m * matrix;
         if constexpr (SINGLE) {
           const uint32_t off = (uint32_t)((uintptr_t)from[m] & 15u), last = off + bytes;
@@ -246,7 +247,6 @@ __global__ void __launch_bounds__(kMostThreads) norm_kernel(const __grid_constan
   in.take(row, rows, a.tokens);
   const bool second = a.residual != nullptr;
   in.open(0, a.x, a.ldx, row, rows);
-  in.step[1] = 0;
   if (second) in.open(1, a.residual, a.ldr, row, rows);
   in.begin();
   F2 w[P], b[P];
@@ -431,7 +431,6 @@ __global__ void __launch_bounds__(kMostThreads) norm_grad_kernel(const __grid_co
   const bool third = a.grad_total != nullptr;
   in.open(0, a.x, a.ldx, row, rows);
   in.open(1, a.grad_y, a.ldg, row, rows);
-  in.step[2] = 0;
   if (third) in.open(2, a.grad_total, a.ldgt, row, rows);
   in.begin();
   const float per = __frcp_rn((float)D);

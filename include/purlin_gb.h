@@ -475,7 +475,8 @@ purlin_status purlin_layer_norm_grad(purlin_handle h, const void* grad_y, size_t
  * top_k, packed) as in purlin_route_experts; a token without a pick in [0,
  * experts) is padding and does not count, whatever its logits.  A token's
  * shares are the softmax of its logits, or its sigmoids over (their sum +
- * 1e-20); a row of nothing but -inf has shares of 0.  counts (experts values) =
+ * 1e-20); a row of nothing but -inf has shares of 0, one with NaN (softmax: or
+ * +inf) shares that are NaN.  counts (experts values) =
  * how many picks each expert has; sums (2 x experts + 1) = the same, then the sum
  * of each expert's shares over the tokens, then the number of tokens.  With C, S
  * and N those, *loss = scale x experts x (sum of C S) / (sum of C x N), 0 where

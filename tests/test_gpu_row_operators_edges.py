@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from oracle import operators as O
+from collective_datapath_reduce_gb300 import purlin as P
 from collective_datapath_reduce_gb300 import torch_api as purlin
 from test_gpu_operators import DEV, E24, Guarded, h  # noqa: F401 (h: a fixture)
 from test_gpu_row_operators import BF16, F32, everything, status
@@ -169,7 +170,8 @@ def test_rows_behind_the_last_stay_as_they_were(h):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("T,D", [(20003, 16), (20003, 9), (9729, 128), (2433, 65), (305, 1280), (153, 4096), (3, 5120), (5000, 24)])
+@pytest.mark.parametrize("T,D", [(20003, 16), (20003, 9), (9729, 128), (2433, 65), (305, 1280), (153, 4096), (3, 5120), (5000, 24),
+                                 (300, 8200), (5, 12288), (5, 12296)])
 def test_rows_that_share_a_warp_or_do_not_fill_the_last_round(h, T, D, dtype):  # noqa: F811
     """Against torch in 64 bits on the GPU: the lanes of a warp run out of rows at different times."""
     g = torch.Generator(device=DEV).manual_seed(D)
@@ -225,3 +227,21 @@ def test_balance_of_every_lie_of_the_logits(h, T, E, dtype):  # noqa: F811
     u = 2.0 ** -8 if dtype is BF16 else E24
     size = p * (c + (p * c).sum(1, keepdim=True))
     assert ((grad.view.double() - dx).abs() <= u * dx.abs() + (2 * rel + 40 * E24) * size).all() and grad.intact()
+
+
+def test_one_row_with_a_stride_past_64_bits_of_bytes(h):  # noqa: F811
+    """The distance to a row that is not there does not matter, whatever it wraps to."""
+    x, res, y, y2, stats = (torch.randn(1, 64, device=DEV) for _ in range(5))
+    stats = torch.empty(1, 2, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    purlin.layer_norm(x, None, None, y, h, residual=res)
+    huge = 1 << 61
+    assert P.purlin_layer_norm(h.raw, x, huge, res, huge, 1, 64, P.PL_F32, None, None, P.PL_F32, 1e-5, y2, huge, None, 0, stats,
+                               s) == P.PL_OK
+    assert torch.equal(y, y2)
+    dx, dx2, dw, dw2 = torch.empty_like(x), torch.empty_like(x), torch.empty(64, device=DEV), torch.empty(64, device=DEV)
+    purlin.layer_norm_grad(res, x, stats, None, dx, dw, None, h, grad_total=y)
+    ws = torch.empty(P.purlin_layer_norm_grad_bytes(1, 64), dtype=torch.uint8, device=DEV)
+    assert P.purlin_layer_norm_grad(h.raw, res, huge, x, huge, stats, 1, 64, P.PL_F32, None, P.PL_F32, y, huge, dx2, huge, dw2, None,
+                                    ws, ws.numel(), s) == P.PL_OK
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
