@@ -14,6 +14,7 @@ from __future__ import annotations
 import enum
 import operator
 import threading
+import types
 
 import torch
 
@@ -30,6 +31,7 @@ class Scores(enum.IntEnum):
 
 
 _DTYPES = {torch.float32: P.PL_F32, torch.bfloat16: P.PL_BF16}
+_Function = types.FunctionType
 
 
 class Handle:
@@ -296,17 +298,20 @@ def _call(fn, what, handle, stream, *args):
 
 def _call_in_workspace(fn, what, handle, stream, nbytes, *args):
     """_call with a workspace and its size behind args.  A call is several
-    launches on one block, so no other thread's may come between them."""
+    launches on one block, so no other thread's may come between them.  The
+    library's own functions take an address, the binding's a tensor too."""
     if nbytes == 0:
         return _call(fn, what, handle, stream, *args, None, 0)
     index = handle.device.index
     if index is None or torch.cuda.current_device() != index:
         with _on(handle), handle.lock:
             ws = _workspace(nbytes, stream, handle)
+            ws = ws if type(fn) is _Function else ws.data_ptr()
             return _check(fn(handle.raw, *args, ws, nbytes, _stream(stream, handle.device)), what)
     key = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, handle.device)
     with handle.lock:
         ws = _block(nbytes, key, handle) if stream is None else _workspace(nbytes, key, handle)
+        ws = ws if type(fn) is _Function else ws.data_ptr()
         _check(fn(handle.raw, *args, ws, nbytes, key), what)
 
 
@@ -450,10 +455,25 @@ def embed_grad(grad_out, tokens, grad_table, handle: Handle, first=0, scale=1.0,
                        base, ldb, grad_table, ldt, dt, R, int(first))
 
 
-def _vector(t, n, dtype, what, name):
-    """Checks a vector of n columns that may be None."""
-    if t is not None:
-        _packed(t, (n,), dtype, what, name)
+# The row operators' calls are short, and the host's: checks ask a contiguous
+# tensor of the right shape and type four questions, and the library is called
+# with addresses.
+
+def _rows_of(t, shape, dtype, what, name):
+    """Checks a matrix of the given shape and returns its row stride."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        return shape[1]
+    return _matrix(t, shape[0], shape[1], dtype, what, name)
+
+
+def _vector_of(t, shape, dtype, what, name):
+    """Checks a packed tensor and returns its address."""
+    if not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda):
+        _packed(t, shape, dtype, what, name)
+    return t.data_ptr()
+
+
+_F32 = torch.float32
 
 
 def layer_norm(x, weight, bias, y, handle: Handle, residual=None, total=None, stats=None, eps=1e-5, stream=None):
@@ -464,20 +484,20 @@ def layer_norm(x, weight, bias, y, handle: Handle, residual=None, total=None, st
     mean and 1 / deviation, for the gradient.  y and total may each be x or
     residual itself."""
     what = "layer_norm"
-    T, D = _two(x, what, "x")
+    shape, dtype = x.shape, x.dtype
+    T, D = shape if len(shape) == 2 else _two(x, what, "x")
     dt = _values(x, what)
-    ldx = _matrix(x, T, D, x.dtype, what, "x")
-    ldy = _matrix(y, T, D, x.dtype, what, "y")
-    ldr = _matrix(residual, T, D, x.dtype, what, "residual") if residual is not None else 0
-    ldt = _matrix(total, T, D, x.dtype, what, "total") if total is not None else 0
+    ldx = _rows_of(x, shape, dtype, what, "x")
+    ldy = _rows_of(y, shape, dtype, what, "y")
+    r, ldr = (None, 0) if residual is None else (residual.data_ptr(), _rows_of(residual, shape, dtype, what, "residual"))
+    t, ldt = (None, 0) if total is None else (total.data_ptr(), _rows_of(total, shape, dtype, what, "total"))
     of = weight if weight is not None else bias
-    dw = P.PL_F32 if of is None else _values(of, what)
-    _vector(weight, D, of.dtype if of is not None else None, what, "weight")
-    _vector(bias, D, of.dtype if of is not None else None, what, "bias")
-    if stats is not None:
-        _packed(stats, (T, 2), torch.float32, what, "stats")
-    _call(P.purlin_layer_norm, what, handle, stream, x, ldx, residual, ldr, T, D, dt, weight, bias, dw, eps, y, ldy, total,
-          ldt, stats)
+    dw, wtype = (P.PL_F32, None) if of is None else (_values(of, what), of.dtype)
+    w = None if weight is None else _vector_of(weight, (D,), wtype, what, "weight")
+    b = None if bias is None else _vector_of(bias, (D,), wtype, what, "bias")
+    s = None if stats is None else _vector_of(stats, (T, 2), _F32, what, "stats")
+    _call(P.load().purlin_layer_norm, what, handle, stream, x.data_ptr(), ldx, r, ldr, T, D, dt, w, b, dw, eps, y.data_ptr(),
+          ldy, t, ldt, s)
 
 
 def layer_norm_grad(grad_y, x, stats, weight, grad_x, grad_weight, grad_bias, handle: Handle, grad_total=None,
@@ -487,21 +507,24 @@ def layer_norm_grad(grad_y, x, stats, weight, grad_x, grad_weight, grad_bias, ha
     and grad_bias = those of weight and bias, in one dtype, each may be None.
     weight: None for 1.  grad_x may be grad_y, x or grad_total itself."""
     what = "layer_norm_grad"
-    T, D = _two(grad_y, what, "grad_y")
+    shape, dtype = grad_y.shape, grad_y.dtype
+    T, D = shape if len(shape) == 2 else _two(grad_y, what, "grad_y")
     dt = _values(grad_y, what)
-    ldg = _matrix(grad_y, T, D, grad_y.dtype, what, "grad_y")
-    ldx = _matrix(x, T, D, grad_y.dtype, what, "x")
-    _packed(stats, (T, 2), torch.float32, what, "stats")
-    ldt = _matrix(grad_total, T, D, grad_y.dtype, what, "grad_total") if grad_total is not None else 0
-    ldo = _matrix(grad_x, T, D, grad_y.dtype, what, "grad_x")
+    ldg = _rows_of(grad_y, shape, dtype, what, "grad_y")
+    ldx = _rows_of(x, shape, dtype, what, "x")
+    s = _vector_of(stats, (T, 2), _F32, what, "stats")
+    t, ldt = (None, 0) if grad_total is None else (grad_total.data_ptr(),
+                                                   _rows_of(grad_total, shape, dtype, what, "grad_total"))
+    ldo = _rows_of(grad_x, shape, dtype, what, "grad_x")
     of = weight if weight is not None else grad_weight if grad_weight is not None else grad_bias
-    dw, dtype = (P.PL_F32, None) if of is None else (_values(of, what), of.dtype)
-    _vector(weight, D, dtype, what, "weight")
-    _vector(grad_weight, D, dtype, what, "grad_weight")
-    _vector(grad_bias, D, dtype, what, "grad_bias")
-    nbytes = P.purlin_layer_norm_grad_bytes(T, D) if grad_weight is not None or grad_bias is not None else 0
-    _call_in_workspace(P.purlin_layer_norm_grad, what, handle, stream, nbytes, grad_y, ldg, x, ldx, stats, T, D, dt, weight,
-                       dw, grad_total, ldt, grad_x, ldo, grad_weight, grad_bias)
+    dw, wtype = (P.PL_F32, None) if of is None else (_values(of, what), of.dtype)
+    w = None if weight is None else _vector_of(weight, (D,), wtype, what, "weight")
+    gw = None if grad_weight is None else _vector_of(grad_weight, (D,), wtype, what, "grad_weight")
+    gb = None if grad_bias is None else _vector_of(grad_bias, (D,), wtype, what, "grad_bias")
+    lib = P.load()
+    nbytes = 0 if gw is None and gb is None else lib.purlin_layer_norm_grad_bytes(T, D)
+    _call_in_workspace(lib.purlin_layer_norm_grad, what, handle, stream, nbytes, grad_y.data_ptr(), ldg, x.data_ptr(), ldx, s,
+                       T, D, dt, w, dw, t, ldt, grad_x.data_ptr(), ldo, gw, gb)
 
 
 def balance_loss(logits, ids, counts, sums, loss, handle: Handle, scores=Scores.SOFTMAX, scale=1.0, stream=None):
@@ -515,16 +538,15 @@ def balance_loss(logits, ids, counts, sums, loss, handle: Handle, scores=Scores.
     what = "balance_loss"
     T, E = _two(logits, what, "logits")
     k = _two(ids, what, "ids")[1]
-    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    ld = _rows_of(logits, (T, E), logits.dtype, what, "logits")
     dt = _values(logits, what)
-    _packed(ids, (T, k), torch.int32, what, "ids")
-    _packed(counts, (E,), torch.int32, what, "counts")
-    _packed(sums, (2 * E + 1,), torch.float32, what, "sums")
-    if loss is not None:
-        _packed(loss, (1,), torch.float32, what, "loss")
-    nbytes = P.purlin_balance_loss_bytes(T, E)
-    _call_in_workspace(P.purlin_balance_loss, what, handle, stream, nbytes, logits, ld, dt, ids, T, k, E, int(scores), scale,
-                       counts, sums, loss)
+    i = _vector_of(ids, (T, k), torch.int32, what, "ids")
+    c = _vector_of(counts, (E,), torch.int32, what, "counts")
+    s = _vector_of(sums, (2 * E + 1,), _F32, what, "sums")
+    of = None if loss is None else _vector_of(loss, (1,), _F32, what, "loss")
+    lib = P.load()
+    _call_in_workspace(lib.purlin_balance_loss, what, handle, stream, lib.purlin_balance_loss_bytes(T, E), logits.data_ptr(),
+                       ld, dt, i, T, k, E, int(scores), scale, c, s, of)
 
 
 def balance_join(sums, loss, handle: Handle, scale=1.0, stream=None):
@@ -532,9 +554,9 @@ def balance_join(sums, loss, handle: Handle, scale=1.0, stream=None):
     what = "balance_join"
     if sums.dim() != 1 or sums.shape[0] < 3 or sums.shape[0] % 2 == 0:
         raise ValueError(f"{what}: sums must hold 2 x experts + 1 values, got {tuple(sums.shape)}")
-    _packed(sums, sums.shape, torch.float32, what, "sums")
-    _packed(loss, (1,), torch.float32, what, "loss")
-    _call(P.purlin_balance_join, what, handle, stream, sums, sums.shape[0] // 2, scale, loss)
+    s = _vector_of(sums, sums.shape, _F32, what, "sums")
+    of = _vector_of(loss, (1,), _F32, what, "loss")
+    _call(P.load().purlin_balance_join, what, handle, stream, s, sums.shape[0] // 2, scale, of)
 
 
 def balance_loss_grad(logits, ids, sums, grad_loss, grad_logits, handle: Handle, scores=Scores.SOFTMAX, scale=1.0,
@@ -544,33 +566,36 @@ def balance_loss_grad(logits, ids, sums, grad_loss, grad_logits, handle: Handle,
     grad_logits, or None for 0; base is grad_logits adds in place (to
     route_experts_grad's, say)."""
     what = "balance_loss_grad"
-    T, E = _two(logits, what, "logits")
+    T, E = shape = _two(logits, what, "logits")
     k = _two(ids, what, "ids")[1]
-    ld = _matrix(logits, T, E, logits.dtype, what, "logits")
+    dtype = logits.dtype
+    ld = _rows_of(logits, shape, dtype, what, "logits")
     dt = _values(logits, what)
-    _packed(ids, (T, k), torch.int32, what, "ids")
-    _packed(sums, (2 * E + 1,), torch.float32, what, "sums")
-    if grad_loss is not None:
-        _packed(grad_loss, (1,), torch.float32, what, "grad_loss")
-    ldb = _matrix(base, T, E, logits.dtype, what, "base") if base is not None else 0
-    ldg = _matrix(grad_logits, T, E, logits.dtype, what, "grad_logits")
-    _call(P.purlin_balance_loss_grad, what, handle, stream, logits, ld, dt, ids, T, k, E, int(scores), scale, sums,
-          grad_loss, base, ldb, grad_logits, ldg)
+    i = _vector_of(ids, (T, k), torch.int32, what, "ids")
+    s = _vector_of(sums, (2 * E + 1,), _F32, what, "sums")
+    g = None if grad_loss is None else _vector_of(grad_loss, (1,), _F32, what, "grad_loss")
+    b, ldb = (None, 0) if base is None else (base.data_ptr(), _rows_of(base, shape, dtype, what, "base"))
+    ldg = _rows_of(grad_logits, shape, dtype, what, "grad_logits")
+    _call(P.load().purlin_balance_loss_grad, what, handle, stream, logits.data_ptr(), ld, dt, i, T, k, E, int(scores), scale, s,
+          g, b, ldb, grad_logits.data_ptr(), ldg)
 
 
 def _teacher(logits, ids, teacher, what, first, vocabulary, temperature, scale):
-    """Checks what the distillation's calls share: (tokens, width, stride, dtype, the C struct)."""
+    """Checks what the distillation's calls share: (tokens, width, stride, dtype, a
+    reference to the C struct, addresses of ids and teacher)."""
     T, R = _two(logits, what, "logits")
     k = _two(ids, what, "ids")[1]
-    ld = _matrix(logits, T, R, logits.dtype, what, "logits")
+    ld = _rows_of(logits, (T, R), logits.dtype, what, "logits")
     dt = _values(logits, what)
-    if ids.dtype not in (torch.int32, torch.int64):
+    wide = ids.dtype is torch.int64
+    if not wide and ids.dtype is not torch.int32:
         raise ValueError(f"{what}: ids must be int32 or int64")
-    _packed(ids, (T, k), ids.dtype, what, "ids")
+    i = _vector_of(ids, (T, k), ids.dtype, what, "ids")
     dq = _values(teacher, what)
-    _packed(teacher, (T, k), teacher.dtype, what, "teacher")
-    return T, R, ld, dt, P.make_distillation(R, first, first + R if vocabulary is None else vocabulary, k,
-                                             8 if ids.dtype is torch.int64 else 4, dq, temperature, scale)
+    t = _vector_of(teacher, (T, k), teacher.dtype, what, "teacher")
+    d = P.make_distillation(R, first, first + R if vocabulary is None else vocabulary, k, 8 if wide else 4, dq, temperature,
+                            scale)
+    return T, R, ld, dt, P.ctypes.byref(d), i, t
 
 
 def distil_loss(logits, ids, teacher, loss, stats, handle: Handle, temperature=1.0, scale=1.0, stream=None):
@@ -581,10 +606,10 @@ def distil_loss(logits, ids, teacher, loss, stats, handle: Handle, temperature=1
     (float32 or bfloat16): tokens x picks; loss: float32, one for each token;
     stats: float32, tokens x 2, for the gradient."""
     what = "distil_loss"
-    T, _, ld, dt, d = _teacher(logits, ids, teacher, what, 0, None, temperature, scale)
-    _packed(loss, (T,), torch.float32, what, "loss")
-    _packed(stats, (T, 2), torch.float32, what, "stats")
-    _call(P.purlin_distil_loss, what, handle, stream, logits, ld, dt, T, d, ids, teacher, loss, stats)
+    T, _, ld, dt, d, i, t = _teacher(logits, ids, teacher, what, 0, None, temperature, scale)
+    of = _vector_of(loss, (T,), _F32, what, "loss")
+    s = _vector_of(stats, (T, 2), _F32, what, "stats")
+    _call(P.load().purlin_distil_loss, what, handle, stream, logits.data_ptr(), ld, dt, T, d, i, t, of, s)
 
 
 def distil_parts(logits, ids, teacher, parts, handle: Handle, first=0, vocabulary=None, temperature=1.0, stream=None):
@@ -592,9 +617,9 @@ def distil_parts(logits, ids, teacher, parts, handle: Handle, first=0, vocabular
     vocabulary.  logits: tokens x words, those of the words first .. first +
     words; vocabulary: the words of all ranges (None: this is the last)."""
     what = "distil_parts"
-    T, _, ld, dt, d = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, 1.0)
-    _packed(parts, (T, 4), torch.float32, what, "parts")
-    _call(P.purlin_distil_parts, what, handle, stream, logits, ld, dt, T, d, ids, teacher, parts)
+    T, _, ld, dt, d, i, t = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, 1.0)
+    p = _vector_of(parts, (T, 4), _F32, what, "parts")
+    _call(P.load().purlin_distil_parts, what, handle, stream, logits.data_ptr(), ld, dt, T, d, i, t, p)
 
 
 def distil_join(parts, loss, stats, handle: Handle, temperature=1.0, scale=1.0, stream=None):
@@ -605,10 +630,10 @@ def distil_join(parts, loss, stats, handle: Handle, temperature=1.0, scale=1.0, 
     ranges = parts.numel() // (4 * T) if T else 1
     if parts.shape[-1:] != (4,) or ranges == 0 or parts.numel() != 4 * T * ranges:
         raise ValueError(f"{what}: parts must be ranges x {T} x 4, got {tuple(parts.shape)}")
-    _packed(parts, parts.shape, torch.float32, what, "parts")
-    _packed(loss, (T,), torch.float32, what, "loss")
-    _packed(stats, (T, 2), torch.float32, what, "stats")
-    _call(P.purlin_distil_join, what, handle, stream, parts, ranges, T, temperature, scale, loss, stats)
+    p = _vector_of(parts, parts.shape, _F32, what, "parts")
+    of = _vector_of(loss, (T,), _F32, what, "loss")
+    s = _vector_of(stats, (T, 2), _F32, what, "stats")
+    _call(P.load().purlin_distil_join, what, handle, stream, p, ranges, T, temperature, scale, of, s)
 
 
 def distil_loss_grad(logits, ids, teacher, stats, grad_loss, grad_logits, handle: Handle, first=0, vocabulary=None,
@@ -616,12 +641,12 @@ def distil_loss_grad(logits, ids, teacher, stats, grad_loss, grad_logits, handle
     """grad_logits (like logits, or logits itself) = grad_loss[t] x the gradient of
     loss[t], for a range's logits too, given the whole vocabulary's stats."""
     what = "distil_loss_grad"
-    T, R, ld, dt, d = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, scale)
-    _packed(stats, (T, 2), torch.float32, what, "stats")
-    _packed(grad_loss, (T,), torch.float32, what, "grad_loss")
-    ldg = _matrix(grad_logits, T, R, logits.dtype, what, "grad_logits")
-    _call(P.purlin_distil_loss_grad, what, handle, stream, logits, ld, dt, T, d, ids, teacher, stats, grad_loss, grad_logits,
-          ldg)
+    T, R, ld, dt, d, i, t = _teacher(logits, ids, teacher, what, first, vocabulary, temperature, scale)
+    s = _vector_of(stats, (T, 2), _F32, what, "stats")
+    g = _vector_of(grad_loss, (T,), _F32, what, "grad_loss")
+    ldg = _rows_of(grad_logits, (T, R), logits.dtype, what, "grad_logits")
+    _call(P.load().purlin_distil_loss_grad, what, handle, stream, logits.data_ptr(), ld, dt, T, d, i, t, s, g,
+          grad_logits.data_ptr(), ldg)
 
 
 _numel, _data_ptr, _is_contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
