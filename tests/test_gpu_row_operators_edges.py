@@ -171,7 +171,7 @@ def test_rows_behind_the_last_stay_as_they_were(h):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,D", [(20003, 16), (20003, 9), (9729, 128), (2433, 65), (305, 1280), (153, 4096), (3, 5120), (5000, 24),
-                                 (300, 8200), (5, 12288), (5, 12296)])
+                                 (300, 8200), (5, 12288), (5, 12296), (8, 8192), (20, 8192), (33, 8192)])
 def test_rows_that_share_a_warp_or_do_not_fill_the_last_round(h, T, D, dtype):  # noqa: F811
     """Against torch in 64 bits on the GPU: the lanes of a warp run out of rows at different times."""
     g = torch.Generator(device=DEV).manual_seed(D)
