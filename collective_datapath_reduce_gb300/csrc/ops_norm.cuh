@@ -33,9 +33,15 @@ template <int N>
 __device__ __forceinline__ void copies_left() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+// 16 bytes of shared memory, or zeros where `on` is false.
+__device__ __forceinline__ uint4 ld_shared16_if(uint32_t at, bool on) {
   uint4 u;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "mov.u32 %3, 0;\n\t@q ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+      : "r"(at), "r"((uint32_t)on)
+      : "memory");
   return u;
 }
 template <typename T>
@@ -68,7 +74,9 @@ struct Ring {
 };
 
 // A thread's view of a row: NV vectors of N elements, tpr vectors apart, as P
-// pairs.  For a vector beside the row it reads the row's first and counts it 0 times.
+// pairs.  A vector beside the row is zeros (kSingle: the row's first element), and
+// counts 0 times.  No thread reads what another's copy brings, but for kSingle, whose
+// threads wait for each other first.
 template <typename T, Lie LIE, int NV, int M>
 struct Stream {
   static constexpr bool SINGLE = LIE == Lie::kSingle;
@@ -161,7 +169,7 @@ struct Stream {
     at += m * matrix;
     if constexpr (!SINGLE) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) pairs_of<T>(ld_shared16(at + (there(j) ? offset(j) : 0)), v + j * (N / 2));
+      for (int j = 0; j < NV; ++j) pairs_of<T>(ld_shared16_if(at + offset(j), there(j)), v + j * (N / 2));
     } else {
       at += (uint32_t)((uintptr_t)row & 15u);
 #pragma unroll

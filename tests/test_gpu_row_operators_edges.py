@@ -1,5 +1,6 @@
 """Layer norm, balance and distillation at odd addresses of every buffer, in host memory, past 32-bit offsets, by threads."""
 
+import math
 import threading
 
 import numpy as np
@@ -245,3 +246,25 @@ def test_one_row_with_a_stride_past_64_bits_of_bytes(h):  # noqa: F811
     assert P.purlin_layer_norm_grad(h.raw, res, huge, x, huge, stats, 1, 64, P.PL_F32, None, P.PL_F32, y, huge, dx2, huge, dw2, None,
                                     ws, ws.numel(), s) == P.PL_OK
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("D", [520, 1544, 5120, 8192])
+def test_rows_of_nan_leave_nothing_for_the_rows_behind_them(h, D):  # noqa: F811
+    """Every row is its own: whatever a call before, or the row before, left on the chip."""
+    g = torch.Generator(device=DEV).manual_seed(D)
+    for dtype in (F32, BF16):
+        x = torch.randn(4096, D, generator=g, device=DEV).to(dtype)
+        bad = torch.full_like(x, math.nan)
+        mixed = x.clone()
+        mixed[::2] = math.nan
+        y, dx, junk, stats, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(4096, 2, device=DEV), torch.empty(D, device=DEV)
+        for _ in range(20):
+            purlin.layer_norm(bad, None, None, junk, h, residual=bad)
+            purlin.layer_norm(x, None, None, y, h, stats=stats)
+            purlin.layer_norm_grad(bad, bad, stats, None, junk, None, None, h, grad_total=bad)
+            purlin.layer_norm_grad(x, x, stats, None, dx, dw, None, h)
+            assert torch.isfinite(y).all() and torch.isfinite(stats).all() and torch.isfinite(dx).all() and torch.isfinite(dw).all()
+            purlin.layer_norm(mixed, None, None, junk, h)
+            assert torch.equal(junk[1::2], y[1::2]) and torch.isnan(junk[::2]).all()
+            purlin.layer_norm_grad(mixed, mixed, stats, None, junk, None, None, h)
+            assert torch.equal(junk[1::2], dx[1::2])
