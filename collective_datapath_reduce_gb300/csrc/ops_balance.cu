@@ -117,6 +117,13 @@ __device__ __forceinline__ F2 inverse(F2 x) {
   return f2(s.x, s.y);
 }
 
+// The lesser of two values, NaN if one of them is.
+__device__ __forceinline__ float lesser(float x, float y) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+
 // A token's logits become its scores as shares of one, x; `slope` is what a
 // score's derivative has beside them, 1 - sigmoid = exp(-logit) x sigmoid.  A row
 // of nothing but -inf has shares of 0.  No decision hangs on them, so neither
@@ -131,9 +138,9 @@ __device__ __forceinline__ void shares(const Lane<T, N>& row, int sigmoid, F2 (&
   if (sigmoid) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      // exp(-x) at most 2^127: a sigmoid below 2^-126 is 0, and the slope a number
+      // exp(-x) at most 2^127: a sigmoid below 2^-126 is 0, and the slope a number, of NaN neither
       const float2 a = split(x[i] * f2(-kLog2e));
-      const F2 e = ex2(f2(fminf(a.x, 127.f), fminf(a.y, 127.f)));
+      const F2 e = ex2(f2(lesser(a.x, 127.f), lesser(a.y, 127.f)));
       x[i] = inverse(f2(1.f) + e);
       slope[i] = e * x[i];
       sum = sum + x[i];
