@@ -307,7 +307,9 @@ Ring ring_of(Lie lie, uint64_t width, int tpr, int n) {
   const uint32_t row = r.smem();
   for (r.stages = 2; r.stages < 5 && (uint32_t)(r.stages - 1) * row < 64 * 1024; ++r.stages) {
   }
-  while (r.groups > 1 && r.smem() > kSmem) --r.groups;
+  // whole warps, whose lanes vote and shuffle together (binary32 rows of 136 to 160 values, three matrices)
+  const int step = std::max(1, 32 / tpr);
+  while (r.groups > step && r.smem() > kSmem) r.groups -= step;
   return r;
 }
 
