@@ -119,13 +119,17 @@ class DistilStep(expert_step.ExpertStep):
         return grad_x, of_weight[0], of_bias[0]
 
     def backward(self, f):
-        """Gradients in the order of parameters(), given forward's second result."""
+        """Gradients in the order of parameters(), given forward's second result, once: the logits,
+        the largest of what it holds, become their gradients in place."""
         s, h = self.shape, self.handle
+        logits = f.pop("logits_of", None)
+        if logits is None:
+            raise RuntimeError("backward: this forward's logits are gradients by now; run forward again")
         count = s.world * s.tokens
         grad_loss = self._new(count, dtype=torch.float32).fill_(1 / count)
         grad_rows, grad_tables = [], []
         for r, table in enumerate(self.tables):
-            dz = f["logits_of"][r]
+            dz = logits[r]
             purlin.distil_loss_grad(dz, f["words"][r], f["teacher"][r], f["stats"][r], grad_loss, dz, h,
                                     first=r * table.shape[0], vocabulary=s.vocabulary, temperature=s.temperature,
                                     scale=s.temperature ** 2)
