@@ -448,8 +448,9 @@ purlin_status purlin_clip_grad_norm(purlin_handle h, const void* const* grads, v
  * and 0.  stats (tokens x 2, packed), unless NULL, receives each row's mean and
  * 1 / sqrt(variance + eps), which the gradient reads.  y and total may each be x
  * or residual itself (same stride).  The variance is the mean of the squares of
- * the distances from the mean, in binary32: squares that overflow it make the
- * row's y 0 or NaN. */
+ * the distances from the mean, in binary32: where the squares overflow, 1 /
+ * deviation is 0 and the row's y the bias (0 without one); where the row's sum
+ * does, or a distance itself, y is NaN. */
 purlin_status purlin_layer_norm(purlin_handle h, const void* x, size_t x_stride, const void* residual,
                                 size_t residual_stride, size_t tokens, size_t width, purlin_dtype dtype,
                                 const void* weight, const void* bias, purlin_dtype weight_dtype, float eps, void* y,
