@@ -233,13 +233,15 @@ __device__ __forceinline__ float lanes_sum(float x, int tpr) {
 inline bool even(const void* p, uint64_t ld, uint64_t size) { return !p || (((uintptr_t)p | ld * size) & 15u) == 0; }
 
 constexpr uint32_t kSmem = 200 * 1024;
-constexpr uint64_t kMostRow = 32 * 1024;  // bytes: of three matrices two fit
 
 // How the threads of a CTA share rows: NV vectors in each, in groups of tpr threads.
 // The group whose row costs the fewest instructions, by 14 instructions an element
-// and 40 around them in each warp, 30 more where warps wait for each other (without
-// these, 5120 bf16 values go to 20 warps, not 7: 134 us for 16384 rows, not 102; 20011 rows of 520
-// binary32 to 5 warps, not one: 38 us for the gradient, not 24).
+// and 40 around them in each warp, 30 more where warps wait for each other.  Without the 40
+// and 30, 5120 bf16 values go to 10 warps, not 7 (16384 rows with a residual: 125 us, not 100),
+// and 520 binary32 values to 5 warps, not one (20011 rows: 39 us, not 12; the gradient 44, not
+// 23).  What 512 / tpr threads leave idle does not count, and should: 7168 and 8192 bf16 values
+// go to 10 and 11 warps, alone on their SM (8192 rows with a residual: 85 and 89 us, the gradient
+// 135 and 142), where 14 and 16 warps with two vectors a thread take 78 and 83, 87 and 94.
 struct Shape {
   int cost = 0, nv = 0, tpr = 0;
   bool whole = false;
@@ -272,13 +274,15 @@ purlin_status with_shape(bool aligned, uint64_t width, F f, G wide) {
   constexpr integral_constant<int, 5> five{};
   constexpr int V = V16<T>;
   Shape s;
-  if (aligned && width * sizeof(T) <= kMostRow) {
+  if (aligned) {
     if constexpr (V == 8) {
       for (int nv : {1, 2, 3}) s.consider(V, nv, width);
       if (s.nv == 3) return f(part, three, s.tpr);
     } else {
       for (int nv : {1, 2, 4}) s.consider(V, nv, width);
-      if (width <= 32 * 5 * V) s.consider(V, 5, width);  // registers: only where it saves the barrier
+      // five, for their registers, only where a warp at most then has the row (160 / 320 / 640 values, 64 MB of
+      // them: 17.9 / 18.4 / 19.0 us, without 23.6 / 24.0 / 34.8; the gradient 32.4 / 32.3 / 32.8, without 36.9 / 36.6 / 41.4)
+      if (width <= 32 * 5 * V) s.consider(V, 5, width);
       if (s.nv == 5) return f(part, five, s.tpr);
       if (s.nv == 4) return s.whole ? f(whole, four, s.tpr) : f(part, four, s.tpr);
     }
