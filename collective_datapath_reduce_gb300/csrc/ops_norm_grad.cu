@@ -13,6 +13,8 @@
 // halves and one round of loads in the join 50.  Launching the join early cost 2 us (its CTAs
 // take the places of this kernel's last ones), and so did launching it at this one's
 // end; CTAs of 768 threads at 80 registers took 64 us, of 1024 with 8 elements each 89.
+// With 24 bf16 values a thread (kPart, 3) the registers are at their limit and some are
+// spilled: 8192 x 5120 in 74 us, half the copy bandwidth (37.1 us).
 #include "ops_norm.cuh"
 
 namespace pl {

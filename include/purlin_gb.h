@@ -326,6 +326,9 @@ purlin_status purlin_atom_reduce(purlin_handle h, const void* const* src, int ns
  *     these calls need no order among each other.
  *   - Indices are read on the device and checked there: each operator says
  *     what one outside its range does.  None is followed out of a buffer.
+ *   - Exponentials of the balance's scores and the distillation's logits are
+ *     approximate: e^-d within (3 d + 4) 2^-24 of itself, 0 below the smallest
+ *     normal number.  Those that order experts, in routing, are not.
  *   - What an operator finds wrong on the device has a status word of its own,
  *     which purlin_status_get reads too: it stops no collective. */
 #define PURLIN_MAX_EXPERTS 1024
