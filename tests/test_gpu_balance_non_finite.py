@@ -8,7 +8,7 @@ import torch
 
 from oracle import operators as O
 from collective_datapath_reduce_gb300 import torch_api as purlin
-from test_gpu_operators import DEV, DTYPES, E24, U, Guarded, close, h, ints, make, spread  # noqa: F401 (h: a fixture)
+from test_gpu_operators import DTYPES, E24, U, Guarded, close, h, ints, make, spread  # noqa: F401 (h: a fixture)
 from test_gpu_row_operators import F32, share_error
 
 pytestmark = pytest.mark.gpu
